@@ -171,6 +171,81 @@ int ma_adamw_step(int64_t n, int64_t t, float beta1, float beta2, float eps, flo
 int ma_adamw8_step(int64_t n, int64_t t, float beta1, float beta2, float eps, float lr, float wd, float *theta,
                    const uint16_t *grads, int8_t *cm, uint8_t *cv, float *sm, float *sr, hipStream_t stream);
 
+/*
+ * The Muon optimizer's operators, stateless, on caller-owned device arrays: for
+ * the matrices of a model, beside MicroAdam for the rest of it.  All take a
+ * batch of `batch` equally shaped rows x cols matrices; element (b, i, j) of an
+ * array with strides (row, bat) is at b*bat + i*row + j, strides in elements.
+ * The momentum arrays are contiguous.
+ *
+ * Orthogonalizing U (n = the shorter side, X its orientation of n rows):
+ *   X <- U / max(|U|_F, eps);  `steps` times, with its own (a, b, c) each:
+ *   A = X X^T,  X <- (a I + b A + c A A) X
+ * coefficients: host array of 3*steps floats.  With (3.4445, -4.7750, 2.0315)
+ * five times, singular values from about 0.01 to 1 end between 0.68 and 1.2.
+ * X, A and a I + b A + c A A are rounded to 11 bits (fp16 with a fixed power of
+ * two) after every product, products are summed in fp32: the result is within
+ * about 2e-3 of the formula's (2-norm over 2-norm) for matrices whose singular
+ * values lie within two orders of magnitude; directions that are smaller by
+ * 2^-11 and more are lost in the rounding of their larger neighbours.
+ * Coefficients for which a singular value could pass 1.95, an eigenvalue of the
+ * polynomial 15, or all values shrink below 1e-3 are rejected (MA_EINVAL).
+ * A zero matrix gives zeros, one with a NaN or an infinity gives NaN throughout.
+ *
+ * workspace: device memory of at least ma_orthogonalize_workspace(batch, rows,
+ * cols) bytes (0 for an empty batch or sizes that the calls refuse), 256-byte
+ * aligned, on the stream's device, the call's own until its work on `stream` is
+ * done; what it holds before and after does not matter.  Nothing is allocated,
+ * every launch goes to `stream`, and a call can be captured into a HIP graph.
+ * A matrix has at most 2^33 elements (MA_EUNSUPPORTED).  steps: 1..64.
+ * batch = 0, rows = 0 or cols = 0: MA_OK, nothing done.  MA_EINVAL: null or
+ * misaligned pointers (each array to its elements), negative sizes, a small
+ * workspace, strides of a written array that overlap.
+ */
+#define MA_TYPE_F32 0
+#define MA_TYPE_BF16 1
+
+size_t ma_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols);
+
+/* out (bf16) = x (f32 or bf16) orthogonalized.  out may be x itself (same
+ * strides); otherwise they must not overlap. */
+int ma_orthogonalize(int64_t batch, int64_t rows, int64_t cols, const void *x, int x_type, int64_t x_row,
+                     int64_t x_batch, uint16_t *out, int64_t out_row, int64_t out_batch, int steps,
+                     const float *coefficients, float eps, void *workspace, size_t workspace_bytes,
+                     hipStream_t stream);
+
+/*
+ * One Muon step:  momentum <- beta*momentum + (1-beta)*g (fp32, [batch][rows][cols],
+ * zero before the first step);  U = beta*momentum + (1-beta)*g if nesterov, else
+ * the momentum;  params <- params*(1 - lr*wd) - lr*scale*orthogonalized(U).
+ * params f32 or bf16 (widened, updated in fp32, rounded to nearest even once),
+ * grads bf16 (raw bits).  0 <= beta < 1, wd >= 0; lr, wd, scale finite.
+ */
+int ma_muon_step(int64_t batch, int64_t rows, int64_t cols, void *params, int p_type, int64_t p_row,
+                 int64_t p_batch, const uint16_t *grads, int64_t g_row, int64_t g_batch, float *momentum, double lr,
+                 double beta, double wd, double scale, int nesterov, int steps, const float *coefficients, float eps,
+                 void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * The same step with the momentum held in 8 bits (1 + 4/256 bytes per
+ * parameter): codes int8 [batch][rows][cols], scales fp32
+ * [batch][rows][ceil(cols/256)], one for 256 elements of a row (the last block
+ * of a row may be short), all zero before the first step.  A step forms
+ * m = beta*code*scale + (1-beta)*g in 64 bits, makes U of it unrounded, and
+ * writes scale' = fp32(max|m| / 127) and code' = the nearest integer to
+ * m/scale' (ties to even; a block of zeros has scale 0 and codes 0).  A block
+ * with a NaN or an infinity gets the scale NaN and codes 0: it reads as NaN.
+ */
+int ma_muon8_step(int64_t batch, int64_t rows, int64_t cols, void *params, int p_type, int64_t p_row,
+                  int64_t p_batch, const uint16_t *grads, int64_t g_row, int64_t g_batch, int8_t *codes,
+                  float *scales, double lr, double beta, double wd, double scale, int nesterov, int steps,
+                  const float *coefficients, float eps, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Reads an 8-bit momentum: out (fp32, rows x cols) = code*scale; codes and
+ * scales as ma_muon8_step lays them out (rows: batch*rows of it). */
+int ma_momentum8_values(int64_t rows, int64_t cols, const int8_t *codes, const float *scales, float *out,
+                        hipStream_t stream);
+
 /* Optimizer-state bytes the second paragraph of the MicroAdam page counts:
  * ceil(d/2) + 4*m*k (0.9d at m = 10, k = d/100).  0 for NULL. */
 size_t ma_state_bytes(const ma_ctx *h);

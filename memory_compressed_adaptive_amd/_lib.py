@@ -29,12 +29,16 @@ MA_STATE_CODES = 0
 MA_STATE_STATS = 1
 MA_STATE_WINDOW = 2
 
+MA_TYPE_F32 = 0
+MA_TYPE_BF16 = 1
+
 # every symbol include/microadam.h declares
 EXPORTS = (
     "ma_create", "ma_step", "ma_step_bf16", "ma_step_noalloc", "ma_adamw_step", "ma_adamw8_step", "ma_state_bytes", "ma_aux_bytes", "ma_destroy", "ma_last_error",
     "ma_last_error_message", "ma_get_step", "ma_num_blocks", "ma_set_step", "ma_set_flags",
     "ma_set_lr", "ma_read_state", "ma_write_state", "ma_export_state", "ma_import_state", "ma_debug_moments", "ma_debug_residual", "ma_set_timing",
     "ma_kernel_times", "ma_set_pipeline", "ma_get_pipeline", "ma_set_count_touched", "ma_touched_count",
+    "ma_orthogonalize_workspace", "ma_orthogonalize", "ma_muon_step", "ma_muon8_step", "ma_momentum8_values",
 )
 
 _lib = None
@@ -55,6 +59,7 @@ def lib():
                           "(or __graft_entry__.build())")
     L = C.CDLL(LIB_PATH)
     p, i32, i64, u32, u64, f32 = C.c_void_p, C.c_int32, C.c_int64, C.c_uint32, C.c_uint64, C.c_float
+    f64, size = C.c_double, C.c_size_t
     L.ma_create.restype = p
     L.ma_create.argtypes = [i64, i32, i64, i32, i32, f32, f32, f32, f32, f32, u64]
     L.ma_step.restype = C.c_int
@@ -111,6 +116,18 @@ def lib():
     L.ma_set_count_touched.argtypes = [p, C.c_int]
     L.ma_touched_count.restype = i64
     L.ma_touched_count.argtypes = [p]
+    L.ma_orthogonalize_workspace.restype = size
+    L.ma_orthogonalize_workspace.argtypes = [i64, i64, i64]
+    L.ma_orthogonalize.restype = C.c_int
+    L.ma_orthogonalize.argtypes = [i64, i64, i64, p, C.c_int, i64, i64, p, i64, i64, C.c_int, p, f32, p, size, p]
+    L.ma_muon_step.restype = C.c_int
+    L.ma_muon_step.argtypes = [i64, i64, i64, p, C.c_int, i64, i64, p, i64, i64, p, f64, f64, f64, f64, C.c_int,
+                               C.c_int, p, f32, p, size, p]
+    L.ma_muon8_step.restype = C.c_int
+    L.ma_muon8_step.argtypes = [i64, i64, i64, p, C.c_int, i64, i64, p, i64, i64, p, p, f64, f64, f64, f64, C.c_int,
+                                C.c_int, p, f32, p, size, p]
+    L.ma_momentum8_values.restype = C.c_int
+    L.ma_momentum8_values.argtypes = [i64, i64, p, p, p, p]
     _lib = L
     return L
 

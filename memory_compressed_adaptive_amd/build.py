@@ -2,7 +2,8 @@
 
     python -m memory_compressed_adaptive_amd.build
 
-libmicroadam.so  -- the MicroAdam step (C ABI in include/microadam.h)
+libmicroadam.so  -- the MicroAdam step and the Muon operators (C ABI in
+                    include/microadam.h)
 libmasynth.so    -- the seeded synthetic-input generator used by the benchmark
                     and the tests (no optimizer arithmetic in it)
 
@@ -15,6 +16,8 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -25,7 +28,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 COMMON = [
-    "-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC", "-shared",
+    "-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC",
     "-ffp-contract=off", "-fno-fast-math", "-fhip-fp32-correctly-rounded-divide-sqrt",
     "-fno-gpu-flush-denormals-to-zero",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -34,32 +37,40 @@ COMMON = [
 ]
 
 TARGETS = {
-    "libmicroadam.so": [os.path.join(CSRC, "microadam.hip")],
+    "libmicroadam.so": [os.path.join(CSRC, "microadam.hip"), os.path.join(CSRC, "muon.hip")],
     "libmasynth.so": [os.path.join(CSRC, "synth.hip")],
 }
 
 
+def _run(cmd: list[str], what: str, verbose: bool) -> None:
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError(f"hipcc failed for {what}")
+    if verbose and r.stderr.strip():
+        # hipcc's host pass does not know the packed-fp32 feature; harmless
+        lines = [ln for ln in r.stderr.splitlines() if "packed-fp32-ops" not in ln]
+        if any(ln.strip() for ln in lines):
+            sys.stderr.write("\n".join(lines) + "\n")
+
+
 def build(verbose: bool = False, only: str | None = None) -> list[str]:
+    """Compiles every source to an object (all at once), then links each library."""
     out = []
-    for name, srcs in TARGETS.items():
-        if only and name != only:
-            continue
-        dst = os.path.join(PKG, name)
-        tmp = dst + ".tmp"
-        cmd = [HIPCC, *COMMON, *srcs, "-o", tmp]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            sys.stderr.write(r.stdout + r.stderr)
-            raise RuntimeError(f"hipcc failed for {name}")
-        elif verbose and (r.stderr.strip()):
-            # hipcc's host pass does not know the packed-fp32 feature; harmless
-            lines = [ln for ln in r.stderr.splitlines() if "packed-fp32-ops" not in ln]
-            if any(ln.strip() for ln in lines):
-                sys.stderr.write("\n".join(lines) + "\n")
-        os.replace(tmp, dst)
-        out.append(dst)
+    targets = {name: srcs for name, srcs in TARGETS.items() if not only or name == only}
+    with tempfile.TemporaryDirectory() as tmpdir, ThreadPoolExecutor() as pool:
+        obj = {src: os.path.join(tmpdir, os.path.basename(src) + ".o") for srcs in targets.values() for src in srcs}
+        jobs = [pool.submit(_run, [HIPCC, *COMMON, "-c", src, "-o", o], src, verbose) for src, o in obj.items()]
+        for job in jobs:
+            job.result()
+        for name, srcs in targets.items():
+            dst = os.path.join(PKG, name)
+            tmp = dst + ".tmp"
+            _run([HIPCC, f"--offload-arch={ARCH}", "-fPIC", "-shared", *(obj[src] for src in srcs), "-o", tmp], name, verbose)
+            os.replace(tmp, dst)
+            out.append(dst)
     return out
 
 

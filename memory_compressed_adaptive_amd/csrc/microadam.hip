@@ -14,6 +14,7 @@
 #include "microadam.h"
 #include "microadam_kernels.hpp"
 #include "adamw_kernels.hpp"
+#include "host.hpp"
 
 using namespace microadam;
 
@@ -21,6 +22,10 @@ namespace {
 
 thread_local int g_err = MA_OK;
 thread_local char g_msg[512] = "";
+
+}  // namespace
+
+namespace microadam {
 
 int fail(int code, const char *fmt, ...) {
   g_err = code;
@@ -35,6 +40,10 @@ void clear_error() {
   g_err = MA_OK;
   g_msg[0] = 0;
 }
+
+}  // namespace microadam
+
+namespace {
 
 // Largest dynamic LDS the update kernel asks for: three of its workgroups,
 // with their static LDS (under 1 KiB), fit one CU's 160 KiB.  A long window
@@ -218,20 +227,6 @@ int64_t floor_mul_div(int64_t k, int64_t x, int64_t d) {
   const unsigned __int128 p = (unsigned __int128)(uint64_t)k * (uint64_t)x;
   return (int64_t)(p / (uint64_t)d);
 }
-
-// Device guard: runs with the handle's device current, restores afterwards.
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = true;
-  explicit DeviceGuard(int dev) {
-    if (hipGetDevice(&prev) != hipSuccess) { ok = false; return; }
-    if (prev != dev && hipSetDevice(dev) != hipSuccess) ok = false;
-  }
-  ~DeviceGuard() {
-    int cur = -1;
-    if (prev >= 0 && hipGetDevice(&cur) == hipSuccess && cur != prev) (void)hipSetDevice(prev);
-  }
-};
 
 // Compressor launches for blocks [b0, b1): blocks below n_full take the
 // bounds-free kernel (plus the kernel finishing what it deferred), the rest

@@ -1,0 +1,322 @@
+// Host side of the Muon operators: argument checks, the workspace's layout and
+// the launches, all on the caller's stream.  The C ABI is declared and
+// documented in include/microadam.h.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "host.hpp"
+#include "microadam.h"
+#include "muon_kernels.hpp"
+
+using namespace microadam;
+
+namespace {
+
+constexpr int64_t kMaxElems = int64_t(1) << 33;     // of one matrix: keeps every launch's grid in range
+constexpr int kMaxSteps = 64;
+constexpr int kNormParts = 256;                     // most partial sums of squares for one matrix
+constexpr size_t kWorkspaceAim = size_t(512) << 20; // a batch is cut into runs of matrices of about this much workspace
+
+struct Coefficients { float v[kMaxSteps][3]; };
+
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// How a batch of r x c matrices is cut and laid out in the workspace.
+struct Plan {
+  int64_t r, c, n, m;       // n <= m: the wide orientation's sides
+  bool tall;
+  int64_t np, mp;           // padded
+  int64_t chunk;            // matrices at a time
+  int nparts;
+  size_t x_bytes, a_bytes, part_bytes, bytes;
+
+  Plan(int64_t batch, int64_t rows, int64_t cols) : r(rows), c(cols) {
+    tall = r > c;
+    n = std::min(r, c);
+    m = std::max(r, c);
+    np = round_up(n, kTile);
+    mp = round_up(m, kTile);
+    nparts = (int)std::min<int64_t>(kNormParts, (r * ((c + 255) / 256) + 15) / 16);
+    const size_t one = 3 * 2 * (size_t)(np * mp) + 2 * 2 * (size_t)(np * np) + 8 * (size_t)nparts;
+    chunk = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(batch, 65535), (int64_t)(kWorkspaceAim / one)));
+    x_bytes = (size_t)round_up(2 * chunk * np * mp, 256);
+    a_bytes = (size_t)round_up(2 * chunk * np * np, 256);
+    part_bytes = (size_t)round_up(8 * chunk * nparts, 256);
+    bytes = 3 * x_bytes + 2 * a_bytes + part_bytes;
+  }
+};
+
+bool sizes_ok(int64_t batch, int64_t rows, int64_t cols) {
+  return batch >= 0 && rows >= 0 && cols >= 0 && batch <= (int64_t(1) << 31) && rows <= kMaxElems && cols <= kMaxElems &&
+         (rows == 0 || cols <= kMaxElems / rows);
+}
+
+// Whether the iterates stay inside the fp16 formats: with every singular value
+// in [0, hi], a step maps s to s (a + b s^2 + c s^4); a + b x + c x^2 are the
+// eigenvalues of P.  Extremes of both lie at ends or where a derivative is 0.
+bool coefficients_ok(const float *k, int steps, const char **why) {
+  double hi = 1.0;
+  for (int t = 0; t < steps; ++t) {
+    const double a = k[3 * t], b = k[3 * t + 1], c = k[3 * t + 2];
+    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) { *why = "not finite"; return false; }
+    double xs[5] = {0.0, hi * hi, 0.0, 0.0, 0.0};
+    int nx = 2;
+    if (c != 0.0) {
+      xs[nx++] = -b / (2 * c);                       // of a + b x + c x^2
+      const double disc = 9 * b * b - 20 * a * c;    // of s (a + b s^2 + c s^4): a + 3 b x + 5 c x^2 = 0
+      if (disc >= 0) {
+        xs[nx++] = (-3 * b + std::sqrt(disc)) / (10 * c);
+        xs[nx++] = (-3 * b - std::sqrt(disc)) / (10 * c);
+      }
+    } else if (b != 0.0) {
+      xs[nx++] = -a / (3 * b);
+    }
+    double top = 0.0;
+    for (int q = 0; q < nx; ++q) {
+      const double x = xs[q];
+      if (!(x >= 0.0 && x <= hi * hi)) continue;
+      const double p = a + b * x + c * x * x;
+      if (!(std::fabs(p) <= 15.0)) { *why = "an eigenvalue of a I + b A + c A A can pass 15"; return false; }
+      top = std::max(top, std::fabs(p) * std::sqrt(x));
+    }
+    hi = top * 1.01;                                 // with room for the roundings
+    if (!(hi <= 1.95)) { *why = "a singular value can pass 1.95"; return false; }
+    if (hi < 1e-3) { *why = "the singular values vanish"; return false; }
+  }
+  return true;
+}
+
+template <int ROLE>
+void product(const MuonProduct &a, int64_t chunk, hipStream_t s) {
+  const dim3 grid((unsigned)(a.m / kTile), (unsigned)(a.n / kTile), (unsigned)chunk);
+  hipLaunchKernelGGL((muon_product_kernel<ROLE>), grid, dim3(256), 0, s, a);
+}
+
+struct MuonOutput {
+  void *out;
+  int bf16, update;
+  int64_t row, batch;
+  double decay, rate;
+};
+
+template <int MOM>
+hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonOutput &o, int steps, const Coefficients &k,
+               float eps, void *workspace, hipStream_t s) {
+  char *w = (char *)workspace;
+  _Float16 *x = (_Float16 *)w, *t0 = (_Float16 *)(w + p.x_bytes), *t1 = (_Float16 *)(w + 2 * p.x_bytes);
+  _Float16 *ga = (_Float16 *)(w + 3 * p.x_bytes), *gp = (_Float16 *)(w + 3 * p.x_bytes + p.a_bytes);
+  double *part = (double *)(w + 3 * p.x_bytes + 2 * p.a_bytes);
+  const int64_t nm = p.np * p.mp, nn = p.np * p.np;
+  for (int64_t b0 = 0; b0 < batch; b0 += p.chunk) {
+    const int64_t cb = std::min(p.chunk, batch - b0);
+    hipLaunchKernelGGL((muon_norm_kernel<MOM>), dim3((unsigned)p.nparts, (unsigned)cb), dim3(256), 0, s, in, b0, part,
+                       p.nparts);
+    const int64_t sp = p.tall ? p.np : p.mp, tp = p.tall ? p.mp : p.np;   // columns of the stored orientation, of the other
+    const dim3 lg((unsigned)((sp + kLoadCols - 1) / kLoadCols), (unsigned)((tp + kLoadRows - 1) / kLoadRows), (unsigned)cb);
+    hipLaunchKernelGGL((muon_load_kernel<MOM>), lg, dim3(256), 0, s, in, b0, part, p.nparts, eps,
+                       p.tall ? t0 : x, sp, p.tall ? x : t0, tp);
+    _Float16 *xt = t0, *nt = t1;
+    for (int t = 0; t < steps; ++t) {
+      MuonProduct a = {};
+      a.a = k.v[t][0], a.b = k.v[t][1], a.c = k.v[t][2];
+      a.l = a.r = x;
+      a.l_mat = a.r_mat = nm;
+      a.k = p.mp;
+      a.m = a.n = p.np;
+      a.d = ga;
+      product<kGram>(a, cb, s);
+      a.l = a.r = ga;
+      a.l_mat = a.r_mat = nn;
+      a.k = p.np;
+      a.d = gp;
+      product<kPoly>(a, cb, s);
+      if (t + 1 < steps) {
+        a.l = xt, a.l_mat = nm, a.m = p.mp;
+        a.r = gp, a.r_mat = nn, a.n = p.np;
+        a.d = x, a.dt = nt;
+        product<kUpdate>(a, cb, s);
+        std::swap(xt, nt);
+        continue;
+      }
+      // the fastest index of `out` is the wide orientation's m, or n if the matrix is tall
+      a.l = p.tall ? gp : xt, a.l_mat = p.tall ? nn : nm, a.m = p.tall ? p.np : p.mp;
+      a.r = p.tall ? xt : gp, a.r_mat = p.tall ? nm : nn, a.n = p.tall ? p.mp : p.np;
+      a.out = o.out, a.out_bf16 = o.bf16, a.update = o.update;
+      a.out_row = o.row, a.out_batch = o.batch, a.rows = p.r, a.cols = p.c;
+      a.decay = (float)o.decay, a.rate = (float)o.rate;
+      a.b0 = b0;
+      product<kOut>(a, cb, s);
+    }
+  }
+  return hipGetLastError();
+}
+
+// Checks that all calls share; MA_OK and *empty when there is nothing to do.
+int check(const char *who, int64_t batch, int64_t rows, int64_t cols, int steps, const float *coefficients, float eps,
+          const void *workspace, size_t workspace_bytes, bool *empty) {
+  *empty = false;
+  if (batch < 0 || rows < 0 || cols < 0) return fail(MA_EINVAL, "%s: batch, rows and cols must be >= 0", who);
+  if (!sizes_ok(batch, rows, cols)) return fail(MA_EUNSUPPORTED, "%s: a matrix of more than 2^33 elements", who);
+  if (steps < 1 || steps > kMaxSteps) return fail(MA_EINVAL, "%s: steps must be in 1..%d", who, kMaxSteps);
+  if (!coefficients) return fail(MA_EINVAL, "%s: null coefficients", who);
+  if (!(eps > 0.f) || !std::isfinite(eps)) return fail(MA_EINVAL, "%s: eps must be positive and finite", who);
+  const char *why = "";
+  if (!coefficients_ok(coefficients, steps, &why)) return fail(MA_EINVAL, "%s: coefficients: %s", who, why);
+  if (!batch || !rows || !cols) { *empty = true; return MA_OK; }
+  const Plan p(batch, rows, cols);
+  if (!workspace || ((uintptr_t)workspace & 255u)) return fail(MA_EINVAL, "%s: the workspace must be 256-byte aligned", who);
+  if (workspace_bytes < p.bytes)
+    return fail(MA_EINVAL, "%s: a workspace of %zu bytes, %zu are needed", who, workspace_bytes, p.bytes);
+  return MA_OK;
+}
+
+// Strides count up; what is written must not overlap (what is read may: a
+// stride of 0 reads one matrix or one row again).
+bool strides_ok(int64_t batch, int64_t rows, int64_t cols, int64_t row, int64_t bat, bool written) {
+  if (row < 0 || bat < 0) return false;
+  if (!written) return true;
+  if (rows > 1 && row < cols) return false;
+  return batch <= 1 || (__int128)bat >= (__int128)(rows - 1) * row + cols;
+}
+
+bool aligned_runs(const void *p, int elem, int64_t row, int64_t bat, int64_t rows, int64_t batch) {
+  return ((uintptr_t)p & (uintptr_t)(4 * elem - 1)) == 0 && (rows == 1 || row % 4 == 0) && (batch == 1 || bat % 4 == 0);
+}
+
+int device_of(hipStream_t stream, int *dev) {
+  if (!stream || stream == hipStreamLegacy || stream == hipStreamPerThread) return hipGetDevice(dev) == hipSuccess ? MA_OK : MA_EHIP;
+  return hipStreamGetDevice(stream, dev) == hipSuccess ? MA_OK : MA_EHIP;
+}
+
+Coefficients copy(const float *k, int steps) {
+  Coefficients c = {};
+  for (int t = 0; t < steps; ++t)
+    for (int e = 0; e < 3; ++e) c.v[t][e] = k[3 * t + e];
+  return c;
+}
+
+template <int MOM>
+int enqueue(const char *who, int64_t batch, const MuonInput &in, const MuonOutput &o, int steps, const float *coefficients,
+            float eps, void *workspace, hipStream_t stream) {
+  int dev = 0;
+  if (device_of(stream, &dev) != MA_OK) return fail(MA_EHIP, "%s: the stream has no device", who);
+  DeviceGuard guard(dev);
+  if (!guard.ok) return fail(MA_EHIP, "%s: device %d cannot be made current", who, dev);
+  const hipError_t e = run<MOM>(Plan(batch, in.r, in.c), batch, in, o, steps, copy(coefficients, steps), eps, workspace, stream);
+  if (e != hipSuccess) return fail(MA_EHIP, "%s: launch failed: %s", who, hipGetErrorString(e));
+  return MA_OK;
+}
+
+// what ma_muon_step and ma_muon8_step share
+int check_step(const char *who, int64_t batch, int64_t rows, int64_t cols, const void *params, int p_type, int64_t p_row,
+               int64_t p_batch, const uint16_t *grads, int64_t g_row, int64_t g_batch, double lr, double beta, double wd,
+               double scale) {
+  if (p_type != MA_TYPE_F32 && p_type != MA_TYPE_BF16) return fail(MA_EINVAL, "%s: unknown type %d", who, p_type);
+  if (!params || !grads) return fail(MA_EINVAL, "%s: null pointer", who);
+  if (((uintptr_t)params & (p_type == MA_TYPE_F32 ? 3u : 1u)) || ((uintptr_t)grads & 1u))
+    return fail(MA_EINVAL, "%s: misaligned pointer", who);
+  if (!(beta >= 0.0 && beta < 1.0)) return fail(MA_EINVAL, "%s: beta must be in [0, 1)", who);
+  if (!std::isfinite(lr) || !std::isfinite(scale) || !(wd >= 0.0) || !std::isfinite(wd))
+    return fail(MA_EINVAL, "%s: lr, scale and wd must be finite, wd >= 0", who);
+  if (!strides_ok(batch, rows, cols, p_row, p_batch, true) || !strides_ok(batch, rows, cols, g_row, g_batch, false))
+    return fail(MA_EINVAL, "%s: strides", who);
+  return MA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t ma_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols) {
+  if (!sizes_ok(batch, rows, cols) || !batch || !rows || !cols) return 0;
+  return Plan(batch, rows, cols).bytes;
+}
+
+int ma_orthogonalize(int64_t batch, int64_t rows, int64_t cols, const void *x, int x_type, int64_t x_row, int64_t x_batch,
+                     uint16_t *out, int64_t out_row, int64_t out_batch, int steps, const float *coefficients, float eps,
+                     void *workspace, size_t workspace_bytes, hipStream_t stream) {
+  clear_error();
+  const char *who = "ma_orthogonalize";
+  bool empty;
+  if (const int rc = check(who, batch, rows, cols, steps, coefficients, eps, workspace, workspace_bytes, &empty)) return rc;
+  if (x_type != MA_TYPE_F32 && x_type != MA_TYPE_BF16) return fail(MA_EINVAL, "%s: unknown type %d", who, x_type);
+  if (empty) return MA_OK;
+  const int elem = x_type == MA_TYPE_F32 ? 4 : 2;
+  if (!x || !out) return fail(MA_EINVAL, "%s: null pointer", who);
+  if (((uintptr_t)x & (uintptr_t)(elem - 1)) || ((uintptr_t)out & 1u)) return fail(MA_EINVAL, "%s: misaligned pointer", who);
+  if (!strides_ok(batch, rows, cols, x_row, x_batch, false) || !strides_ok(batch, rows, cols, out_row, out_batch, true))
+    return fail(MA_EINVAL, "%s: strides", who);
+  MuonInput in = {};
+  in.x = x, in.x_bf16 = x_type == MA_TYPE_BF16, in.x_row = x_row, in.x_batch = x_batch;
+  in.r = rows, in.c = cols;
+  in.vec = aligned_runs(x, elem, x_row, x_batch, rows, batch);
+  const MuonOutput o = {out, 1, 0, out_row, out_batch, 1.0, 0.0};
+  return enqueue<kMomNone>(who, batch, in, o, steps, coefficients, eps, workspace, stream);
+}
+
+int ma_muon_step(int64_t batch, int64_t rows, int64_t cols, void *params, int p_type, int64_t p_row, int64_t p_batch,
+                 const uint16_t *grads, int64_t g_row, int64_t g_batch, float *momentum, double lr, double beta, double wd,
+                 double scale, int nesterov, int steps, const float *coefficients, float eps, void *workspace,
+                 size_t workspace_bytes, hipStream_t stream) {
+  clear_error();
+  const char *who = "ma_muon_step";
+  bool empty;
+  if (const int rc = check(who, batch, rows, cols, steps, coefficients, eps, workspace, workspace_bytes, &empty)) return rc;
+  if (empty) return MA_OK;
+  if (const int rc = check_step(who, batch, rows, cols, params, p_type, p_row, p_batch, grads, g_row, g_batch, lr, beta, wd, scale))
+    return rc;
+  if (!momentum || ((uintptr_t)momentum & 3u)) return fail(MA_EINVAL, "%s: null or misaligned momentum", who);
+  MuonInput in = {};
+  in.x = grads, in.x_bf16 = 1, in.x_row = g_row, in.x_batch = g_batch;
+  in.mom = momentum, in.beta = beta, in.nesterov = nesterov != 0;
+  in.r = rows, in.c = cols;
+  in.vec = aligned_runs(grads, 2, g_row, g_batch, rows, batch) && ((uintptr_t)momentum & 15u) == 0 && cols % 4 == 0;
+  const MuonOutput o = {params, p_type == MA_TYPE_BF16, 1, p_row, p_batch, 1.0 - lr * wd, lr * scale};
+  return enqueue<kMom32>(who, batch, in, o, steps, coefficients, eps, workspace, stream);
+}
+
+int ma_muon8_step(int64_t batch, int64_t rows, int64_t cols, void *params, int p_type, int64_t p_row, int64_t p_batch,
+                  const uint16_t *grads, int64_t g_row, int64_t g_batch, int8_t *codes, float *scales, double lr, double beta,
+                  double wd, double scale, int nesterov, int steps, const float *coefficients, float eps, void *workspace,
+                  size_t workspace_bytes, hipStream_t stream) {
+  clear_error();
+  const char *who = "ma_muon8_step";
+  bool empty;
+  if (const int rc = check(who, batch, rows, cols, steps, coefficients, eps, workspace, workspace_bytes, &empty)) return rc;
+  if (empty) return MA_OK;
+  if (const int rc = check_step(who, batch, rows, cols, params, p_type, p_row, p_batch, grads, g_row, g_batch, lr, beta, wd, scale))
+    return rc;
+  if (!codes || !scales || ((uintptr_t)scales & 3u)) return fail(MA_EINVAL, "%s: null or misaligned momentum", who);
+  MuonInput in = {};
+  in.x = grads, in.x_bf16 = 1, in.x_row = g_row, in.x_batch = g_batch;
+  in.codes = codes, in.scales = scales, in.beta = beta, in.nesterov = nesterov != 0;
+  in.r = rows, in.c = cols;
+  in.vec = aligned_runs(grads, 2, g_row, g_batch, rows, batch) && ((uintptr_t)codes & 3u) == 0 && cols % 4 == 0;
+  const MuonOutput o = {params, p_type == MA_TYPE_BF16, 1, p_row, p_batch, 1.0 - lr * wd, lr * scale};
+  return enqueue<kMom8>(who, batch, in, o, steps, coefficients, eps, workspace, stream);
+}
+
+int ma_momentum8_values(int64_t rows, int64_t cols, const int8_t *codes, const float *scales, float *out, hipStream_t stream) {
+  clear_error();
+  const char *who = "ma_momentum8_values";
+  if (rows < 0 || cols < 0) return fail(MA_EINVAL, "%s: rows and cols must be >= 0", who);
+  if (!rows || !cols) return MA_OK;
+  if (rows > (int64_t(1) << 46) / cols) return fail(MA_EUNSUPPORTED, "%s: more than 2^46 elements", who);
+  if (!codes || !scales || !out || ((uintptr_t)scales & 3u) || ((uintptr_t)out & 3u))
+    return fail(MA_EINVAL, "%s: null or misaligned pointer", who);
+  int dev = 0;
+  if (device_of(stream, &dev) != MA_OK) return fail(MA_EHIP, "%s: the stream has no device", who);
+  DeviceGuard guard(dev);
+  if (!guard.ok) return fail(MA_EHIP, "%s: device %d cannot be made current", who, dev);
+  const int vec = cols % 4 == 0 && ((uintptr_t)codes & 3u) == 0 && ((uintptr_t)out & 15u) == 0;
+  const int64_t segs = rows * ((cols + 255) / 256);
+  const unsigned grid = (unsigned)std::min<int64_t>((segs + 3) / 4, 256 * 32);
+  hipLaunchKernelGGL(momentum8_values_kernel, dim3(grid), dim3(256), 0, stream, codes, scales, out, rows, cols, vec);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return fail(MA_EHIP, "%s: launch failed: %s", who, hipGetErrorString(e));
+  return MA_OK;
+}
+
+}  // extern "C"
