@@ -197,7 +197,7 @@ int ma_adamw8_step(int64_t n, int64_t t, float beta1, float beta2, float eps, fl
  * aligned, on the stream's device, the call's own until its work on `stream` is
  * done; what it holds before and after does not matter.  Nothing is allocated,
  * every launch goes to `stream`, and a call can be captured into a HIP graph.
- * A matrix has at most 2^33 elements (MA_EUNSUPPORTED).  steps: 1..64.
+ * A matrix has at most 2^33 elements and sides of 2^21 (MA_EUNSUPPORTED).  steps: 1..64.
  * batch = 0, rows = 0 or cols = 0: MA_OK, nothing done.  MA_EINVAL: null or
  * misaligned pointers (each array to its elements), negative sizes, a small
  * workspace, strides of a written array that overlap.

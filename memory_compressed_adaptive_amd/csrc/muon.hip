@@ -15,6 +15,7 @@ using namespace microadam;
 namespace {
 
 constexpr int64_t kMaxElems = int64_t(1) << 33;     // of one matrix: keeps every launch's grid in range
+constexpr int64_t kMaxSide = int64_t(1) << 21;      // 256 rows' bytes stay under 2^31
 constexpr int kMaxSteps = 64;
 constexpr int kNormParts = 256;                     // most partial sums of squares for one matrix
 constexpr size_t kWorkspaceAim = size_t(512) << 20; // a batch is cut into runs of matrices of about this much workspace
@@ -36,20 +37,20 @@ struct Plan {
     tall = r > c;
     n = std::min(r, c);
     m = std::max(r, c);
-    np = round_up(n, kTile);
-    mp = round_up(m, kTile);
+    np = round_up(n, 64);
+    mp = round_up(m, 64);
     nparts = (int)std::min<int64_t>(kNormParts, (r * ((c + 255) / 256) + 15) / 16);
-    const size_t one = 3 * 2 * (size_t)(np * mp) + 2 * 2 * (size_t)(np * np) + 8 * (size_t)nparts;
+    const size_t one = 2 * 2 * (size_t)(np * mp) + 2 * 2 * (size_t)(np * np) + 8 * (size_t)nparts;
     chunk = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(batch, 65535), (int64_t)(kWorkspaceAim / one)));
     x_bytes = (size_t)round_up(2 * chunk * np * mp, 256);
     a_bytes = (size_t)round_up(2 * chunk * np * np, 256);
     part_bytes = (size_t)round_up(8 * chunk * nparts, 256);
-    bytes = 3 * x_bytes + 2 * a_bytes + part_bytes;
+    bytes = 2 * x_bytes + 2 * a_bytes + part_bytes;
   }
 };
 
 bool sizes_ok(int64_t batch, int64_t rows, int64_t cols) {
-  return batch >= 0 && rows >= 0 && cols >= 0 && batch <= (int64_t(1) << 31) && rows <= kMaxElems && cols <= kMaxElems &&
+  return batch >= 0 && rows >= 0 && cols >= 0 && batch <= (int64_t(1) << 31) && rows <= kMaxSide && cols <= kMaxSide &&
          (rows == 0 || cols <= kMaxElems / rows);
 }
 
@@ -88,15 +89,55 @@ bool coefficients_ok(const float *k, int steps, const char **why) {
   return true;
 }
 
+using Tile64 = Tile<64, 64, 2, 2, 64, 2>;
+using Tile128 = Tile<128, 128, 2, 2, 64, 2>;
+using Tile192 = Tile<192, 192, 2, 2, 32, 3>;
+using Tile256 = Tile<256, 256, 4, 2, 64, 2>;
+
+template <class T, int ROLE>
+void product_t(MuonProduct a, int64_t chunk, hipStream_t s) {
+  a.tiles_m = (int)((a.m + T::BM - 1) / T::BM);
+  a.tiles_n = (int)((a.n + T::BN - 1) / T::BN);
+  a.tiles = ROLE <= kPoly ? a.tiles_n * (a.tiles_n + 1) / 2 : a.tiles_m * a.tiles_n;
+  hipLaunchKernelGGL((muon_product_kernel<T, ROLE>), dim3((unsigned)(a.tiles * chunk)), dim3(T::kThreads), 0, s, a);
+}
+
+// The tile with the shortest expected time: rounds of workgroups over the 256
+// CUs times what 64 of the summed index take in a round.  Measured on products
+// that fill the card: 1.88 us with 256 x 256 tiles (one workgroup on a CU),
+// 1.25 with 192 x 192 (one), 1.10 with 128 x 128 (two; 0.6 where there is only
+// one), 0.75 with 64 x 64 (four; 0.35).  Large tiles read less for each
+// product; smaller ones waste less of the last round and of the half that a
+// symmetric result leaves out (4096: 136 tiles of 256 take 1.88, 253 of 192 1.25).
+int pick_tile(int64_t m, int64_t n, int64_t chunk, bool symmetric) {
+  const struct { int side, per_cu; double one, full; } kinds[] = {
+      {256, 1, 1.88, 1.88}, {192, 1, 1.25, 1.25}, {128, 2, 0.60, 1.10}, {64, 4, 0.35, 0.75}};
+  int best = 0;
+  double least = 0.0;
+  for (const auto &k : kinds) {
+    const int64_t tm = (m + k.side - 1) / k.side, tn = (n + k.side - 1) / k.side;
+    const int64_t tiles = (symmetric ? tn * (tn + 1) / 2 : tm * tn) * chunk;
+    const int64_t whole = tiles / (256 * k.per_cu), rest = tiles - whole * 256 * k.per_cu;
+    const double tail = rest == 0 ? 0.0 : k.one + (k.full - k.one) * (double)((rest - 1) / 256) / std::max(1, k.per_cu - 1);
+    const double t = (double)whole * k.full + tail;
+    if (!best || t < least) best = k.side, least = t;
+  }
+  return best;
+}
+
 template <int ROLE>
 void product(const MuonProduct &a, int64_t chunk, hipStream_t s) {
-  const dim3 grid((unsigned)(a.m / kTile), (unsigned)(a.n / kTile), (unsigned)chunk);
-  hipLaunchKernelGGL((muon_product_kernel<ROLE>), grid, dim3(256), 0, s, a);
+  switch (pick_tile(a.m, a.n, chunk, ROLE <= kPoly)) {
+    case 256: return product_t<Tile256, ROLE>(a, chunk, s);
+    case 192: return product_t<Tile192, ROLE>(a, chunk, s);
+    case 128: return product_t<Tile128, ROLE>(a, chunk, s);
+    default: return product_t<Tile64, ROLE>(a, chunk, s);
+  }
 }
 
 struct MuonOutput {
   void *out;
-  int bf16, update;
+  int bf16, update, vec;
   int64_t row, batch;
   double decay, rate;
 };
@@ -105,49 +146,56 @@ template <int MOM>
 hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonOutput &o, int steps, const Coefficients &k,
                float eps, void *workspace, hipStream_t s) {
   char *w = (char *)workspace;
-  _Float16 *x = (_Float16 *)w, *t0 = (_Float16 *)(w + p.x_bytes), *t1 = (_Float16 *)(w + 2 * p.x_bytes);
-  _Float16 *ga = (_Float16 *)(w + 3 * p.x_bytes), *gp = (_Float16 *)(w + 3 * p.x_bytes + p.a_bytes);
-  double *part = (double *)(w + 3 * p.x_bytes + 2 * p.a_bytes);
+  _Float16 *x0 = (_Float16 *)w, *x1 = (_Float16 *)(w + p.x_bytes);
+  _Float16 *ga = (_Float16 *)(w + 2 * p.x_bytes), *gp = (_Float16 *)(w + 2 * p.x_bytes + p.a_bytes);
+  double *part = (double *)(w + 2 * p.x_bytes + 2 * p.a_bytes);
   const int64_t nm = p.np * p.mp, nn = p.np * p.np;
   for (int64_t b0 = 0; b0 < batch; b0 += p.chunk) {
     const int64_t cb = std::min(p.chunk, batch - b0);
     hipLaunchKernelGGL((muon_norm_kernel<MOM>), dim3((unsigned)p.nparts, (unsigned)cb), dim3(256), 0, s, in, b0, part,
                        p.nparts);
-    const int64_t sp = p.tall ? p.np : p.mp, tp = p.tall ? p.mp : p.np;   // columns of the stored orientation, of the other
+    const int64_t sp = p.tall ? p.np : p.mp, tp = p.tall ? p.mp : p.np;
     const dim3 lg((unsigned)((sp + kLoadCols - 1) / kLoadCols), (unsigned)((tp + kLoadRows - 1) / kLoadRows), (unsigned)cb);
-    hipLaunchKernelGGL((muon_load_kernel<MOM>), lg, dim3(256), 0, s, in, b0, part, p.nparts, eps,
-                       p.tall ? t0 : x, sp, p.tall ? x : t0, tp);
-    _Float16 *xt = t0, *nt = t1;
+    _Float16 *x = x0, *nx = x1;
+    if (p.tall)
+      hipLaunchKernelGGL((muon_load_kernel<MOM, true>), lg, dim3(256), 0, s, in, b0, part, p.nparts, eps, x, sp, tp);
+    else
+      hipLaunchKernelGGL((muon_load_kernel<MOM, false>), lg, dim3(256), 0, s, in, b0, part, p.nparts, eps, x, sp, tp);
     for (int t = 0; t < steps; ++t) {
       MuonProduct a = {};
       a.a = k.v[t][0], a.b = k.v[t][1], a.c = k.v[t][2];
       a.l = a.r = x;
       a.l_mat = a.r_mat = nm;
-      a.k = p.mp;
+      a.l_ld = a.r_ld = a.k = p.mp;
       a.m = a.n = p.np;
       a.d = ga;
       product<kGram>(a, cb, s);
       a.l = a.r = ga;
       a.l_mat = a.r_mat = nn;
-      a.k = p.np;
+      a.l_ld = a.r_ld = a.k = p.np;
       a.d = gp;
       product<kPoly>(a, cb, s);
+      a.l = x, a.l_mat = nm, a.l_ld = a.m = p.mp;
+      a.r = gp;
       if (t + 1 < steps) {
-        a.l = xt, a.l_mat = nm, a.m = p.mp;
-        a.r = gp, a.r_mat = nn, a.n = p.np;
-        a.d = x, a.dt = nt;
+        a.d = nx;
         product<kUpdate>(a, cb, s);
-        std::swap(xt, nt);
+        std::swap(x, nx);
         continue;
       }
-      // the fastest index of `out` is the wide orientation's m, or n if the matrix is tall
-      a.l = p.tall ? gp : xt, a.l_mat = p.tall ? nn : nm, a.m = p.tall ? p.np : p.mp;
-      a.r = p.tall ? xt : gp, a.r_mat = p.tall ? nm : nn, a.n = p.tall ? p.mp : p.np;
-      a.out = o.out, a.out_bf16 = o.bf16, a.update = o.update;
+      a.out = o.out, a.out_bf16 = o.bf16, a.update = o.update, a.out_vec = o.vec;
       a.out_row = o.row, a.out_batch = o.batch, a.rows = p.r, a.cols = p.c;
       a.decay = (float)o.decay, a.rate = (float)o.rate;
       a.b0 = b0;
-      product<kOut>(a, cb, s);
+      if (p.tall) {   // the fastest index of `out` is P's
+        std::swap(a.l, a.r);
+        std::swap(a.l_mat, a.r_mat);
+        std::swap(a.l_ld, a.r_ld);
+        std::swap(a.m, a.n);
+        product<kOutTall>(a, cb, s);
+      } else {
+        product<kOut>(a, cb, s);
+      }
     }
   }
   return hipGetLastError();
@@ -158,7 +206,7 @@ int check(const char *who, int64_t batch, int64_t rows, int64_t cols, int steps,
           const void *workspace, size_t workspace_bytes, bool *empty) {
   *empty = false;
   if (batch < 0 || rows < 0 || cols < 0) return fail(MA_EINVAL, "%s: batch, rows and cols must be >= 0", who);
-  if (!sizes_ok(batch, rows, cols)) return fail(MA_EUNSUPPORTED, "%s: a matrix of more than 2^33 elements", who);
+  if (!sizes_ok(batch, rows, cols)) return fail(MA_EUNSUPPORTED, "%s: a matrix of more than 2^33 elements or a side over 2^21", who);
   if (steps < 1 || steps > kMaxSteps) return fail(MA_EINVAL, "%s: steps must be in 1..%d", who, kMaxSteps);
   if (!coefficients) return fail(MA_EINVAL, "%s: null coefficients", who);
   if (!(eps > 0.f) || !std::isfinite(eps)) return fail(MA_EINVAL, "%s: eps must be positive and finite", who);
@@ -181,7 +229,7 @@ bool strides_ok(int64_t batch, int64_t rows, int64_t cols, int64_t row, int64_t 
   return batch <= 1 || (__int128)bat >= (__int128)(rows - 1) * row + cols;
 }
 
-bool aligned_runs(const void *p, int elem, int64_t row, int64_t bat, int64_t rows, int64_t batch) {
+int aligned_runs(const void *p, int elem, int64_t row, int64_t bat, int64_t rows, int64_t batch) {
   return ((uintptr_t)p & (uintptr_t)(4 * elem - 1)) == 0 && (rows == 1 || row % 4 == 0) && (batch == 1 || bat % 4 == 0);
 }
 
@@ -252,7 +300,7 @@ int ma_orthogonalize(int64_t batch, int64_t rows, int64_t cols, const void *x, i
   in.x = x, in.x_bf16 = x_type == MA_TYPE_BF16, in.x_row = x_row, in.x_batch = x_batch;
   in.r = rows, in.c = cols;
   in.vec = aligned_runs(x, elem, x_row, x_batch, rows, batch);
-  const MuonOutput o = {out, 1, 0, out_row, out_batch, 1.0, 0.0};
+  const MuonOutput o = {out, 1, 0, aligned_runs(out, 2, out_row, out_batch, rows, batch), out_row, out_batch, 1.0, 0.0};
   return enqueue<kMomNone>(who, batch, in, o, steps, coefficients, eps, workspace, stream);
 }
 
@@ -273,7 +321,7 @@ int ma_muon_step(int64_t batch, int64_t rows, int64_t cols, void *params, int p_
   in.mom = momentum, in.beta = beta, in.nesterov = nesterov != 0;
   in.r = rows, in.c = cols;
   in.vec = aligned_runs(grads, 2, g_row, g_batch, rows, batch) && ((uintptr_t)momentum & 15u) == 0 && cols % 4 == 0;
-  const MuonOutput o = {params, p_type == MA_TYPE_BF16, 1, p_row, p_batch, 1.0 - lr * wd, lr * scale};
+  const MuonOutput o = {params, p_type == MA_TYPE_BF16, 1, aligned_runs(params, p_type == MA_TYPE_BF16 ? 2 : 4, p_row, p_batch, rows, batch), p_row, p_batch, 1.0 - lr * wd, lr * scale};
   return enqueue<kMom32>(who, batch, in, o, steps, coefficients, eps, workspace, stream);
 }
 
@@ -294,7 +342,7 @@ int ma_muon8_step(int64_t batch, int64_t rows, int64_t cols, void *params, int p
   in.codes = codes, in.scales = scales, in.beta = beta, in.nesterov = nesterov != 0;
   in.r = rows, in.c = cols;
   in.vec = aligned_runs(grads, 2, g_row, g_batch, rows, batch) && ((uintptr_t)codes & 3u) == 0 && cols % 4 == 0;
-  const MuonOutput o = {params, p_type == MA_TYPE_BF16, 1, p_row, p_batch, 1.0 - lr * wd, lr * scale};
+  const MuonOutput o = {params, p_type == MA_TYPE_BF16, 1, aligned_runs(params, p_type == MA_TYPE_BF16 ? 2 : 4, p_row, p_batch, rows, batch), p_row, p_batch, 1.0 - lr * wd, lr * scale};
   return enqueue<kMom8>(who, batch, in, o, steps, coefficients, eps, workspace, stream);
 }
 

@@ -19,10 +19,9 @@
 // random 768 x 768 matrices), in fp16 by 1.2e-3, at the same matrix rate; the
 // rounding of the bf16 result alone is 1.7e-3.
 //
-// Layout.  All products take both operands with the summed index contiguous.
-// X X^T and A A (A is its own transpose) have that; P X needs X^T, so X is
-// kept in both orientations.  Sides are padded with zeros to a multiple of the
-// tile: products keep the padding zero, so the main loops have no bounds.
+// Layout.  X is held once, in its wide orientation.  Sides are padded with zeros
+// to a multiple of 64 (the products keep the padding of X and A zero), so the
+// summed index needs no bounds.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -181,23 +180,23 @@ __device__ __forceinline__ double block_scale(const double *part, int nparts, fl
 }
 
 // ------------------------------------------------------------------ momentum, X0
-// Writes the new momentum, and X0 in both orientations: S (the stored one, sp
-// columns to a row) and T (its transpose, tp to a row), zeros in the padding.
-// A block of 256 threads takes 64 rows x 256 columns of the stored matrix: 4
-// columns to a lane, so that a wave holds the 256 elements of an 8-bit block.
+// Writes the new momentum, and X0 in its wide orientation with zeros in the
+// padding: as the matrix is stored, or transposed if that is tall.  A block of
+// 256 threads takes 64 rows x 256 columns of the stored matrix: 4 columns to a
+// lane, so that a wave holds the 256 elements of an 8-bit block.  sp, tp: the
+// stored orientation's padded columns and rows.
 constexpr int kLoadRows = 64, kLoadCols = 256;
 
-template <int MOM>
+template <int MOM, bool TALL>
 __global__ __launch_bounds__(256) void muon_load_kernel(MuonInput I, int64_t b0, const double *part, int nparts,
-                                                        float eps, _Float16 *S, int64_t sp, _Float16 *T, int64_t tp) {
+                                                        float eps, _Float16 *X, int64_t sp, int64_t tp) {
   __shared__ double s4[4];
-  __shared__ _Float16 tile[kLoadRows][kLoadCols + 4];
+  __shared__ _Float16 tile[TALL ? kLoadRows : 1][kLoadCols + 4];
   const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6);
   const int64_t lb = blockIdx.z, b = b0 + lb;
   const double scale = block_scale(part + lb * nparts, nparts, eps, s4);
   const int64_t i0 = (int64_t)blockIdx.y * kLoadRows, j0 = (int64_t)blockIdx.x * kLoadCols, j = j0 + 4 * lane;
-  S += lb * sp * tp;
-  T += lb * sp * tp;
+  X += lb * sp * tp;
   for (int q = wave; q < kLoadRows; q += 4) {
     const int64_t i = i0 + q;
     half4 h = {0, 0, 0, 0};
@@ -252,9 +251,10 @@ __global__ __launch_bounds__(256) void muon_load_kernel(MuonInput I, int64_t b0,
         if (lane == 0 && j0 < I.c) I.scales[(b * I.r + i) * ((I.c + 255) / 256) + j0 / 256] = step;
       }
     }
-    if (j < sp && i < tp) *(half4 *)(S + i * sp + j) = h;
-    *(half4 *)&tile[q][4 * lane] = h;
+    if (TALL) *(half4 *)&tile[q][4 * lane] = h;
+    else if (j < sp && i < tp) *(half4 *)(X + i * sp + j) = h;
   }
+  if (!TALL) return;
   __syncthreads();
   // transposed: 8 consecutive rows of a column to a lane, 8 lanes to a column
   const int rg = (int)(threadIdx.x & 7u);
@@ -262,108 +262,408 @@ __global__ __launch_bounds__(256) void muon_load_kernel(MuonInput I, int64_t b0,
     half8 h;
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[e] = tile[8 * rg + e][cc];
-    if (j0 + cc < sp && i0 + 8 * rg < tp) *(half8 *)(T + (j0 + cc) * tp + i0 + 8 * rg) = h;
+    if (j0 + cc < sp && i0 + 8 * rg < tp) *(half8 *)(X + (j0 + cc) * tp + i0 + 8 * rg) = h;
   }
 }
 
 // ------------------------------------------------------------------ products
-// D = L R^T with L (M x K) and R (N x K), K contiguous in both, fp32 sums.
+// D[n][m] = sum over k of L(m, k) R(n, k), fp32 sums.
 enum {
-  kGram = 0,    // A = X X^T:                     L = R = X
-  kPoly = 1,    // P = a I + b A + c A A:         L = R = A
-  kUpdate = 2,  // X <- P X in both orientations: L = X^T, R = P
-  kOut = 3,     // the last X, written where the caller wants it
+  kGram = 0,     // A = X X^T:               L = R = X
+  kPoly = 1,     // P = a I + b A + c A A:   L = R = A
+  kUpdate = 2,   // X' = P X:                L = X^T, R = P
+  kOut = 3,      // the last X', with L and R as in kUpdate, written where the caller wants it
+  kOutTall = 4,  // the same for a tall matrix, whose rows are the columns of X': L = P, R = X^T
 };
 
 struct MuonProduct {
   const _Float16 *l, *r;
   int64_t l_mat, r_mat;     // elements from one matrix to the next
-  int64_t k;                // and the row stride of both
-  _Float16 *d, *dt;         // d: [N][M]; dt: [M][N] (kUpdate)
+  int64_t l_ld, r_ld;       // and from one row of the stored array to the next
+  int64_t k;
+  _Float16 *d;              // [N][M]
   int64_t m, n;
+  int tiles_m, tiles_n, tiles;   // of one matrix
   float a, b, c;
   // kOut: element (n, m) goes to out[b][n][m], rows x cols of them
   void *out;
   int out_bf16, update;     // update: theta <- theta * decay - rate * x
+  int out_vec;              // runs of 4 elements are aligned
   int64_t out_row, out_batch, rows, cols;
   float decay, rate;
   int64_t b0;
 };
 
-constexpr int kTile = 64;
+// One workgroup makes a BM x BN tile of D with WM x WN waves, in steps of BK of
+// the summed index.  The panels of both operands go from memory straight into
+// LDS, S stages of them: while one is multiplied, the next S-1 are on their
+// way.  A wave holds the fragments for the next 16 in registers, so that LDS
+// reads run under the matrix instructions; the only barrier of a step stands
+// before its last 16, when all fragments of the stage are in registers, and
+// the copies that refill the stage are issued between that last 16's products.
+//
+// Panels come in two kinds.  Rows: the summed index is contiguous in memory; a
+// panel is B rows of BK, and a lane's 8 values are one b128 read.  Columns:
+// the other index is contiguous (X as the operand X^T of P X); a panel is BK
+// rows of B, and a lane's 8 values are two b64 reads that transpose a 4 x 16
+// block of 16-bit values among 16 lanes.  So X is kept in one orientation.
+//
+// Banks (64 of 4 bytes; a read serves 256 bytes a cycle).  Rows: 16-byte chunk
+// c of row r lies at c ^ (r / (rows in 256 bytes)), so that 16 lanes (rows) of
+// a b128 read take different banks (with c ^ (r & 7) at BK = 64 every read
+// counted four cycles of conflicts on top of its four).  Columns: 64-byte
+// chunk c of row k lies at c ^ k modulo the chunks in 256 bytes, so that the
+// four rows of a transposing read do.  The copies to LDS write their lanes one
+// after the other; the order is made by which chunk a lane loads.
+template <int BM_, int BN_, int WM_, int WN_, int BK_, int S_>
+struct Tile {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, S = S_;
+  static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;   // a wave's part, in 32 x 32 products
+  static constexpr int LI = BM * BK / 512 / kWaves, RI = BN * BK / 512 / kWaves; // 1 KiB copies of a wave
+  static constexpr int kStageBytes = (BM + BN) * BK * 2;
+  static_assert(LI * 512 * kWaves == BM * BK && RI * 512 * kWaves == BN * BK, "copies divide evenly among the waves");
+  static_assert(BK == 32 || BK == 64, "LDS orders are made for these");
+  static constexpr int kOutBytes = kWaves * 32 * (TM * 4 + 16);   // the epilogue's part of LDS
+  static constexpr int kLds = S * kStageBytes > kOutBytes ? S * kStageBytes : kOutBytes;
+  static_assert(kLds <= 160 * 1024, "LDS of a CU");
+};
 
-// Four waves of 32 x 32 over a 64 x 64 tile.
-template <int ROLE>
-__global__ __launch_bounds__(256) void muon_product_kernel(MuonProduct A) {
-  __shared__ _Float16 sl[kTile][kTile + 8], sr[kTile][kTile + 8];
-  const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6);
-  const int wm = (wave & 1) * 32, wn = (wave >> 1) * 32;
-  const int64_t m0 = (int64_t)blockIdx.x * kTile, n0 = (int64_t)blockIdx.y * kTile, lb = blockIdx.z;
-  if (ROLE <= kPoly && m0 > n0) return;   // symmetric: the other half is this one's mirror image
-  const _Float16 *l = A.l + lb * A.l_mat + m0 * A.k, *r = A.r + lb * A.r_mat + n0 * A.k;
-  float16v acc;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-  for (int64_t k0 = 0; k0 < A.k; k0 += kTile) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int at = (int)threadIdx.x + q * 256, row = at >> 3, col = (at & 7) * 8;
-      *(half8 *)&sl[row][col] = *(const half8 *)(l + row * A.k + k0 + col);
-      *(half8 *)&sr[row][col] = *(const half8 *)(r + row * A.k + k0 + col);
+typedef int int4v __attribute__((ext_vector_type(4)));
+typedef short short4v __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) short4v lds_short4;
+
+// A buffer resource over `bytes` bytes at p (uniform); loads past them give 0.
+__device__ __forceinline__ int4v buffer_of(const char *p, int64_t bytes) {
+  const uint64_t a = (uint64_t)p;
+  int4v r;
+  r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+  r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32) & 0xffff);
+  r[2] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(bytes < 0xffffffffll ? bytes : 0xffffffffll));
+  r[3] = 0x00020000;
+  return r;
+}
+
+// 16 bytes a lane, from p + voff to LDS at `lds` + 16 * lane.  In asm, because
+// after the builtin the compiler waits for every such copy before any later
+// LDS read; here the waits are the kernel's own (stage_wait).
+__device__ __forceinline__ void copy_to_lds(int4v p, uint32_t lds, uint32_t voff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(voff), "s"(p) : "memory", "m0");
+}
+
+// This wave's copies are done but for the last N, and so are its LDS reads;
+// then all waves meet.
+template <int N>
+__device__ __forceinline__ void stage_wait() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(N) : "memory");
+}
+
+// One wave's LDS writes are done before its later reads of other lanes' values.
+__device__ __forceinline__ void wave_lds_fence() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Which tile (ti along M, tj along N) of which matrix a workgroup makes.
+// Workgroups go to the eight XCDs in turn; each XCD gets one run of tiles,
+// taken in blocks of 4 x 4, so that the panels its 32 CUs read at a time fit
+// its L2.  SYM: only tiles with ti <= tj, the others are their mirror images.
+template <bool SYM>
+__device__ __forceinline__ void tile_of(const MuonProduct &A, int &lb, int &ti, int &tj) {
+  const uint32_t total = gridDim.x, id = blockIdx.x, xcd = id & 7, per = total >> 3, rem = total & 7;
+  const uint32_t at = xcd * per + (xcd < rem ? xcd : rem) + (id >> 3);
+  lb = (int)(at / (uint32_t)A.tiles);
+  int r = (int)(at - (uint32_t)lb * A.tiles);
+  if (SYM) {
+    // before row block J lie 4J (4J + 1) / 2 tiles
+    int J = (int)((sqrtf(4.f + 32.f * (float)r) - 2.f) * 0.0625f);
+    while (8 * J * J + 2 * J > r) --J;
+    while (8 * (J + 1) * (J + 1) + 2 * (J + 1) <= r) ++J;
+    r -= 8 * J * J + 2 * J;
+    const int h = A.tiles_n - 4 * J < 4 ? A.tiles_n - 4 * J : 4;
+    if (r < 4 * h * J) {
+      const int I = r / (4 * h);
+      r -= I * 4 * h;
+      ti = 4 * I + (r & 3);
+      tj = 4 * J + (r >> 2);
+    } else {
+      r -= 4 * h * J;
+      const int y = r >= 6 ? 3 : r >= 3 ? 2 : r >= 1 ? 1 : 0;
+      ti = 4 * J + r - y * (y + 1) / 2;
+      tj = 4 * J + y;
     }
-    __syncthreads();
-#pragma unroll
-    for (int kk = 0; kk < kTile; kk += 16) {
-      const half8 x = *(const half8 *)&sl[wm + (lane & 31)][kk + (lane >> 5) * 8];
-      const half8 y = *(const half8 *)&sr[wn + (lane & 31)][kk + (lane >> 5) * 8];
-      acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x, y, acc, 0, 0, 0);
-    }
-    __syncthreads();
+  } else {
+    const int J = r / (4 * A.tiles_m), h = A.tiles_n - 4 * J < 4 ? A.tiles_n - 4 * J : 4;
+    r -= J * 4 * A.tiles_m;
+    ti = r / h;
+    tj = 4 * J + r - ti * h;
   }
-  const int64_t nn = n0 + wn + (lane & 31);
+  lb = __builtin_amdgcn_readfirstlane(lb);
+  ti = __builtin_amdgcn_readfirstlane(ti);
+  tj = __builtin_amdgcn_readfirstlane(tj);
+}
+
+// Where 16-byte chunk g of a B-wide panel in LDS comes from: bytes from the
+// panel's start in memory, with rows of ld bytes.
+template <bool COLS, int B, int BK>
+__device__ __forceinline__ uint32_t panel_source(int g, uint32_t ld) {
+  if (COLS) {
+    constexpr int kRow = B / 8;   // chunks in a row
+    const int row = g / kRow, p = g % kRow;
+    constexpr int kIn = B % 128 == 0 ? 4 : 2;   // 64-byte chunks that are exchanged, in 256 bytes (128: two rows of them)
+    const int x = kIn == 4 ? row & 3 : row >> 1 & 1;
+    return (uint32_t)row * ld + (uint32_t)(p ^ (x << 2)) * 16;
+  }
+  constexpr int kRow = BK / 8, kRows256 = 16 / kRow;
+  const int row = g / kRow, p = g % kRow;
+  return (uint32_t)row * ld + (uint32_t)(p ^ (row / kRows256 & (kRow - 1))) * 16;
+}
+
+// A lane's 8 values for the product at 16 * ks: index `at` + (lane & 31) of the
+// panel, summed index 16 * ks + 8 * (lane / 32) + 0..7.
+template <bool COLS, int B, int BK>
+__device__ __forceinline__ half8 panel_read(const char *panel, int at, int ks, int lane) {
+  if (COLS) {
+    // lanes 16q..16q+15 transpose 4 rows of 16 columns: lane s of them points
+    // at row s / 4, columns 4 (s & 3) ..+3 and gets column s of the four rows
+    union { short4v s[2]; half8 h; } u;
+    const int s = lane & 15, col = at + (lane & 16) + 4 * (s & 3);
+    const int c16 = col >> 3, rest = (col & 7) * 2;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const int64_t mm = m0 + wm + 8 * q + 4 * (lane >> 5);   // and the next three
-    float v[4];
+    for (int e = 0; e < 2; ++e) {
+      const int row = 16 * ks + 8 * (lane >> 5) + 4 * e + (s >> 2);
+      constexpr int kIn = B % 128 == 0 ? 4 : 2;
+      const int x = kIn == 4 ? row & 3 : row >> 1 & 1;
+      u.s[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_short4 *)(panel + row * (B * 2) + ((c16 ^ (x << 2)) * 16 + rest)));
+    }
+    return u.h;
+  }
+  constexpr int kRow = BK / 8, kRows256 = 16 / kRow;
+  const int row = at + (lane & 31);
+  return *(const half8 *)(panel + row * (BK * 2) + (((2 * ks + (lane >> 5)) ^ (row / kRows256 & (kRow - 1))) * 16));
+}
+
+template <class T, int ROLE>
+__global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A) {
+  constexpr bool LC = ROLE == kUpdate || ROLE == kOut, RC = ROLE == kOutTall, OUT = ROLE >= kOut;
+  __shared__ __attribute__((aligned(1024))) char smem[T::kLds];
+  const int lane = (int)(threadIdx.x & 63u), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int wm = wave % T::WM * T::TM, wn = wave / T::WM * T::TN;
+  int lb, ti, tj;
+  tile_of<ROLE <= kPoly>(A, lb, ti, tj);
+  const int64_t m0 = (int64_t)ti * T::BM, n0 = (int64_t)tj * T::BN;
+
+  // Panels that pass the matrix: rows past its last read as zeros (the buffer
+  // ends there); columns past a row's last read the next row, and only reach
+  // elements of D past its sides, which are not stored.
+  const int64_t l_ld = 2 * A.l_ld, r_ld = 2 * A.r_ld;   // bytes of a row; 256 rows stay under 2^31
+  const char *pl = (const char *)(A.l + lb * A.l_mat) + (LC ? 2 * m0 : m0 * l_ld);
+  const char *pr = (const char *)(A.r + lb * A.r_mat) + (RC ? 2 * n0 : n0 * r_ld);
+  const int64_t nl = (const char *)(A.l + (lb + 1) * A.l_mat) - pl, nr = (const char *)(A.r + (lb + 1) * A.r_mat) - pr;
+  const int64_t sl = LC ? T::BK * l_ld : T::BK * 2, sr = RC ? T::BK * r_ld : T::BK * 2;   // to the next step
+  uint32_t vl[T::LI], vr[T::RI];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = acc[4 * q + e];
-    if (ROLE == kOut) {
-      if (nn >= A.rows) continue;
-      const int64_t at = (A.b0 + lb) * A.out_batch + nn * A.out_row + mm;
+  for (int i = 0; i < T::LI; ++i) vl[i] = panel_source<LC, T::BM, T::BK>((wave + i * T::kWaves) * 64 + lane, (uint32_t)l_ld);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if (mm + e >= A.cols) continue;
-        const float x = v[e] * (1.f / (kScaleX * kScaleP));
-        if (A.out_bf16) {
-          uint16_t *p = (uint16_t *)A.out + at + e;
-          *p = f32_bf16(A.update ? bf16_f32(*p) * A.decay - A.rate * x : x);
-        } else {
-          float *p = (float *)A.out + at + e;
-          *p = A.update ? *p * A.decay - A.rate * x : x;
+  for (int i = 0; i < T::RI; ++i) vr[i] = panel_source<RC, T::BN, T::BK>((wave + i * T::kWaves) * 64 + lane, (uint32_t)r_ld);
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)smem + wave * 1024;
+
+  // copy i of step t into stage `to`
+  auto copy = [&](int i, int4v bl, int4v br, int to) {
+    const uint32_t at = lds0 + to * T::kStageBytes;
+    if (i < T::LI) copy_to_lds(bl, at + i * (T::kWaves * 1024), vl[i]);
+    else copy_to_lds(br, at + T::BM * T::BK * 2 + (i - T::LI) * (T::kWaves * 1024), vr[i - T::LI]);
+  };
+  constexpr int kCopies = T::LI + T::RI;
+
+  float16v acc[T::FM][T::FN];
+#pragma unroll
+  for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+
+  half8 x[2][T::FM], y[2][T::FN];
+  auto fragments = [&](int stage, int ks, half8 *fx, half8 *fy) {
+    const char *p = smem + stage * T::kStageBytes;
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i) fx[i] = panel_read<LC, T::BM, T::BK>(p, wm + 32 * i, ks, lane);
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j) fy[j] = panel_read<RC, T::BN, T::BK>(p + T::BM * T::BK * 2, wn + 32 * j, ks, lane);
+  };
+
+  const int nk = (int)(A.k / T::BK);
+  constexpr int kSteps = T::BK / 16;
+#pragma unroll
+  for (int t = 0; t < T::S; ++t)
+    if (t < nk) {
+      const int4v bl = buffer_of(pl + t * sl, nl - t * sl), br = buffer_of(pr + t * sr, nr - t * sr);
+#pragma unroll
+      for (int i = 0; i < kCopies; ++i) copy(i, bl, br, t);
+    }
+  if (nk >= T::S) stage_wait<(T::S - 1) * kCopies>();
+  else stage_wait<0>();
+  fragments(0, 0, x[0], y[0]);
+  int stage = 0;
+  for (int t = 0; t < nk; ++t) {
+#pragma unroll
+    for (int ks = 0; ks < kSteps - 1; ++ks) {
+      // in this order: left alone, the compiler moves the reads behind the products
+      fragments(stage, ks + 1, x[(ks + 1) & 1], y[(ks + 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+        for (int i = 0; i < T::FM; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[ks & 1][i], y[ks & 1][j], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    const int next = stage + 1 == T::S ? 0 : stage + 1;
+    const bool refill = t + T::S < nk;
+    if (t + 1 < nk) {
+      // the next stage is whole, and nobody reads this one any more
+      if (t + T::S <= nk) stage_wait<(T::S - 2) * kCopies>();
+      else stage_wait<0>();
+      fragments(next, 0, x[0], y[0]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    const int64_t ol = (t + T::S) * sl, orr = (t + T::S) * sr;
+    const int4v bl = buffer_of(pl + ol, nl - ol), br = buffer_of(pr + orr, nr - orr);
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+      for (int i = 0; i < T::FM; ++i) {
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[1][i], y[1][j], acc[i][j], 0, 0, 0);
+        // the copies are spread over the products
+        constexpr int kEach = (kCopies + T::FM * T::FN - 1) / (T::FM * T::FN);
+        const int q = j * T::FM + i;
+        if (refill) {
+#pragma unroll
+          for (int c = q * kEach; c < (q + 1) * kEach && c < kCopies; ++c) copy(c, bl, br, stage);
         }
       }
+    __builtin_amdgcn_sched_barrier(0);
+    stage = next;
+  }
+  __syncthreads();   // the stages' LDS is the epilogue's now
+
+  // Each wave brings 32 rows (n) x TM of its part through LDS at a time, so
+  // that memory is written in whole runs of a row.
+  char *mine = smem + wave * (32 * (T::TM * 4 + 16));
+#pragma unroll
+  for (int j = 0; j < T::FN; ++j) {
+    const int64_t nb = n0 + wn + 32 * j, mb = m0 + wm;
+    if (OUT) {
+      constexpr int kStride = T::TM * 4 + 16;
+#pragma unroll
+      for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *(float4 *)(mine + (lane & 31) * kStride + (32 * i + 8 * q + 4 * (lane >> 5)) * 4) =
+              make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+      wave_lds_fence();
+      constexpr int kChunks = T::TM / 4;   // of a row
+#pragma unroll 4
+      for (int g = lane; g < 32 * kChunks; g += 64) {
+        const int row = g / kChunks, c = g % kChunks;
+        const float4 w = *(const float4 *)(mine + row * kStride + c * 16);
+        const float v[4] = {w.x, w.y, w.z, w.w};
+        const int64_t nn = nb + row, mm = mb + 4 * c;
+        if (nn >= A.rows || mm >= A.cols) continue;
+        const int64_t at = (A.b0 + lb) * A.out_batch + nn * A.out_row + mm;
+        constexpr float kUnit = 1.f / (kScaleX * kScaleP);
+        if (A.out_vec && mm + 4 <= A.cols) {
+          if (A.out_bf16) {
+            uint16_t *p = (uint16_t *)A.out + at;
+            float t4[4] = {0.f, 0.f, 0.f, 0.f};
+            if (A.update) {
+              const uint2 o = *(const uint2 *)p;
+              t4[0] = __uint_as_float(o.x << 16), t4[1] = __uint_as_float(o.x & 0xffff0000u);
+              t4[2] = __uint_as_float(o.y << 16), t4[3] = __uint_as_float(o.y & 0xffff0000u);
+            }
+            uint32_t b[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              b[e] = f32_bf16(A.update ? t4[e] * A.decay - A.rate * (v[e] * kUnit) : v[e] * kUnit);
+            *(uint2 *)p = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
+          } else {
+            float *p = (float *)A.out + at;
+            float4 o = *(const float4 *)p;
+            o.x = o.x * A.decay - A.rate * (v[0] * kUnit);
+            o.y = o.y * A.decay - A.rate * (v[1] * kUnit);
+            o.z = o.z * A.decay - A.rate * (v[2] * kUnit);
+            o.w = o.w * A.decay - A.rate * (v[3] * kUnit);
+            *(float4 *)p = o;
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (mm + e >= A.cols) continue;
+            const float o = v[e] * kUnit;
+            if (A.out_bf16) {
+              uint16_t *p = (uint16_t *)A.out + at + e;
+              *p = f32_bf16(A.update ? bf16_f32(*p) * A.decay - A.rate * o : o);
+            } else {
+              float *p = (float *)A.out + at + e;
+              *p = *p * A.decay - A.rate * o;
+            }
+          }
+        }
+      }
+      wave_lds_fence();
       continue;
     }
-    half4 h;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float x;
-      if (ROLE == kGram) x = v[e] * (1.f / kScaleX);
-      if (ROLE == kUpdate) x = v[e] * (1.f / kScaleP);
-      if (ROLE == kPoly) {
-        const float s = (float)A.l[lb * A.l_mat + nn * A.k + mm + e];
-        x = (A.b * (kScaleP / kScaleX)) * s + (A.c * (kScaleP / (kScaleX * kScaleX))) * v[e];
-        if (nn == mm + e) x += A.a * kScaleP;
-      }
-      h[e] = (_Float16)x;
-    }
+    constexpr int kStride = T::TM * 2 + 16;
+    const int64_t dn = A.m;   // elements of a row of D
     _Float16 *d = A.d + lb * A.m * A.n;
-    *(half4 *)(d + nn * A.m + mm) = h;
-    _Float16 *dt = ROLE == kUpdate ? A.dt + lb * A.m * A.n : d;
-    if (ROLE == kUpdate || m0 < n0) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) dt[(mm + e) * A.n + nn] = h[e];
+    for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = 32 * i + 8 * q + 4 * (lane >> 5);
+        const int64_t nn = nb + (lane & 31), mm = mb + r;   // and the next three
+        half4 h, s = {0, 0, 0, 0};
+        if (ROLE == kPoly && nn < A.n && mm < A.m) s = *(const half4 *)(A.l + lb * A.l_mat + nn * dn + mm);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float v = acc[i][j][4 * q + e];
+          float o = 0.f;
+          if (ROLE == kGram) o = v * (1.f / kScaleX);
+          if (ROLE == kUpdate) o = v * (1.f / kScaleP);
+          if (ROLE == kPoly) {
+            o = (A.b * (kScaleP / kScaleX)) * (float)s[e] + (A.c * (kScaleP / (kScaleX * kScaleX))) * v;
+            if (nn == mm + e) o += A.a * kScaleP;
+          }
+          h[e] = (_Float16)o;
+        }
+        *(half4 *)(mine + (lane & 31) * kStride + r * 2) = h;
+      }
+    wave_lds_fence();
+    constexpr int kChunks = T::TM / 8;
+#pragma unroll
+    for (int g = lane; g < 32 * kChunks; g += 64) {
+      const int row = g / kChunks, c = g % kChunks;
+      const half8 h = *(const half8 *)(mine + row * kStride + c * 16);
+      if (nb + row < A.n && mb + 8 * c < A.m) *(half8 *)(d + (nb + row) * dn + mb + 8 * c) = h;
     }
+    if (ROLE <= kPoly && ti < tj) {
+      // the mirror image: lane s of 16 gets column s of 4 rows at a time
+      const int s = lane & 15, oct = lane >> 4;
+#pragma unroll
+      for (int c = 0; c < T::TM / 16; ++c) {
+        union { short4v s[2]; half8 h; } u;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          u.s[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds_short4 *)(mine + (8 * oct + 4 * e + (s >> 2)) * kStride + (16 * c + 4 * (s & 3)) * 2));
+        const int64_t mm = mb + 16 * c + s, nn = nb + 8 * oct;
+        if (mm < A.m && nn < A.n) *(half8 *)(d + mm * dn + nn) = u.h;
+      }
+    }
+    wave_lds_fence();
   }
 }
 
