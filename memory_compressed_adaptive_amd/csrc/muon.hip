@@ -16,20 +16,39 @@ namespace {
 
 constexpr int64_t kMaxElems = int64_t(1) << 33;     // of one matrix: keeps every launch's grid in range
 constexpr int64_t kMaxSide = int64_t(1) << 21;      // 256 rows' bytes stay under 2^31
-constexpr int kMaxSteps = 64;
-constexpr int kNormParts = 256;                     // most partial sums of squares for one matrix
+constexpr int kNormParts = 2048;                    // most partial sums of squares for one matrix
 constexpr size_t kWorkspaceAim = size_t(512) << 20; // a batch is cut into runs of matrices of about this much workspace
 
 struct Coefficients { float v[kMaxSteps][3]; };
 
 int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
 
+// LDS that muon_small_kernel needs for n x m; 0 if it has no kernel for n.
+int64_t small_lds(int64_t n, int64_t m) {
+  const int64_t mp = round_up(m, 32);
+  switch ((n + 31) / 32) {
+    case 1: return SmallLds<1>::bytes(mp);
+    case 2: return SmallLds<2>::bytes(mp);
+    case 3: return SmallLds<3>::bytes(mp);
+    case 4: return SmallLds<4>::bytes(mp);
+    default: return 0;
+  }
+}
+
+bool fits_small(int64_t n, int64_t m) {
+  const int64_t bytes = small_lds(n, m);
+  return bytes > 0 && bytes <= 160 * 1024;
+}
+
 // How a batch of r x c matrices is cut and laid out in the workspace.
 struct Plan {
   int64_t r, c, n, m;       // n <= m: the wide orientation's sides
   bool tall;
+  bool small;               // a workgroup for each matrix, no workspace
   int64_t np, mp;           // padded
   int64_t chunk;            // matrices at a time
+  MuonRun run;              // how waves go over the stored matrix
+  uint32_t runs;
   int nparts;
   size_t x_bytes, a_bytes, part_bytes, bytes;
 
@@ -39,13 +58,18 @@ struct Plan {
     m = std::max(r, c);
     np = round_up(n, 64);
     mp = round_up(m, 64);
-    nparts = (int)std::min<int64_t>(kNormParts, (r * ((c + 255) / 256) + 15) / 16);
+    run.lanes = 64;
+    while (run.lanes > 1 && 2 * run.lanes >= c) run.lanes /= 2;   // 4 columns to a lane
+    run.segs = (uint32_t)((c + 4 * run.lanes - 1) / (4 * run.lanes));
+    runs = (uint32_t)((r + 64 / run.lanes - 1) / (64 / run.lanes)) * run.segs;
+    nparts = (int)std::min<int64_t>(kNormParts, (runs + 15) / 16);   // four runs to a wave
     const size_t one = 2 * 2 * (size_t)(np * mp) + 2 * 2 * (size_t)(np * np) + 8 * (size_t)nparts;
     chunk = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(batch, 65535), (int64_t)(kWorkspaceAim / one)));
     x_bytes = (size_t)round_up(2 * chunk * np * mp, 256);
     a_bytes = (size_t)round_up(2 * chunk * np * np, 256);
     part_bytes = (size_t)round_up(8 * chunk * nparts, 256);
-    bytes = 2 * x_bytes + 2 * a_bytes + part_bytes;
+    small = fits_small(n, m);
+    bytes = small ? 256 : 2 * x_bytes + 2 * a_bytes + part_bytes;
   }
 };
 
@@ -135,15 +159,40 @@ void product(const MuonProduct &a, int64_t chunk, hipStream_t s) {
   }
 }
 
-struct MuonOutput {
-  void *out;
-  int bf16, update, vec;
-  int64_t row, batch;
-  double decay, rate;
-};
+template <int NB, int MOM>
+hipError_t launch_small(int64_t batch, const MuonInput &in, const MuonRun &r, MuonSmall small, const MuonTarget &o,
+                        size_t lds, hipStream_t s) {
+  const hipError_t e = hipFuncSetAttribute((const void *)muon_small_kernel<NB, MOM>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                           160 * 1024);
+  if (e != hipSuccess) return e;
+  for (small.b0 = 0; small.b0 < batch; small.b0 += 1 << 22)   // 2^31 threads in a launch
+    hipLaunchKernelGGL((muon_small_kernel<NB, MOM>), dim3((unsigned)std::min<int64_t>(batch - small.b0, 1 << 22)), dim3(512),
+                       lds, s, in, r, small, o);
+  return hipGetLastError();
+}
 
 template <int MOM>
-hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonOutput &o, int steps, const Coefficients &k,
+hipError_t run_small(const Plan &p, int64_t batch, const MuonInput &in, const MuonTarget &o, int steps, const Coefficients &k,
+                     float eps, hipStream_t s) {
+  MuonSmall small = {};
+  for (int t = 0; t < steps; ++t)
+    for (int e = 0; e < 3; ++e) small.k[t][e] = k.v[t][e];
+  small.steps = steps;
+  small.tall = p.tall;
+  small.mp = (int)round_up(p.m, 32);
+  small.eps = eps;
+  small.runs = p.runs;
+  const size_t lds = (size_t)small_lds(p.n, p.m);
+  switch ((p.n + 31) / 32) {
+    case 1: return launch_small<1, MOM>(batch, in, p.run, small, o, lds, s);
+    case 2: return launch_small<2, MOM>(batch, in, p.run, small, o, lds, s);
+    case 3: return launch_small<3, MOM>(batch, in, p.run, small, o, lds, s);
+    default: return launch_small<4, MOM>(batch, in, p.run, small, o, lds, s);
+  }
+}
+
+template <int MOM>
+hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonTarget &o, int steps, const Coefficients &k,
                float eps, void *workspace, hipStream_t s) {
   char *w = (char *)workspace;
   _Float16 *x0 = (_Float16 *)w, *x1 = (_Float16 *)(w + p.x_bytes);
@@ -152,15 +201,17 @@ hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonOutp
   const int64_t nm = p.np * p.mp, nn = p.np * p.np;
   for (int64_t b0 = 0; b0 < batch; b0 += p.chunk) {
     const int64_t cb = std::min(p.chunk, batch - b0);
-    hipLaunchKernelGGL((muon_norm_kernel<MOM>), dim3((unsigned)p.nparts, (unsigned)cb), dim3(256), 0, s, in, b0, part,
-                       p.nparts);
+    hipLaunchKernelGGL((muon_norm_kernel<MOM>), dim3((unsigned)p.nparts, (unsigned)cb), dim3(256), 0, s, in,
+                       p.run, p.runs, b0, part, p.nparts);
     const int64_t sp = p.tall ? p.np : p.mp, tp = p.tall ? p.mp : p.np;
-    const dim3 lg((unsigned)((sp + kLoadCols - 1) / kLoadCols), (unsigned)((tp + kLoadRows - 1) / kLoadRows), (unsigned)cb);
+    const dim3 lg((unsigned)((sp + 4 * p.run.lanes - 1) / (4 * p.run.lanes)), (unsigned)((tp + kLoadRows - 1) / kLoadRows), (unsigned)cb);
     _Float16 *x = x0, *nx = x1;
     if (p.tall)
-      hipLaunchKernelGGL((muon_load_kernel<MOM, true>), lg, dim3(256), 0, s, in, b0, part, p.nparts, eps, x, sp, tp);
+      hipLaunchKernelGGL((muon_load_kernel<MOM, true>), lg, dim3(256), 0, s, in, p.run, b0, part, p.nparts, eps, x,
+                         sp, tp);
     else
-      hipLaunchKernelGGL((muon_load_kernel<MOM, false>), lg, dim3(256), 0, s, in, b0, part, p.nparts, eps, x, sp, tp);
+      hipLaunchKernelGGL((muon_load_kernel<MOM, false>), lg, dim3(256), 0, s, in, p.run, b0, part, p.nparts, eps, x,
+                         sp, tp);
     for (int t = 0; t < steps; ++t) {
       MuonProduct a = {};
       a.a = k.v[t][0], a.b = k.v[t][1], a.c = k.v[t][2];
@@ -183,9 +234,7 @@ hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonOutp
         std::swap(x, nx);
         continue;
       }
-      a.out = o.out, a.out_bf16 = o.bf16, a.update = o.update, a.out_vec = o.vec;
-      a.out_row = o.row, a.out_batch = o.batch, a.rows = p.r, a.cols = p.c;
-      a.decay = (float)o.decay, a.rate = (float)o.rate;
+      a.out = o;
       a.b0 = b0;
       if (p.tall) {   // the fastest index of `out` is P's
         std::swap(a.l, a.r);
@@ -238,6 +287,12 @@ int device_of(hipStream_t stream, int *dev) {
   return hipStreamGetDevice(stream, dev) == hipSuccess ? MA_OK : MA_EHIP;
 }
 
+MuonTarget target(void *params, int type, int64_t row, int64_t bat, int64_t batch, int64_t rows, int64_t cols, double lr,
+                  double wd, double scale) {
+  return {params, type == MA_TYPE_BF16, 1, aligned_runs(params, type == MA_TYPE_BF16 ? 2 : 4, row, bat, rows, batch), row, bat,
+          rows, cols, (float)(1.0 - lr * wd), (float)(lr * scale)};
+}
+
 Coefficients copy(const float *k, int steps) {
   Coefficients c = {};
   for (int t = 0; t < steps; ++t)
@@ -246,13 +301,16 @@ Coefficients copy(const float *k, int steps) {
 }
 
 template <int MOM>
-int enqueue(const char *who, int64_t batch, const MuonInput &in, const MuonOutput &o, int steps, const float *coefficients,
+int enqueue(const char *who, int64_t batch, const MuonInput &in, const MuonTarget &o, int steps, const float *coefficients,
             float eps, void *workspace, hipStream_t stream) {
   int dev = 0;
   if (device_of(stream, &dev) != MA_OK) return fail(MA_EHIP, "%s: the stream has no device", who);
   DeviceGuard guard(dev);
   if (!guard.ok) return fail(MA_EHIP, "%s: device %d cannot be made current", who, dev);
-  const hipError_t e = run<MOM>(Plan(batch, in.r, in.c), batch, in, o, steps, copy(coefficients, steps), eps, workspace, stream);
+  const Plan p(batch, in.r, in.c);
+  const Coefficients k = copy(coefficients, steps);
+  const hipError_t e = p.small ? run_small<MOM>(p, batch, in, o, steps, k, eps, stream)
+                                            : run<MOM>(p, batch, in, o, steps, k, eps, workspace, stream);
   if (e != hipSuccess) return fail(MA_EHIP, "%s: launch failed: %s", who, hipGetErrorString(e));
   return MA_OK;
 }
@@ -300,7 +358,7 @@ int ma_orthogonalize(int64_t batch, int64_t rows, int64_t cols, const void *x, i
   in.x = x, in.x_bf16 = x_type == MA_TYPE_BF16, in.x_row = x_row, in.x_batch = x_batch;
   in.r = rows, in.c = cols;
   in.vec = aligned_runs(x, elem, x_row, x_batch, rows, batch);
-  const MuonOutput o = {out, 1, 0, aligned_runs(out, 2, out_row, out_batch, rows, batch), out_row, out_batch, 1.0, 0.0};
+  const MuonTarget o = {out, 1, 0, aligned_runs(out, 2, out_row, out_batch, rows, batch), out_row, out_batch, rows, cols, 1.f, 0.f};
   return enqueue<kMomNone>(who, batch, in, o, steps, coefficients, eps, workspace, stream);
 }
 
@@ -321,7 +379,7 @@ int ma_muon_step(int64_t batch, int64_t rows, int64_t cols, void *params, int p_
   in.mom = momentum, in.beta = beta, in.nesterov = nesterov != 0;
   in.r = rows, in.c = cols;
   in.vec = aligned_runs(grads, 2, g_row, g_batch, rows, batch) && ((uintptr_t)momentum & 15u) == 0 && cols % 4 == 0;
-  const MuonOutput o = {params, p_type == MA_TYPE_BF16, 1, aligned_runs(params, p_type == MA_TYPE_BF16 ? 2 : 4, p_row, p_batch, rows, batch), p_row, p_batch, 1.0 - lr * wd, lr * scale};
+  const MuonTarget o = target(params, p_type, p_row, p_batch, batch, rows, cols, lr, wd, scale);
   return enqueue<kMom32>(who, batch, in, o, steps, coefficients, eps, workspace, stream);
 }
 
@@ -342,7 +400,7 @@ int ma_muon8_step(int64_t batch, int64_t rows, int64_t cols, void *params, int p
   in.codes = codes, in.scales = scales, in.beta = beta, in.nesterov = nesterov != 0;
   in.r = rows, in.c = cols;
   in.vec = aligned_runs(grads, 2, g_row, g_batch, rows, batch) && ((uintptr_t)codes & 3u) == 0 && cols % 4 == 0;
-  const MuonOutput o = {params, p_type == MA_TYPE_BF16, 1, aligned_runs(params, p_type == MA_TYPE_BF16 ? 2 : 4, p_row, p_batch, rows, batch), p_row, p_batch, 1.0 - lr * wd, lr * scale};
+  const MuonTarget o = target(params, p_type, p_row, p_batch, batch, rows, cols, lr, wd, scale);
   return enqueue<kMom8>(who, batch, in, o, steps, coefficients, eps, workspace, stream);
 }
 

@@ -61,101 +61,184 @@ __device__ __forceinline__ uint16_t f32_bf16(float f) {
   return (uint16_t)((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
 }
 
-// Four consecutive inputs of row i (columns j..j+3; zeros past the last).
-__device__ __forceinline__ void load4_in(const MuonInput &I, int64_t b, int64_t i, int64_t j, float v[4]) {
-  const int64_t at = b * I.x_batch + i * I.x_row + j;
-  if (I.x_bf16) {
-    const uint16_t *p = (const uint16_t *)I.x + at;
-    if (I.vec && j + 4 <= I.c) {
-      const uint2 w = *(const uint2 *)p;
-      v[0] = __uint_as_float(w.x << 16);
-      v[1] = __uint_as_float(w.x & 0xffff0000u);
-      v[2] = __uint_as_float(w.y << 16);
-      v[3] = __uint_as_float(w.y & 0xffff0000u);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = j + e < I.c ? bf16_f32(p[e]) : 0.f;
-    }
-  } else {
-    const float *p = (const float *)I.x + at;
-    if (I.vec && j + 4 <= I.c) {
-      const float4 w = *(const float4 *)p;
-      v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = j + e < I.c ? p[e] : 0.f;
-    }
-  }
-}
-
-// The new momentum and the matrix to orthogonalise at row i, columns j..j+3
-// (zeros past the last column).  m64: the 8-bit form's momentum, which decides
-// its codes.  It is formed in 64 bits: a code lies where a product and a sum
-// would each have moved it in fp32 about once in 1e5 elements, and what is
-// written is then what the formula gives, on any machine; the pass is bound by
-// memory either way.
-template <int MOM>
-__device__ __forceinline__ void muon_elems(const MuonInput &I, int64_t b, int64_t i, int64_t j, float u[4],
-                                           float m32[4], double m64[4]) {
+// What memory holds of four consecutive elements: row i, columns j..j+3 (zeros
+// outside the matrix).  Reading and using them are apart, so that a kernel can
+// have several reads on their way.
+struct MuonRaw {
   float g[4];
-  load4_in(I, b, i, j, g);
-  if (MOM == kMomNone) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) u[e] = g[e];
-    return;
-  }
-  const float b32 = (float)I.beta, o32 = (float)(1.0 - I.beta);
-  const int64_t at = (b * I.r + i) * I.c + j;
-  if (MOM == kMom32) {
-    float mo[4];
-    if (I.vec && j + 4 <= I.c) {
-      const float4 w = *(const float4 *)(I.mom + at);
-      mo[0] = w.x, mo[1] = w.y, mo[2] = w.z, mo[3] = w.w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) mo[e] = j + e < I.c ? I.mom[at + e] : 0.f;
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) m32[e] = mo[e] * b32 + g[e] * o32;
-  } else {
-    const double s = (double)I.scales[(b * I.r + i) * ((I.c + kMomentumBlock - 1) / kMomentumBlock) + j / kMomentumBlock];
-    uint32_t w = 0;
-    if (I.vec && j + 4 <= I.c) {
-      w = *(const uint32_t *)(I.codes + at);
+  float mo[4];    // kMom32
+  uint32_t w;     // kMom8: four codes
+  float s;        // and their scale
+};
+
+template <int MOM>
+__device__ __forceinline__ MuonRaw muon_raw(const MuonInput &I, int64_t b, int64_t i, int64_t j) {
+  MuonRaw R = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}, 0u, 0.f};
+  if (i >= I.r || j >= I.c) return R;
+  const bool run = I.vec && j + 4 <= I.c;
+  const int64_t at = b * I.x_batch + i * I.x_row + j;
+  if (MOM != kMomNone || I.x_bf16) {
+    const uint16_t *p = (const uint16_t *)I.x + at;
+    if (run) {
+      const uint2 w = *(const uint2 *)p;
+      R.g[0] = __uint_as_float(w.x << 16);
+      R.g[1] = __uint_as_float(w.x & 0xffff0000u);
+      R.g[2] = __uint_as_float(w.y << 16);
+      R.g[3] = __uint_as_float(w.y & 0xffff0000u);
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (j + e < I.c) w |= (uint32_t)(uint8_t)I.codes[at + e] << (8 * e);
+        if (j + e < I.c) R.g[e] = bf16_f32(p[e]);
     }
+  } else {
+    const float *p = (const float *)I.x + at;
+    if (run) {
+      const float4 w = *(const float4 *)p;
+      R.g[0] = w.x, R.g[1] = w.y, R.g[2] = w.z, R.g[3] = w.w;
+    } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      // a block whose scale is NaN holds NaN; columns past the last hold 0
-      m64[e] = j + e < I.c ? I.beta * ((double)(int8_t)(w >> (8 * e)) * s) + (1.0 - I.beta) * (double)g[e] : 0.0;
-      m32[e] = (float)m64[e];
+      for (int e = 0; e < 4; ++e)
+        if (j + e < I.c) R.g[e] = p[e];
     }
   }
+  if (MOM == kMomNone) return R;
+  const int64_t row = b * I.r + i, mat = row * I.c + j;
+  if (MOM == kMom32) {
+    if (run) {
+      const float4 w = *(const float4 *)(I.mom + mat);
+      R.mo[0] = w.x, R.mo[1] = w.y, R.mo[2] = w.z, R.mo[3] = w.w;
+    } else {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) u[e] = I.nesterov ? m32[e] * b32 + g[e] * o32 : m32[e];
+      for (int e = 0; e < 4; ++e)
+        if (j + e < I.c) R.mo[e] = I.mom[mat + e];
+    }
+  } else {
+    R.s = I.scales[row * ((I.c + kMomentumBlock - 1) / kMomentumBlock) + j / kMomentumBlock];
+    if (run) {
+      R.w = *(const uint32_t *)(I.codes + mat);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j + e < I.c) R.w |= (uint32_t)(uint8_t)I.codes[mat + e] << (8 * e);
+    }
+  }
+  return R;
 }
+
+// The matrix to orthogonalise (u) and the new momentum (m32, m64) of those four
+// elements; 0 past the last column.  m64: the 8-bit form's momentum, which
+// decides its codes.  It is formed in 64 bits: a code lies where a product and
+// a sum would each have moved it in fp32 about once in 1e5 elements, and what
+// is written is then what the formula gives, on any machine; the pass is bound
+// by memory either way.
+template <int MOM>
+__device__ __forceinline__ void muon_elems(const MuonInput &I, const MuonRaw &R, int64_t j, float u[4], float m32[4],
+                                           double m64[4]) {
+  if (MOM == kMomNone) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[e] = R.g[e];
+    return;
+  }
+  const float b32 = (float)I.beta, o32 = (float)(1.0 - I.beta);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (MOM == kMom32) {
+      m32[e] = R.mo[e] * b32 + R.g[e] * o32;
+    } else {
+      // a block whose scale is NaN holds NaN; columns past the last hold 0
+      m64[e] = j + e < I.c ? I.beta * ((double)(int8_t)(R.w >> (8 * e)) * (double)R.s) + (1.0 - I.beta) * (double)R.g[e] : 0.0;
+      m32[e] = (float)m64[e];
+    }
+    u[e] = I.nesterov ? m32[e] * b32 + R.g[e] * o32 : m32[e];
+  }
+}
+
+// Writes the new momentum of row i, columns j..j+3 (nothing outside the
+// matrix).  kMom8: `lanes` consecutive lanes hold a block of 256 (or the row's
+// short last one, or the whole of a shorter row).  All lanes of a wave call it.
+template <int MOM>
+__device__ __forceinline__ void muon_store_momentum(const MuonInput &I, int64_t b, int64_t i, int64_t j, int lanes,
+                                                    const float m32[4], const double m64[4]) {
+  if (MOM == kMomNone) return;
+  const bool in = i < I.r && j < I.c, run = I.vec && j + 4 <= I.c;
+  const int64_t row = b * I.r + i, mat = row * I.c + j;
+  if (MOM == kMom32) {
+    if (!in) return;
+    if (run) {
+      *(float4 *)(I.mom + mat) = make_float4(m32[0], m32[1], m32[2], m32[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j + e < I.c) I.mom[mat + e] = m32[e];
+    }
+    return;
+  }
+  // the largest magnitude is 127 steps; a block with a non-finite value gets
+  // the scale NaN and codes 0, and reads back as NaN.  A NaN counts as an
+  // infinity here (fmax would drop it).
+  double top = 0.0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) top = fmax(top, m64[e] == m64[e] ? fabs(m64[e]) : (double)__builtin_inff());
+  for (int o = lanes >> 1; o >= 1; o >>= 1) top = fmax(top, __shfl_xor(top, o, 64));
+  const bool bad = !(top < (double)__builtin_inff());
+  const float step = bad ? __builtin_nanf("") : (float)(top / 127.0);
+  const double inv = step > 0.f ? 1.0 / (double)step : 0.0;
+  uint32_t w = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const double q8 = bad ? 0.0 : fmin(fmax(rint(m64[e] * inv), -127.0), 127.0);
+    w |= ((uint32_t)(int32_t)q8 & 0xffu) << (8 * e);
+  }
+  if (!in) return;
+  if (run) {
+    *(uint32_t *)(I.codes + mat) = w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (j + e < I.c) I.codes[mat + e] = (int8_t)(w >> (8 * e));
+  }
+  if (j % kMomentumBlock == 0) I.scales[row * ((I.c + kMomentumBlock - 1) / kMomentumBlock) + j / kMomentumBlock] = step;
+}
+
+// A wave takes `lanes` lanes to a row (4 columns each; 64, or fewer for narrow
+// matrices) and so 64 / lanes rows at once: run q of them, this lane's element.
+struct MuonRun {
+  uint32_t segs;   // runs along a row: ceil(c / (4 lanes))
+  int lanes;
+  __device__ __forceinline__ void at(uint32_t q, int lane, int64_t &i, int64_t &j) const {
+    const uint32_t rows = q / segs, seg = q - rows * segs;
+    i = (int64_t)rows * (64 / lanes) + lane / lanes;
+    j = ((int64_t)seg * lanes + (lane & (lanes - 1))) * 4;
+  }
+};
 
 // ------------------------------------------------------------------ |U|_F
 // Sum of squares of U in 64 bits (a gradient's squares can pass either end of
-// fp32's range): block p of matrix b writes part[b][p].  One wave takes runs of
-// 256 columns of a row; no atomics, so results do not depend on timing.
+// fp32's range): block p of matrix b writes part[b][p].  No atomics, so results
+// do not depend on timing.  Four reads of a lane are on their way at a time.
 template <int MOM>
-__global__ __launch_bounds__(256) void muon_norm_kernel(MuonInput I, int64_t b0, double *part, int nparts) {
+__global__ __launch_bounds__(256) void muon_norm_kernel(MuonInput I, MuonRun run, uint32_t runs, int64_t b0, double *part,
+                                                        int nparts) {
   const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6);
   const int64_t lb = blockIdx.y, b = b0 + lb;
-  const int64_t segs = (I.c + 255) / 256, total = I.r * segs;
+  const uint32_t stride = (uint32_t)nparts * 4;
   double sum = 0.0;
-  for (int64_t q = (int64_t)blockIdx.x * 4 + wave; q < total; q += (int64_t)nparts * 4) {
-    const int64_t i = q / segs, j = (q - i * segs) * 256 + 4 * lane;
-    if (j < I.c) {
+  for (uint32_t q0 = blockIdx.x * 4 + wave; q0 < runs; q0 += 4 * stride) {
+    MuonRaw R[4];
+    int64_t j[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      int64_t i;
+      run.at(q0 + e * stride, lane, i, j[e]);   // past the last run: rows past the last, zeros
+      R[e] = muon_raw<MOM>(I, b, i, j[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
       float u[4], m32[4];
       double m64[4];
-      muon_elems<MOM>(I, b, i, j, u, m32, m64);
+      muon_elems<MOM>(I, R[e], j[e], u, m32, m64);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) sum += (double)u[e] * (double)u[e];
+      for (int f = 0; f < 4; ++f) sum += (double)u[f] * (double)u[f];
     }
   }
 #pragma unroll
@@ -166,103 +249,122 @@ __global__ __launch_bounds__(256) void muon_norm_kernel(MuonInput I, int64_t b0,
   if (threadIdx.x == 0) part[lb * nparts + blockIdx.x] = (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// 2^14 / max(|U|_F, eps), by every thread of a 256-thread block
-__device__ __forceinline__ double block_scale(const double *part, int nparts, float eps, double *s4) {
-  const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6);
-  double sum = 0.0;
-  for (int p = (int)threadIdx.x; p < nparts; p += 256) sum += part[p];
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
-  if (lane == 0) s4[wave] = sum;
-  __syncthreads();
-  const double norm = sqrt((s4[0] + s4[1]) + (s4[2] + s4[3]));
+// 2^14 / max(|U|_F, eps) from the sum of squares
+__device__ __forceinline__ double muon_scale(double squares, float eps) {
+  const double norm = sqrt(squares);
   return (double)kScaleX / (norm >= (double)eps || norm != norm ? norm : (double)eps);
 }
 
 // ------------------------------------------------------------------ momentum, X0
 // Writes the new momentum, and X0 in its wide orientation with zeros in the
 // padding: as the matrix is stored, or transposed if that is tall.  A block of
-// 256 threads takes 64 rows x 256 columns of the stored matrix: 4 columns to a
-// lane, so that a wave holds the 256 elements of an 8-bit block.  sp, tp: the
-// stored orientation's padded columns and rows.
-constexpr int kLoadRows = 64, kLoadCols = 256;
+// 256 threads takes 64 rows x 4 * run.lanes columns of the stored matrix.  sp,
+// tp: the stored orientation's padded columns and rows.
+constexpr int kLoadRows = 64;
 
 template <int MOM, bool TALL>
-__global__ __launch_bounds__(256) void muon_load_kernel(MuonInput I, int64_t b0, const double *part, int nparts,
+__global__ __launch_bounds__(256) void muon_load_kernel(MuonInput I, MuonRun run, int64_t b0, const double *part, int nparts,
                                                         float eps, _Float16 *X, int64_t sp, int64_t tp) {
   __shared__ double s4[4];
-  __shared__ _Float16 tile[TALL ? kLoadRows : 1][kLoadCols + 4];
+  __shared__ _Float16 tile[TALL ? kLoadRows : 1][256 + 4];
   const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6);
   const int64_t lb = blockIdx.z, b = b0 + lb;
-  const double scale = block_scale(part + lb * nparts, nparts, eps, s4);
-  const int64_t i0 = (int64_t)blockIdx.y * kLoadRows, j0 = (int64_t)blockIdx.x * kLoadCols, j = j0 + 4 * lane;
+  const int64_t i0 = (int64_t)blockIdx.y * kLoadRows, j0 = (int64_t)blockIdx.x * (4 * run.lanes);
+  const int col = 4 * (lane & (run.lanes - 1)), rows = 64 / run.lanes;
+  const int64_t j = j0 + col;
+  double sum = 0.0;
+  for (int p = (int)threadIdx.x; p < nparts; p += 256) sum += part[lb * nparts + p];
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
+  if (lane == 0) s4[wave] = sum;
+  __syncthreads();
+  const double scale = muon_scale((s4[0] + s4[1]) + (s4[2] + s4[3]), eps);
   X += lb * sp * tp;
-  for (int q = wave; q < kLoadRows; q += 4) {
-    const int64_t i = i0 + q;
-    half4 h = {0, 0, 0, 0};
-    if (i < I.r) {   // uniform in the wave
+  for (int q0 = wave * rows; q0 < kLoadRows; q0 += 16 * rows) {
+    MuonRaw R[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int q = q0 + e * 4 * rows + lane / run.lanes;
+      R[e] = muon_raw<MOM>(I, b, q < kLoadRows ? i0 + q : I.r, j);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (q0 + e * 4 * rows >= kLoadRows) break;
+      const int q = q0 + e * 4 * rows + lane / run.lanes;
+      const int64_t i = i0 + q;
       float u[4], m32[4];
       double m64[4] = {0, 0, 0, 0};
-      if (j < I.c) {
-        muon_elems<MOM>(I, b, i, j, u, m32, m64);
+      muon_elems<MOM>(I, R[e], j, u, m32, m64);
+      half4 h;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) h[e] = j + e < I.c ? (_Float16)(float)((double)u[e] * scale) : (_Float16)0.f;
-      }
-      const int64_t at = (b * I.r + i) * I.c + j;
-      if (MOM == kMom32 && j < I.c) {
-        if (I.vec && j + 4 <= I.c) {
-          *(float4 *)(I.mom + at) = make_float4(m32[0], m32[1], m32[2], m32[3]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (j + e < I.c) I.mom[at + e] = m32[e];
-        }
-      }
-      if (MOM == kMom8) {
-        // the largest magnitude is 127 steps; a block with a non-finite value
-        // gets the scale NaN and codes 0, and reads back as NaN
-        double top = 0.0;
-        bool bad = false;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          bad |= !(fabs(m64[e]) < __builtin_inf());
-          top = fmax(top, fabs(m64[e]));
-        }
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) top = fmax(top, __shfl_xor(top, o, 64));
-        bad = __any(bad);
-        const float step = bad ? __builtin_nanf("") : (float)(top / 127.0);
-        const double inv = step > 0.f ? 1.0 / (double)step : 0.0;
-        uint32_t w = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const double q8 = bad ? 0.0 : fmin(fmax(rint(m64[e] * inv), -127.0), 127.0);
-          w |= ((uint32_t)(int32_t)q8 & 0xffu) << (8 * e);
-        }
-        if (j < I.c) {
-          if (I.vec && j + 4 <= I.c) {
-            *(uint32_t *)(I.codes + at) = w;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (j + e < I.c) I.codes[at + e] = (int8_t)(w >> (8 * e));
-          }
-        }
-        if (lane == 0 && j0 < I.c) I.scales[(b * I.r + i) * ((I.c + 255) / 256) + j0 / 256] = step;
-      }
+      for (int f = 0; f < 4; ++f) h[f] = i < I.r && j + f < I.c ? (_Float16)(float)((double)u[f] * scale) : (_Float16)0.f;
+      muon_store_momentum<MOM>(I, b, i, j, run.lanes, m32, m64);
+      if (TALL) *(half4 *)&tile[q][col] = h;
+      else if (j < sp && i < tp) *(half4 *)(X + i * sp + j) = h;
     }
-    if (TALL) *(half4 *)&tile[q][4 * lane] = h;
-    else if (j < sp && i < tp) *(half4 *)(X + i * sp + j) = h;
   }
   if (!TALL) return;
   __syncthreads();
   // transposed: 8 consecutive rows of a column to a lane, 8 lanes to a column
   const int rg = (int)(threadIdx.x & 7u);
-  for (int cc = (int)(threadIdx.x >> 3); cc < kLoadCols; cc += 32) {
+  for (int cc = (int)(threadIdx.x >> 3); cc < 4 * run.lanes; cc += 32) {
     half8 h;
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[e] = tile[8 * rg + e][cc];
     if (j0 + cc < sp && i0 + 8 * rg < tp) *(half8 *)(X + (j0 + cc) * tp + i0 + 8 * rg) = h;
+  }
+}
+
+// Where the orthogonalised matrices go: rows x cols elements each.
+struct MuonTarget {
+  void *out;
+  int bf16, update;     // update: theta <- theta * decay - rate * x; otherwise (bf16) x itself
+  int vec;              // runs of 4 elements are aligned
+  int64_t row, batch, rows, cols;
+  float decay, rate;
+};
+
+// Four consecutive sums of the last product, v, to row i, columns j..j+3 of
+// matrix b (nothing outside it).
+__device__ __forceinline__ void write_out(const MuonTarget &T, int64_t b, int64_t i, int64_t j, const float v[4]) {
+  if (i >= T.rows || j >= T.cols) return;
+  const int64_t at = b * T.batch + i * T.row + j;
+  constexpr float kUnit = 1.f / (kScaleX * kScaleP);
+  if (T.vec && j + 4 <= T.cols) {
+    if (T.bf16) {
+      uint16_t *p = (uint16_t *)T.out + at;
+      float old[4] = {0.f, 0.f, 0.f, 0.f};
+      if (T.update) {
+        const uint2 w = *(const uint2 *)p;
+        old[0] = __uint_as_float(w.x << 16), old[1] = __uint_as_float(w.x & 0xffff0000u);
+        old[2] = __uint_as_float(w.y << 16), old[3] = __uint_as_float(w.y & 0xffff0000u);
+      }
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = f32_bf16(T.update ? old[e] * T.decay - T.rate * (v[e] * kUnit) : v[e] * kUnit);
+      *(uint2 *)p = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+    } else {
+      float *p = (float *)T.out + at;
+      float4 w = *(const float4 *)p;
+      w.x = w.x * T.decay - T.rate * (v[0] * kUnit);
+      w.y = w.y * T.decay - T.rate * (v[1] * kUnit);
+      w.z = w.z * T.decay - T.rate * (v[2] * kUnit);
+      w.w = w.w * T.decay - T.rate * (v[3] * kUnit);
+      *(float4 *)p = w;
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (j + e >= T.cols) continue;
+    const float x = v[e] * kUnit;
+    if (T.bf16) {
+      uint16_t *p = (uint16_t *)T.out + at + e;
+      *p = f32_bf16(T.update ? bf16_f32(*p) * T.decay - T.rate * x : x);
+    } else {
+      float *p = (float *)T.out + at + e;
+      *p = *p * T.decay - T.rate * x;
+    }
   }
 }
 
@@ -285,12 +387,7 @@ struct MuonProduct {
   int64_t m, n;
   int tiles_m, tiles_n, tiles;   // of one matrix
   float a, b, c;
-  // kOut: element (n, m) goes to out[b][n][m], rows x cols of them
-  void *out;
-  int out_bf16, update;     // update: theta <- theta * decay - rate * x
-  int out_vec;              // runs of 4 elements are aligned
-  int64_t out_row, out_batch, rows, cols;
-  float decay, rate;
+  MuonTarget out;           // kOut: element (n, m) of matrix b0 + i goes to its row n, column m
   int64_t b0;
 };
 
@@ -349,7 +446,7 @@ __device__ __forceinline__ int4v buffer_of(const char *p, int64_t bytes) {
 // LDS read; here the waits are the kernel's own (stage_wait).
 __device__ __forceinline__ void copy_to_lds(int4v p, uint32_t lds, uint32_t voff) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :: "s"(lds), "v"(voff), "s"(p) : "memory", "m0");
+               :: "s"(lds), "v"(voff), "s"(p) : "memory");   // nothing else here uses m0
 }
 
 // This wave's copies are done but for the last N, and so are its LDS reads;
@@ -572,46 +669,7 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
         const float4 w = *(const float4 *)(mine + row * kStride + c * 16);
         const float v[4] = {w.x, w.y, w.z, w.w};
         const int64_t nn = nb + row, mm = mb + 4 * c;
-        if (nn >= A.rows || mm >= A.cols) continue;
-        const int64_t at = (A.b0 + lb) * A.out_batch + nn * A.out_row + mm;
-        constexpr float kUnit = 1.f / (kScaleX * kScaleP);
-        if (A.out_vec && mm + 4 <= A.cols) {
-          if (A.out_bf16) {
-            uint16_t *p = (uint16_t *)A.out + at;
-            float t4[4] = {0.f, 0.f, 0.f, 0.f};
-            if (A.update) {
-              const uint2 o = *(const uint2 *)p;
-              t4[0] = __uint_as_float(o.x << 16), t4[1] = __uint_as_float(o.x & 0xffff0000u);
-              t4[2] = __uint_as_float(o.y << 16), t4[3] = __uint_as_float(o.y & 0xffff0000u);
-            }
-            uint32_t b[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              b[e] = f32_bf16(A.update ? t4[e] * A.decay - A.rate * (v[e] * kUnit) : v[e] * kUnit);
-            *(uint2 *)p = make_uint2(b[0] | b[1] << 16, b[2] | b[3] << 16);
-          } else {
-            float *p = (float *)A.out + at;
-            float4 o = *(const float4 *)p;
-            o.x = o.x * A.decay - A.rate * (v[0] * kUnit);
-            o.y = o.y * A.decay - A.rate * (v[1] * kUnit);
-            o.z = o.z * A.decay - A.rate * (v[2] * kUnit);
-            o.w = o.w * A.decay - A.rate * (v[3] * kUnit);
-            *(float4 *)p = o;
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (mm + e >= A.cols) continue;
-            const float o = v[e] * kUnit;
-            if (A.out_bf16) {
-              uint16_t *p = (uint16_t *)A.out + at + e;
-              *p = f32_bf16(A.update ? bf16_f32(*p) * A.decay - A.rate * o : o);
-            } else {
-              float *p = (float *)A.out + at + e;
-              *p = *p * A.decay - A.rate * o;
-            }
-          }
-        }
+        write_out(A.out, A.b0 + lb, nn, mm, v);
       }
       wave_lds_fence();
       continue;
@@ -664,6 +722,259 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
       }
     }
     wave_lds_fence();
+  }
+}
+
+// ------------------------------------------------------------------ a whole matrix in one workgroup
+// Matrices whose X, A and P fit a CU's LDS take one launch: momentum, norm, all
+// steps and the result, one workgroup of 8 waves for each matrix.  What bounds
+// it is latency: a step is three short products with a barrier after each.  The
+// other way is 2 + 3 steps launches, of at least 3 us each.
+//
+// NB = ceil(n / 32) blocks of rows.  The symmetric products have NB (NB + 1) / 2
+// tiles of 32 x 32; with one or three of them the summed index of X X^T is cut
+// among the waves (8 or 2 parts), and the parts are added in a fixed order.
+// P X is made in place: a wave reads all of a panel of 32 columns into
+// registers before it writes any of it, and no other wave needs that panel.
+// Rows in LDS are 16 bytes longer than their content: 16 consecutive rows of a
+// b128 read then start in different banks.
+constexpr int kMaxSteps = 64;
+
+struct MuonSmall {
+  float k[kMaxSteps][3];
+  int steps, tall;
+  int mp;               // m rounded up to 32
+  float eps;
+  uint32_t runs;
+  int64_t b0;           // first matrix of this launch
+};
+
+template <int NB>
+struct SmallLds {
+  static constexpr int kRow = 64 * NB + 16;                 // of A and P
+  static constexpr int kTiles = NB * (NB + 1) / 2;
+  static constexpr int kParts = NB == 1 ? 8 : NB == 2 ? 2 : 1;
+  static constexpr int kScratch = kParts / 2 * kTiles * 4096;
+  static constexpr int64_t bytes(int64_t mp) { return 32 * NB * (2 * mp + 16) + 2 * 32 * NB * kRow + kScratch + 64; }
+};
+
+template <int NB, int MOM>
+__global__ __launch_bounds__(512) void muon_small_kernel(MuonInput I, MuonRun run, MuonSmall S, MuonTarget out) {
+  using L = SmallLds<NB>;
+  extern __shared__ __attribute__((aligned(16))) char sm[];
+  const int lane = (int)(threadIdx.x & 63u), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+  const int64_t b = S.b0 + blockIdx.x;
+  const int xrow = 2 * S.mp + 16;
+  char *const X = sm, *const A = X + 32 * NB * xrow, *const P = A + 32 * NB * L::kRow;
+  float *const scratch = (float *)(P + 32 * NB * L::kRow);
+  double *const red = (double *)((char *)scratch + L::kScratch);
+
+  // |U|_F, and zeros for X's padding
+  for (int at = (int)threadIdx.x * 16; at < 32 * NB * xrow; at += 512 * 16) *(float4 *)(X + at) = make_float4(0.f, 0.f, 0.f, 0.f);
+  double sum = 0.0;
+  for (uint32_t q0 = wave; q0 < S.runs; q0 += 32) {
+    MuonRaw R[4];
+    int64_t j[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      int64_t i;
+      run.at(q0 + 8 * e, lane, i, j[e]);
+      R[e] = muon_raw<MOM>(I, b, i, j[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float u[4], m32[4];
+      double m64[4];
+      muon_elems<MOM>(I, R[e], j[e], u, m32, m64);
+#pragma unroll
+      for (int f = 0; f < 4; ++f) sum += (double)u[f] * (double)u[f];
+    }
+  }
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
+  if (lane == 0) red[wave] = sum;
+  __syncthreads();
+  const double scale =
+      muon_scale(((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7])), S.eps);
+
+  // momentum, X0
+  for (uint32_t q0 = wave; q0 < S.runs; q0 += 32) {
+    MuonRaw R[4];
+    int64_t i[4], j[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      run.at(q0 + 8 * e, lane, i[e], j[e]);
+      R[e] = muon_raw<MOM>(I, b, i[e], j[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (q0 + 8 * e >= S.runs) break;
+      float u[4], m32[4];
+      double m64[4] = {0, 0, 0, 0};
+      muon_elems<MOM>(I, R[e], j[e], u, m32, m64);
+      muon_store_momentum<MOM>(I, b, i[e], j[e], run.lanes, m32, m64);
+      if (i[e] >= I.r || j[e] >= I.c) continue;
+      half4 h;
+#pragma unroll
+      for (int f = 0; f < 4; ++f) h[f] = j[e] + f < I.c ? (_Float16)(float)((double)u[f] * scale) : (_Float16)0.f;
+      if (!S.tall) {
+        *(half4 *)(X + i[e] * xrow + j[e] * 2) = h;
+      } else {
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+          if (j[e] + f < I.c) *(_Float16 *)(X + (j[e] + f) * xrow + i[e] * 2) = h[f];
+      }
+    }
+  }
+  __syncthreads();
+
+  const int half = lane >> 5, row = lane & 31;
+  // tile t of the upper triangle, row by row of blocks j >= i
+  auto tile_at = [&](int t, int &ti, int &tj) {
+    tj = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0;
+    ti = t - tj * (tj + 1) / 2;
+  };
+  auto zero = [](float16v &v) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = 0.f;
+  };
+  // four values (m, m + 1, ..) of column n of a symmetric tile, and their mirror image
+  auto put = [&](char *to, int ti, int tj, int q, half4 h) {
+    const int n = 32 * tj + row, m = 32 * ti + 8 * q + 4 * half;
+    *(half4 *)(to + n * L::kRow + m * 2) = h;
+    if (ti < tj) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) *(_Float16 *)(to + (m + e) * L::kRow + n * 2) = h[e];
+    }
+  };
+
+  for (int t = 0; t < S.steps; ++t) {
+    const float ka = S.k[t][0], kb = S.k[t][1], kc = S.k[t][2];
+    // A = X X^T
+    for (int w = wave; w < L::kTiles * L::kParts || L::kParts > 1; w += 8) {
+      const int tile = w % L::kTiles, part = w / L::kTiles;
+      int ti, tj;
+      tile_at(tile, ti, tj);
+      float16v acc, acc2;
+      zero(acc);
+      zero(acc2);
+      if (part < L::kParts) {
+        const int nk = S.mp / 16, k0 = nk * part / L::kParts, k1 = nk * (part + 1) / L::kParts;
+        const char *pl = X + (32 * ti + row) * xrow + 16 * half, *pr = X + (32 * tj + row) * xrow + 16 * half;
+        int k = k0;
+        for (; k + 2 <= k1; k += 2) {
+          const half8 l0 = *(const half8 *)(pl + 32 * k), r0 = *(const half8 *)(pr + 32 * k);
+          const half8 l1 = *(const half8 *)(pl + 32 * k + 32), r1 = *(const half8 *)(pr + 32 * k + 32);
+          acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(l0, r0, acc, 0, 0, 0);
+          acc2 = __builtin_amdgcn_mfma_f32_32x32x16_f16(l1, r1, acc2, 0, 0, 0);
+        }
+        if (k < k1)
+          acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8 *)(pl + 32 * k), *(const half8 *)(pr + 32 * k), acc, 0, 0, 0);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[e] += acc2[e];
+#pragma unroll
+      for (int off = L::kParts / 2; off >= 1; off >>= 1) {
+        float *slot = scratch + ((part & (off - 1)) * L::kTiles + tile) * 1024 + lane * 4;
+        if (part >= off && part < 2 * off) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *(float4 *)(slot + 256 * q) = make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
+        }
+        __syncthreads();
+        if (part < off) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 v = *(const float4 *)(slot + 256 * q);
+            acc[4 * q] += v.x, acc[4 * q + 1] += v.y, acc[4 * q + 2] += v.z, acc[4 * q + 3] += v.w;
+          }
+        }
+        if (off > 1) __syncthreads();
+      }
+      if (part == 0) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          half4 h;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) h[e] = (_Float16)(acc[4 * q + e] * (1.f / kScaleX));
+          put(A, ti, tj, q, h);
+        }
+      }
+      if (L::kParts > 1) break;   // every wave has had its one part
+    }
+    __syncthreads();
+    // P = a I + b A + c A A
+    for (int tile = wave; tile < L::kTiles; tile += 8) {
+      int ti, tj;
+      tile_at(tile, ti, tj);
+      float16v acc;
+      zero(acc);
+#pragma unroll
+      for (int k = 0; k < 2 * NB; ++k)
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8 *)(A + (32 * ti + row) * L::kRow + 16 * half + 32 * k),
+                                                     *(const half8 *)(A + (32 * tj + row) * L::kRow + 16 * half + 32 * k),
+                                                     acc, 0, 0, 0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int n = 32 * tj + row, m = 32 * ti + 8 * q + 4 * half;
+        const half4 s = *(const half4 *)(A + n * L::kRow + m * 2);
+        half4 h;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float o = (kb * (kScaleP / kScaleX)) * (float)s[e] + (kc * (kScaleP / (kScaleX * kScaleX))) * acc[4 * q + e];
+          if (n == m + e) o += ka * kScaleP;
+          h[e] = (_Float16)o;
+        }
+        put(P, ti, tj, q, h);
+      }
+    }
+    __syncthreads();
+    // X <- P X, 32 columns at a time
+    const bool last = t + 1 == S.steps;
+    for (int jp = wave; jp < S.mp / 32; jp += 8) {
+      half8 x[2 * NB];
+      const int s = lane & 15, col = 32 * jp + (lane & 16) + 4 * (s & 3);
+#pragma unroll
+      for (int k = 0; k < 2 * NB; ++k) {
+        union { short4v s[2]; half8 h; } u;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          u.s[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (lds_short4 *)(X + (16 * k + 8 * half + 4 * e + (s >> 2)) * xrow + col * 2));
+        x[k] = u.h;
+      }
+      wave_lds_fence();   // the whole panel is in registers before any of it is written
+#pragma unroll
+      for (int ib = 0; ib < NB; ++ib) {
+        float16v acc;
+        zero(acc);
+        const char *pp = P + (32 * ib + row) * L::kRow + 16 * half;
+        if (last && S.tall) {
+#pragma unroll
+          for (int k = 0; k < 2 * NB; ++k)
+            acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8 *)(pp + 32 * k), x[k], acc, 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 2 * NB; ++k)
+            acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[k], *(const half8 *)(pp + 32 * k), acc, 0, 0, 0);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int m = 8 * q + 4 * half;
+          if (last) {
+            const float v[4] = {acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+            if (S.tall) write_out(out, b, 32 * jp + row, 32 * ib + m, v);
+            else write_out(out, b, 32 * ib + row, 32 * jp + m, v);
+          } else {
+            half4 h;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[e] = (_Float16)(acc[4 * q + e] * (1.f / kScaleP));
+            *(half4 *)(X + (32 * ib + row) * xrow + (32 * jp + m) * 2) = h;
+          }
+        }
+      }
+    }
+    __syncthreads();
   }
 }
 
