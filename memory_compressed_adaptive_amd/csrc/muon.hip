@@ -35,9 +35,13 @@ int64_t small_lds(int64_t n, int64_t m) {
   }
 }
 
-bool fits_small(int64_t n, int64_t m) {
+int small_parts(int64_t n) {
+  return n <= 32 ? SmallLds<1>::kParts : n <= 64 ? SmallLds<2>::kParts : n <= 96 ? SmallLds<3>::kParts : SmallLds<4>::kParts;
+}
+
+bool fits_small(int64_t n, int64_t m, uint32_t runs) {
   const int64_t bytes = small_lds(n, m);
-  return bytes > 0 && bytes <= 160 * 1024;
+  return bytes > 0 && bytes <= 160 * 1024 && runs <= (uint32_t)(kSmallWaves * (n <= 32 ? SmallLds<1>::kRuns : SmallLds<4>::kRuns));
 }
 
 // How a batch of r x c matrices is cut and laid out in the workspace.
@@ -68,7 +72,7 @@ struct Plan {
     x_bytes = (size_t)round_up(2 * chunk * np * mp, 256);
     a_bytes = (size_t)round_up(2 * chunk * np * np, 256);
     part_bytes = (size_t)round_up(8 * chunk * nparts, 256);
-    small = fits_small(n, m);
+    small = fits_small(n, m, runs);
     bytes = small ? 256 : 2 * x_bytes + 2 * a_bytes + part_bytes;
   }
 };
@@ -165,8 +169,9 @@ hipError_t launch_small(int64_t batch, const MuonInput &in, const MuonRun &r, Mu
   const hipError_t e = hipFuncSetAttribute((const void *)muon_small_kernel<NB, MOM>, hipFuncAttributeMaxDynamicSharedMemorySize,
                                            160 * 1024);
   if (e != hipSuccess) return e;
-  for (small.b0 = 0; small.b0 < batch; small.b0 += 1 << 22)   // 2^31 threads in a launch
-    hipLaunchKernelGGL((muon_small_kernel<NB, MOM>), dim3((unsigned)std::min<int64_t>(batch - small.b0, 1 << 22)), dim3(512),
+  for (small.b0 = 0; small.b0 < batch; small.b0 += 1 << 21)   // 2^31 threads in a launch
+    hipLaunchKernelGGL((muon_small_kernel<NB, MOM>), dim3((unsigned)std::min<int64_t>(batch - small.b0, 1 << 21)),
+                       dim3(64 * kSmallWaves),
                        lds, s, in, r, small, o);
   return hipGetLastError();
 }
@@ -181,7 +186,9 @@ hipError_t run_small(const Plan &p, int64_t batch, const MuonInput &in, const Mu
   small.tall = p.tall;
   small.mp = (int)round_up(p.m, 32);
   small.eps = eps;
-  small.runs = p.runs;
+  // parts of at least four products of 16
+  small.parts = 1;
+  while (2 * small.parts <= small_parts(p.n) && small.mp / 16 / (2 * small.parts) >= 4) small.parts *= 2;
   const size_t lds = (size_t)small_lds(p.n, p.m);
   switch ((p.n + 31) / 32) {
     case 1: return launch_small<1, MOM>(batch, in, p.run, small, o, lds, s);
@@ -202,7 +209,7 @@ hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonTarg
   for (int64_t b0 = 0; b0 < batch; b0 += p.chunk) {
     const int64_t cb = std::min(p.chunk, batch - b0);
     hipLaunchKernelGGL((muon_norm_kernel<MOM>), dim3((unsigned)p.nparts, (unsigned)cb), dim3(256), 0, s, in,
-                       p.run, p.runs, b0, part, p.nparts);
+                       p.run, b0, part, p.nparts);
     const int64_t sp = p.tall ? p.np : p.mp, tp = p.tall ? p.mp : p.np;
     const dim3 lg((unsigned)((sp + 4 * p.run.lanes - 1) / (4 * p.run.lanes)), (unsigned)((tp + kLoadRows - 1) / kLoadRows), (unsigned)cb);
     _Float16 *x = x0, *nx = x1;

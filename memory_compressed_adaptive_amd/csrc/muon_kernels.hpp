@@ -55,15 +55,26 @@ struct MuonInput {
 
 __device__ __forceinline__ float bf16_f32(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 
-__device__ __forceinline__ uint16_t f32_bf16(float f) {
-  const uint32_t u = __float_as_uint(f);
-  if ((u & 0x7fffffffu) > 0x7f800000u) return (uint16_t)((u >> 16) | 0x40u);
-  return (uint16_t)((u + 0x7fffu + ((u >> 16) & 1u)) >> 16);
+typedef float float2v __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// two values rounded to nearest even, the first in the low half (one instruction)
+__device__ __forceinline__ uint32_t f32x2_bf16(float lo, float hi) {
+  union { bf16x2 b; uint32_t u; } w;
+  w.b = __builtin_convertvector((float2v{lo, hi}), bf16x2);
+  return w.u;
 }
 
-// What memory holds of four consecutive elements: row i, columns j..j+3 (zeros
-// outside the matrix).  Reading and using them are apart, so that a kernel can
-// have several reads on their way.
+// Where four consecutive elements of a row lie: element offsets into x, into
+// the contiguous momentum and into its scales, and how many of the four are
+// inside the matrix (0 or less: none).
+struct MuonSpot {
+  int64_t x, mat, scale;
+  int n;
+};
+
+// What memory holds of them (zeros outside the matrix).  Reading and using them
+// are apart, so that a kernel can have several reads on their way.
 struct MuonRaw {
   float g[4];
   float mo[4];    // kMom32
@@ -72,67 +83,45 @@ struct MuonRaw {
 };
 
 template <int MOM>
-__device__ __forceinline__ MuonRaw muon_raw(const MuonInput &I, int64_t b, int64_t i, int64_t j) {
+__device__ __forceinline__ MuonRaw muon_raw(const MuonInput &I, const MuonSpot &at) {
   MuonRaw R = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}, 0u, 0.f};
-  if (i >= I.r || j >= I.c) return R;
-  const bool run = I.vec && j + 4 <= I.c;
-  const int64_t at = b * I.x_batch + i * I.x_row + j;
-  if (MOM != kMomNone || I.x_bf16) {
-    const uint16_t *p = (const uint16_t *)I.x + at;
-    if (run) {
-      const uint2 w = *(const uint2 *)p;
+  if (I.vec && at.n >= 4) {
+    if (MOM != kMomNone || I.x_bf16) {
+      const uint2 w = *(const uint2 *)((const uint16_t *)I.x + at.x);
       R.g[0] = __uint_as_float(w.x << 16);
       R.g[1] = __uint_as_float(w.x & 0xffff0000u);
       R.g[2] = __uint_as_float(w.y << 16);
       R.g[3] = __uint_as_float(w.y & 0xffff0000u);
     } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (j + e < I.c) R.g[e] = bf16_f32(p[e]);
-    }
-  } else {
-    const float *p = (const float *)I.x + at;
-    if (run) {
-      const float4 w = *(const float4 *)p;
+      const float4 w = *(const float4 *)((const float *)I.x + at.x);
       R.g[0] = w.x, R.g[1] = w.y, R.g[2] = w.z, R.g[3] = w.w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (j + e < I.c) R.g[e] = p[e];
     }
-  }
-  if (MOM == kMomNone) return R;
-  const int64_t row = b * I.r + i, mat = row * I.c + j;
-  if (MOM == kMom32) {
-    if (run) {
-      const float4 w = *(const float4 *)(I.mom + mat);
+    if (MOM == kMom32) {
+      const float4 w = *(const float4 *)(I.mom + at.mat);
       R.mo[0] = w.x, R.mo[1] = w.y, R.mo[2] = w.z, R.mo[3] = w.w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (j + e < I.c) R.mo[e] = I.mom[mat + e];
     }
+    if (MOM == kMom8) R.w = *(const uint32_t *)(I.codes + at.mat);
   } else {
-    R.s = I.scales[row * ((I.c + kMomentumBlock - 1) / kMomentumBlock) + j / kMomentumBlock];
-    if (run) {
-      R.w = *(const uint32_t *)(I.codes + mat);
-    } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (j + e < I.c) R.w |= (uint32_t)(uint8_t)I.codes[mat + e] << (8 * e);
+    for (int e = 0; e < 4; ++e) {
+      if (e >= at.n) continue;
+      R.g[e] = MOM != kMomNone || I.x_bf16 ? bf16_f32(((const uint16_t *)I.x)[at.x + e]) : ((const float *)I.x)[at.x + e];
+      if (MOM == kMom32) R.mo[e] = I.mom[at.mat + e];
+      if (MOM == kMom8) R.w |= (uint32_t)(uint8_t)I.codes[at.mat + e] << (8 * e);
     }
   }
+  if (MOM == kMom8 && at.n > 0) R.s = I.scales[at.scale];
   return R;
 }
 
 // The matrix to orthogonalise (u) and the new momentum (m32, m64) of those four
-// elements; 0 past the last column.  m64: the 8-bit form's momentum, which
+// elements; 0 outside the matrix.  m64: the 8-bit form's momentum, which
 // decides its codes.  It is formed in 64 bits: a code lies where a product and
 // a sum would each have moved it in fp32 about once in 1e5 elements, and what
 // is written is then what the formula gives, on any machine; the pass is bound
 // by memory either way.
 template <int MOM>
-__device__ __forceinline__ void muon_elems(const MuonInput &I, const MuonRaw &R, int64_t j, float u[4], float m32[4],
+__device__ __forceinline__ void muon_elems(const MuonInput &I, const MuonRaw &R, int n, float u[4], float m32[4],
                                            double m64[4]) {
   if (MOM == kMomNone) {
 #pragma unroll
@@ -145,31 +134,29 @@ __device__ __forceinline__ void muon_elems(const MuonInput &I, const MuonRaw &R,
     if (MOM == kMom32) {
       m32[e] = R.mo[e] * b32 + R.g[e] * o32;
     } else {
-      // a block whose scale is NaN holds NaN; columns past the last hold 0
-      m64[e] = j + e < I.c ? I.beta * ((double)(int8_t)(R.w >> (8 * e)) * (double)R.s) + (1.0 - I.beta) * (double)R.g[e] : 0.0;
+      // a block whose scale is NaN holds NaN; outside the matrix is 0
+      m64[e] = e < n ? I.beta * ((double)(int8_t)(R.w >> (8 * e)) * (double)R.s) + (1.0 - I.beta) * (double)R.g[e] : 0.0;
       m32[e] = (float)m64[e];
     }
     u[e] = I.nesterov ? m32[e] * b32 + R.g[e] * o32 : m32[e];
   }
 }
 
-// Writes the new momentum of row i, columns j..j+3 (nothing outside the
-// matrix).  kMom8: `lanes` consecutive lanes hold a block of 256 (or the row's
-// short last one, or the whole of a shorter row).  All lanes of a wave call it.
+// Writes their new momentum.  kMom8: `lanes` consecutive lanes hold a block of
+// 256 (or the row's short last one, or the whole of a shorter row), and `first`
+// is true in the one that holds its first element.  All lanes of a wave call it.
 template <int MOM>
-__device__ __forceinline__ void muon_store_momentum(const MuonInput &I, int64_t b, int64_t i, int64_t j, int lanes,
+__device__ __forceinline__ void muon_store_momentum(const MuonInput &I, const MuonSpot &at, int lanes, bool first,
                                                     const float m32[4], const double m64[4]) {
   if (MOM == kMomNone) return;
-  const bool in = i < I.r && j < I.c, run = I.vec && j + 4 <= I.c;
-  const int64_t row = b * I.r + i, mat = row * I.c + j;
+  const bool run = I.vec && at.n >= 4;
   if (MOM == kMom32) {
-    if (!in) return;
     if (run) {
-      *(float4 *)(I.mom + mat) = make_float4(m32[0], m32[1], m32[2], m32[3]);
+      *(float4 *)(I.mom + at.mat) = make_float4(m32[0], m32[1], m32[2], m32[3]);
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
-        if (j + e < I.c) I.mom[mat + e] = m32[e];
+        if (e < at.n) I.mom[at.mat + e] = m32[e];
     }
     return;
   }
@@ -189,26 +176,63 @@ __device__ __forceinline__ void muon_store_momentum(const MuonInput &I, int64_t 
     const double q8 = bad ? 0.0 : fmin(fmax(rint(m64[e] * inv), -127.0), 127.0);
     w |= ((uint32_t)(int32_t)q8 & 0xffu) << (8 * e);
   }
-  if (!in) return;
   if (run) {
-    *(uint32_t *)(I.codes + mat) = w;
+    *(uint32_t *)(I.codes + at.mat) = w;
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      if (j + e < I.c) I.codes[mat + e] = (int8_t)(w >> (8 * e));
+      if (e < at.n) I.codes[at.mat + e] = (int8_t)(w >> (8 * e));
   }
-  if (j % kMomentumBlock == 0) I.scales[row * ((I.c + kMomentumBlock - 1) / kMomentumBlock) + j / kMomentumBlock] = step;
+  if (first && at.n > 0) I.scales[at.scale] = step;
 }
 
-// A wave takes `lanes` lanes to a row (4 columns each; 64, or fewer for narrow
-// matrices) and so 64 / lanes rows at once: run q of them, this lane's element.
+// How waves go over a stored matrix: `lanes` lanes to a row (4 columns each; 64,
+// or fewer for narrow matrices) and so 64 / lanes rows at once.
 struct MuonRun {
   uint32_t segs;   // runs along a row: ceil(c / (4 lanes))
   int lanes;
-  __device__ __forceinline__ void at(uint32_t q, int lane, int64_t &i, int64_t &j) const {
-    const uint32_t rows = q / segs, seg = q - rows * segs;
-    i = (int64_t)rows * (64 / lanes) + lane / lanes;
-    j = ((int64_t)seg * lanes + (lane & (lanes - 1))) * 4;
+};
+
+// Run `first`, then every `stride`-th.  What depends on the lane is set up once;
+// a step is a few scalar instructions.
+struct MuonWalk {
+  int group, seg;              // uniform: which rows, which part of them
+  int groups, segs, rows, wide, step_group, step_seg;
+  int di, dj, r, c, blocks;
+  int64_t x0, mat0, scale0, x_row;
+
+  __device__ __forceinline__ MuonWalk(const MuonInput &I, const MuonRun &run, int64_t b, int lane, uint32_t first,
+                                      uint32_t stride) {
+    segs = (int)run.segs;
+    rows = 64 / run.lanes;
+    wide = 4 * run.lanes;
+    di = lane / run.lanes;
+    dj = 4 * (lane & (run.lanes - 1));
+    r = (int)I.r;
+    c = (int)I.c;
+    groups = (r + rows - 1) / rows;
+    blocks = (c + kMomentumBlock - 1) / kMomentumBlock;
+    group = (int)(first / run.segs);
+    seg = (int)(first - (uint32_t)group * run.segs);
+    step_group = (int)(stride / run.segs);
+    step_seg = (int)(stride - (uint32_t)step_group * run.segs);
+    x_row = I.x_row;
+    x0 = b * I.x_batch + di * I.x_row + dj;
+    mat0 = (b * I.r + di) * I.c + dj;
+    scale0 = (b * I.r + di) * blocks;
+  }
+  __device__ __forceinline__ bool more() const { return group < groups; }
+  __device__ __forceinline__ int row() const { return group * rows; }   // of lane 0
+  __device__ __forceinline__ int col() const { return seg * wide; }
+  __device__ __forceinline__ MuonSpot spot() const {
+    const int i = group * rows, j = seg * wide;
+    const int left = c - dj - j;
+    return {x0 + ((int64_t)i * x_row + j), mat0 + ((int64_t)i * c + j), scale0 + ((int64_t)i * blocks + seg), i + di < r ? left : 0};
+  }
+  __device__ __forceinline__ void next() {
+    group += step_group;
+    seg += step_seg;
+    if (seg >= segs) seg -= segs, ++group;
   }
 };
 
@@ -217,26 +241,26 @@ struct MuonRun {
 // fp32's range): block p of matrix b writes part[b][p].  No atomics, so results
 // do not depend on timing.  Four reads of a lane are on their way at a time.
 template <int MOM>
-__global__ __launch_bounds__(256) void muon_norm_kernel(MuonInput I, MuonRun run, uint32_t runs, int64_t b0, double *part,
-                                                        int nparts) {
+__global__ __launch_bounds__(256) void muon_norm_kernel(MuonInput I, MuonRun run, int64_t b0, double *part, int nparts) {
   const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6);
   const int64_t lb = blockIdx.y, b = b0 + lb;
-  const uint32_t stride = (uint32_t)nparts * 4;
   double sum = 0.0;
-  for (uint32_t q0 = blockIdx.x * 4 + wave; q0 < runs; q0 += 4 * stride) {
+  MuonWalk walk(I, run, b, lane, __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + wave), (uint32_t)nparts * 4);
+  while (walk.more()) {
     MuonRaw R[4];
-    int64_t j[4];
+    int n[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      int64_t i;
-      run.at(q0 + e * stride, lane, i, j[e]);   // past the last run: rows past the last, zeros
-      R[e] = muon_raw<MOM>(I, b, i, j[e]);
+      const MuonSpot at = walk.spot();   // past the last run: past the last row, zeros
+      n[e] = at.n;
+      R[e] = muon_raw<MOM>(I, at);
+      walk.next();
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float u[4], m32[4];
       double m64[4];
-      muon_elems<MOM>(I, R[e], j[e], u, m32, m64);
+      muon_elems<MOM>(I, R[e], n[e], u, m32, m64);
 #pragma unroll
       for (int f = 0; f < 4; ++f) sum += (double)u[f] * (double)u[f];
     }
@@ -280,27 +304,31 @@ __global__ __launch_bounds__(256) void muon_load_kernel(MuonInput I, MuonRun run
   __syncthreads();
   const double scale = muon_scale((s4[0] + s4[1]) + (s4[2] + s4[3]), eps);
   X += lb * sp * tp;
+  const int blocks = (int)((I.c + kMomentumBlock - 1) / kMomentumBlock);
   for (int q0 = wave * rows; q0 < kLoadRows; q0 += 16 * rows) {
     MuonRaw R[4];
+    MuonSpot at[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int q = q0 + e * 4 * rows + lane / run.lanes;
-      R[e] = muon_raw<MOM>(I, b, q < kLoadRows ? i0 + q : I.r, j);
+      const int64_t i = i0 + q;
+      at[e] = {b * I.x_batch + i * I.x_row + j, (b * I.r + i) * I.c + j, (b * I.r + i) * blocks + j / kMomentumBlock,
+               q < kLoadRows && i < I.r ? (int)(I.c - j) : 0};
+      R[e] = muon_raw<MOM>(I, at[e]);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (q0 + e * 4 * rows >= kLoadRows) break;
       const int q = q0 + e * 4 * rows + lane / run.lanes;
-      const int64_t i = i0 + q;
       float u[4], m32[4];
       double m64[4] = {0, 0, 0, 0};
-      muon_elems<MOM>(I, R[e], j, u, m32, m64);
+      muon_elems<MOM>(I, R[e], at[e].n, u, m32, m64);
       half4 h;
 #pragma unroll
-      for (int f = 0; f < 4; ++f) h[f] = i < I.r && j + f < I.c ? (_Float16)(float)((double)u[f] * scale) : (_Float16)0.f;
-      muon_store_momentum<MOM>(I, b, i, j, run.lanes, m32, m64);
+      for (int f = 0; f < 4; ++f) h[f] = f < at[e].n ? (_Float16)(float)((double)u[f] * scale) : (_Float16)0.f;
+      muon_store_momentum<MOM>(I, at[e], run.lanes, j % kMomentumBlock == 0, m32, m64);
       if (TALL) *(half4 *)&tile[q][col] = h;
-      else if (j < sp && i < tp) *(half4 *)(X + i * sp + j) = h;
+      else if (j < sp && i0 + q < tp) *(half4 *)(X + (i0 + q) * sp + j) = h;
     }
   }
   if (!TALL) return;
@@ -324,46 +352,66 @@ struct MuonTarget {
   float decay, rate;
 };
 
-// Four consecutive sums of the last product, v, to row i, columns j..j+3 of
-// matrix b (nothing outside it).
-__device__ __forceinline__ void write_out(const MuonTarget &T, int64_t b, int64_t i, int64_t j, const float v[4]) {
-  if (i >= T.rows || j >= T.cols) return;
-  const int64_t at = b * T.batch + i * T.row + j;
+// Four consecutive sums of the last product, v[e], to the elements from
+// at + e step on, for e < N: as many as lie inside the matrix, left - e dj
+// columns of them if fewer than `rows` rows e di have gone by.  All old values
+// are read before the first is written, so that the reads are under way
+// together.
+template <int N>
+__device__ __forceinline__ void write_out(const MuonTarget &T, int64_t at, int64_t step, int rows, int left, int di, int dj,
+                                          const float (*v)[4]) {
   constexpr float kUnit = 1.f / (kScaleX * kScaleP);
-  if (T.vec && j + 4 <= T.cols) {
-    if (T.bf16) {
-      uint16_t *p = (uint16_t *)T.out + at;
-      float old[4] = {0.f, 0.f, 0.f, 0.f};
-      if (T.update) {
-        const uint2 w = *(const uint2 *)p;
-        old[0] = __uint_as_float(w.x << 16), old[1] = __uint_as_float(w.x & 0xffff0000u);
-        old[2] = __uint_as_float(w.y << 16), old[3] = __uint_as_float(w.y & 0xffff0000u);
-      }
-      uint32_t w[4];
+  float old[N][4];
+  if (T.update) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = f32_bf16(T.update ? old[e] * T.decay - T.rate * (v[e] * kUnit) : v[e] * kUnit);
-      *(uint2 *)p = make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-    } else {
-      float *p = (float *)T.out + at;
-      float4 w = *(const float4 *)p;
-      w.x = w.x * T.decay - T.rate * (v[0] * kUnit);
-      w.y = w.y * T.decay - T.rate * (v[1] * kUnit);
-      w.z = w.z * T.decay - T.rate * (v[2] * kUnit);
-      w.w = w.w * T.decay - T.rate * (v[3] * kUnit);
-      *(float4 *)p = w;
+    for (int e = 0; e < N; ++e) {
+      const int n = e * di < rows ? left - e * dj : 0;
+      if (T.bf16) {
+        const uint16_t *p = (const uint16_t *)T.out + (at + e * step);
+        if (T.vec && n >= 4) {
+          const uint2 w = *(const uint2 *)p;
+          old[e][0] = __uint_as_float(w.x << 16), old[e][1] = __uint_as_float(w.x & 0xffff0000u);
+          old[e][2] = __uint_as_float(w.y << 16), old[e][3] = __uint_as_float(w.y & 0xffff0000u);
+        } else {
+#pragma unroll
+          for (int f = 0; f < 4; ++f) old[e][f] = f < n ? bf16_f32(p[f]) : 0.f;
+        }
+      } else {
+        const float *p = (const float *)T.out + (at + e * step);
+        if (T.vec && n >= 4) {
+          const float4 w = *(const float4 *)p;
+          old[e][0] = w.x, old[e][1] = w.y, old[e][2] = w.z, old[e][3] = w.w;
+        } else {
+#pragma unroll
+          for (int f = 0; f < 4; ++f) old[e][f] = f < n ? p[f] : 0.f;
+        }
+      }
     }
-    return;
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (j + e >= T.cols) continue;
-    const float x = v[e] * kUnit;
+  for (int e = 0; e < N; ++e) {
+    const int n = e * di < rows ? left - e * dj : 0;
+    float x[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) x[f] = T.update ? old[e][f] * T.decay - T.rate * (v[e][f] * kUnit) : v[e][f] * kUnit;
     if (T.bf16) {
-      uint16_t *p = (uint16_t *)T.out + at + e;
-      *p = f32_bf16(T.update ? bf16_f32(*p) * T.decay - T.rate * x : x);
+      uint16_t *p = (uint16_t *)T.out + (at + e * step);
+      if (T.vec && n >= 4) {
+        *(uint2 *)p = make_uint2(f32x2_bf16(x[0], x[1]), f32x2_bf16(x[2], x[3]));
+      } else {
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+          if (f < n) p[f] = (uint16_t)f32x2_bf16(x[f], 0.f);
+      }
     } else {
-      float *p = (float *)T.out + at + e;
-      *p = *p * T.decay - T.rate * x;
+      float *p = (float *)T.out + (at + e * step);
+      if (T.vec && n >= 4) {
+        *(float4 *)p = make_float4(x[0], x[1], x[2], x[3]);
+      } else {
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+          if (f < n) p[f] = x[f];
+      }
     }
   }
 }
@@ -662,14 +710,33 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
           *(float4 *)(mine + (lane & 31) * kStride + (32 * i + 8 * q + 4 * (lane >> 5)) * 4) =
               make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
       wave_lds_fence();
-      constexpr int kChunks = T::TM / 4;   // of a row
-#pragma unroll 4
-      for (int g = lane; g < 32 * kChunks; g += 64) {
-        const int row = g / kChunks, c = g % kChunks;
-        const float4 w = *(const float4 *)(mine + row * kStride + c * 16);
-        const float v[4] = {w.x, w.y, w.z, w.w};
-        const int64_t nn = nb + row, mm = mb + 4 * c;
-        write_out(A.out, A.b0 + lb, nn, mm, v);
+      // a row's TM / 4 chunks lie beside each other; 64 lanes take whole rows
+      constexpr int kChunks = T::TM / 4, kTrips = 32 * kChunks / 64, kOnce = kTrips % 4 == 0 ? 4 : 2;
+      static_assert(kTrips % kOnce == 0, "whole groups");
+#pragma unroll
+      for (int g = 0; g < kTrips; g += kOnce) {
+        float v[kOnce][4];
+        // chunks of one lane: kOnce rows apart by the same step where a trip is whole rows
+        if (64 % kChunks == 0) {
+          const int row = (g * 64 + lane) / kChunks, c = lane % kChunks;
+          const int64_t to = (A.b0 + lb) * A.out.batch + (nb + row) * A.out.row + mb + 4 * c;
+#pragma unroll
+          for (int e = 0; e < kOnce; ++e) {
+            const float4 w = *(const float4 *)(mine + (row + e * (64 / kChunks)) * kStride + c * 16);
+            v[e][0] = w.x, v[e][1] = w.y, v[e][2] = w.z, v[e][3] = w.w;
+          }
+          write_out<kOnce>(A.out, to, (64 / kChunks) * A.out.row, (int)(A.out.rows - nb) - row, (int)(A.out.cols - mb) - 4 * c,
+                           64 / kChunks, 0, v);
+        } else {
+#pragma unroll
+          for (int e = 0; e < kOnce; ++e) {
+            const int at = (g + e) * 64 + lane, row = at / kChunks, c = at % kChunks;
+            const float4 w = *(const float4 *)(mine + row * kStride + c * 16);
+            v[0][0] = w.x, v[0][1] = w.y, v[0][2] = w.z, v[0][3] = w.w;
+            write_out<1>(A.out, (A.b0 + lb) * A.out.batch + (nb + row) * A.out.row + mb + 4 * c, 0,
+                         (int)(A.out.rows - nb) - row, (int)(A.out.cols - mb) - 4 * c, 0, 0, v);
+          }
+        }
       }
       wave_lds_fence();
       continue;
@@ -727,25 +794,31 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
 
 // ------------------------------------------------------------------ a whole matrix in one workgroup
 // Matrices whose X, A and P fit a CU's LDS take one launch: momentum, norm, all
-// steps and the result, one workgroup of 8 waves for each matrix.  What bounds
+// steps and the result, one workgroup of 16 waves for each matrix.  What bounds
 // it is latency: a step is three short products with a barrier after each.  The
 // other way is 2 + 3 steps launches, of at least 3 us each.
 //
 // NB = ceil(n / 32) blocks of rows.  The symmetric products have NB (NB + 1) / 2
-// tiles of 32 x 32; with one or three of them the summed index of X X^T is cut
-// among the waves (8 or 2 parts), and the parts are added in a fixed order.
-// P X is made in place: a wave reads all of a panel of 32 columns into
-// registers before it writes any of it, and no other wave needs that panel.
-// Rows in LDS are 16 bytes longer than their content: 16 consecutive rows of a
-// b128 read then start in different banks.
+// tiles of 32 x 32; where there are few, the summed index of X X^T is cut among
+// the waves and the parts are added in a fixed order.  P X is made in place: a
+// wave reads all of a panel of 32 columns into registers before it writes any
+// of it, and no other wave needs that panel.  Rows in LDS are 16 bytes longer
+// than their content: 16 consecutive rows of a b128 read then start in
+// different banks.
+//
+// The matrix is read once: a lane keeps its elements of U until the norm is
+// known.  X0 is U times the power of two that puts its norm in (1/2, 1] 2^14,
+// and what is left of the factor 1 / max(|U|, eps) goes into the fp32 results
+// of the first step's products, which costs no rounding.
 constexpr int kMaxSteps = 64;
+constexpr int kSmallWaves = 16;
 
 struct MuonSmall {
   float k[kMaxSteps][3];
   int steps, tall;
   int mp;               // m rounded up to 32
+  int parts;            // of the summed index of X X^T
   float eps;
-  uint32_t runs;
   int64_t b0;           // first matrix of this launch
 };
 
@@ -753,13 +826,14 @@ template <int NB>
 struct SmallLds {
   static constexpr int kRow = 64 * NB + 16;                 // of A and P
   static constexpr int kTiles = NB * (NB + 1) / 2;
-  static constexpr int kParts = NB == 1 ? 8 : NB == 2 ? 2 : 1;
+  static constexpr int kParts = NB == 1 ? 8 : NB == 2 ? 4 : NB == 3 ? 2 : 1;   // at most; a power of two
   static constexpr int kScratch = kParts / 2 * kTiles * 4096;
-  static constexpr int64_t bytes(int64_t mp) { return 32 * NB * (2 * mp + 16) + 2 * 32 * NB * kRow + kScratch + 64; }
+  static constexpr int kRuns = NB == 1 ? 20 : 16;   // runs of 64 x 4 elements that a wave can keep
+  static constexpr int64_t bytes(int64_t mp) { return 32 * NB * (2 * mp + 16) + 2 * 32 * NB * kRow + kScratch + 8 * kSmallWaves; }
 };
 
 template <int NB, int MOM>
-__global__ __launch_bounds__(512) void muon_small_kernel(MuonInput I, MuonRun run, MuonSmall S, MuonTarget out) {
+__global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonInput I, MuonRun run, MuonSmall S, MuonTarget out) {
   using L = SmallLds<NB>;
   extern __shared__ __attribute__((aligned(16))) char sm[];
   const int lane = (int)(threadIdx.x & 63u), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -769,61 +843,69 @@ __global__ __launch_bounds__(512) void muon_small_kernel(MuonInput I, MuonRun ru
   float *const scratch = (float *)(P + 32 * NB * L::kRow);
   double *const red = (double *)((char *)scratch + L::kScratch);
 
-  // |U|_F, and zeros for X's padding
-  for (int at = (int)threadIdx.x * 16; at < 32 * NB * xrow; at += 512 * 16) *(float4 *)(X + at) = make_float4(0.f, 0.f, 0.f, 0.f);
+  // U and its norm, the new momentum, zeros for X's padding
+  for (int at = (int)threadIdx.x * 16; at < 32 * NB * xrow; at += 1024 * kSmallWaves)
+    *(float4 *)(X + at) = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kGroup = MOM == kMomNone ? 4 : 2;   // reads under way in a lane (registers bound it)
+  float u[L::kRuns][4];
   double sum = 0.0;
-  for (uint32_t q0 = wave; q0 < S.runs; q0 += 32) {
-    MuonRaw R[4];
-    int64_t j[4];
+  {
+    MuonWalk walk(I, run, b, lane, wave, kSmallWaves);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      int64_t i;
-      run.at(q0 + 8 * e, lane, i, j[e]);
-      R[e] = muon_raw<MOM>(I, b, i, j[e]);
-    }
+    for (int g = 0; g < L::kRuns; g += kGroup) {
+      if (!walk.more()) continue;
+      MuonRaw R[kGroup];
+      MuonSpot at[kGroup];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float u[4], m32[4];
-      double m64[4];
-      muon_elems<MOM>(I, R[e], j[e], u, m32, m64);
+      for (int e = 0; e < kGroup; ++e) {
+        at[e] = walk.spot();   // past the last run: past the last row, zeros
+        R[e] = muon_raw<MOM>(I, at[e]);
+        walk.next();
+      }
 #pragma unroll
-      for (int f = 0; f < 4; ++f) sum += (double)u[f] * (double)u[f];
+      for (int e = 0; e < kGroup; ++e) {
+        float m32[4];
+        double m64[4] = {0, 0, 0, 0};
+        muon_elems<MOM>(I, R[e], at[e].n, u[g + e], m32, m64);
+        muon_store_momentum<MOM>(I, at[e], run.lanes, (lane & (run.lanes - 1)) == 0, m32, m64);
+#pragma unroll
+        for (int f = 0; f < 4; ++f) sum += (double)u[g + e][f] * (double)u[g + e][f];
+      }
     }
   }
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
   if (lane == 0) red[wave] = sum;
   __syncthreads();
-  const double scale =
-      muon_scale(((red[0] + red[1]) + (red[2] + red[3])) + ((red[4] + red[5]) + (red[6] + red[7])), S.eps);
-
-  // momentum, X0
-  for (uint32_t q0 = wave; q0 < S.runs; q0 += 32) {
-    MuonRaw R[4];
-    int64_t i[4], j[4];
+  double total = red[0];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      run.at(q0 + 8 * e, lane, i[e], j[e]);
-      R[e] = muon_raw<MOM>(I, b, i[e], j[e]);
-    }
+  for (int w = 1; w < kSmallWaves; ++w) total += red[w];
+  // 1 / max(|U|, eps) = rest * 2^pow, rest in [1, 2); all NaN if the norm is not finite
+  const double factor = muon_scale(total, S.eps) * (1.0 / (double)kScaleX);
+  int pow = 0;
+  const double frac = frexp(factor, &pow);   // in [1/2, 1)
+  const bool fine = factor > 0.0 && factor < (double)__builtin_inff();
+  const float rest = fine ? (float)(2.0 * frac) : __builtin_nanf("");
+  const int shift = fine ? pow - 1 + 14 : 0;
+  {
+    MuonWalk walk(I, run, b, lane, wave, kSmallWaves);
+    const int to = S.tall ? walk.dj * xrow + 2 * walk.di : walk.di * xrow + 2 * walk.dj;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (q0 + 8 * e >= S.runs) break;
-      float u[4], m32[4];
-      double m64[4] = {0, 0, 0, 0};
-      muon_elems<MOM>(I, R[e], j[e], u, m32, m64);
-      muon_store_momentum<MOM>(I, b, i[e], j[e], run.lanes, m32, m64);
-      if (i[e] >= I.r || j[e] >= I.c) continue;
-      half4 h;
+    for (int g = 0; g < L::kRuns; ++g) {
+      if (!walk.more()) continue;
+      const int i = walk.row(), j = walk.col(), n = i + walk.di < walk.r ? walk.c - walk.dj - j : 0;
+      _Float16 h[4];
 #pragma unroll
-      for (int f = 0; f < 4; ++f) h[f] = j[e] + f < I.c ? (_Float16)(float)((double)u[f] * scale) : (_Float16)0.f;
+      for (int f = 0; f < 4; ++f) h[f] = (_Float16)ldexpf(u[g][f], shift);
       if (!S.tall) {
-        *(half4 *)(X + i[e] * xrow + j[e] * 2) = h;
+        // past the last column u is 0, and so is the padding
+        if (n > 0) *(half4 *)(X + to + i * xrow + 2 * j) = half4{h[0], h[1], h[2], h[3]};
       } else {
 #pragma unroll
         for (int f = 0; f < 4; ++f)
-          if (j[e] + f < I.c) *(_Float16 *)(X + (j[e] + f) * xrow + i[e] * 2) = h[f];
+          if (f < n) *(_Float16 *)(X + to + (j + f) * xrow + 2 * i) = h[f];
       }
+      walk.next();
     }
   }
   __syncthreads();
@@ -848,18 +930,34 @@ __global__ __launch_bounds__(512) void muon_small_kernel(MuonInput I, MuonRun ru
     }
   };
 
+  // a panel of 32 columns of X as fragments; the whole of it is in registers
+  // before anything of it is written
+  auto panel = [&](int jp, half8 *x) {
+    const int s = lane & 15;
+    const char *px = X + (8 * half + (s >> 2)) * xrow + (32 * jp + (lane & 16) + 4 * (s & 3)) * 2;
+#pragma unroll
+    for (int k = 0; k < 2 * NB; ++k) {
+      union { short4v s[2]; half8 h; } w;
+      w.s[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(px + 16 * k * xrow));
+      w.s[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_short4 *)(px + (16 * k + 4) * xrow));
+      x[k] = w.h;
+    }
+    wave_lds_fence();
+  };
+
   for (int t = 0; t < S.steps; ++t) {
     const float ka = S.k[t][0], kb = S.k[t][1], kc = S.k[t][2];
-    // A = X X^T
-    for (int w = wave; w < L::kTiles * L::kParts || L::kParts > 1; w += 8) {
-      const int tile = w % L::kTiles, part = w / L::kTiles;
+    const float left = t == 0 ? rest : 1.f;
+    // A = X X^T: wave = part * kTiles + tile
+    {
+      const int tile = wave % L::kTiles, part = wave / L::kTiles;
       int ti, tj;
       tile_at(tile, ti, tj);
       float16v acc, acc2;
       zero(acc);
       zero(acc2);
-      if (part < L::kParts) {
-        const int nk = S.mp / 16, k0 = nk * part / L::kParts, k1 = nk * (part + 1) / L::kParts;
+      if (part < S.parts) {
+        const int nk = S.mp / 16, k0 = nk * part / S.parts, k1 = nk * (part + 1) / S.parts;
         const char *pl = X + (32 * ti + row) * xrow + 16 * half, *pr = X + (32 * tj + row) * xrow + 16 * half;
         int k = k0;
         for (; k + 2 <= k1; k += 2) {
@@ -873,8 +971,7 @@ __global__ __launch_bounds__(512) void muon_small_kernel(MuonInput I, MuonRun ru
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[e] += acc2[e];
-#pragma unroll
-      for (int off = L::kParts / 2; off >= 1; off >>= 1) {
+      for (int off = S.parts / 2; off >= 1; off >>= 1) {
         float *slot = scratch + ((part & (off - 1)) * L::kTiles + tile) * 1024 + lane * 4;
         if (part >= off && part < 2 * off) {
 #pragma unroll
@@ -892,28 +989,31 @@ __global__ __launch_bounds__(512) void muon_small_kernel(MuonInput I, MuonRun ru
         if (off > 1) __syncthreads();
       }
       if (part == 0) {
+        const float unit = left * left * (1.f / kScaleX);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           half4 h;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = (_Float16)(acc[4 * q + e] * (1.f / kScaleX));
+          for (int e = 0; e < 4; ++e) h[e] = (_Float16)(acc[4 * q + e] * unit);
           put(A, ti, tj, q, h);
         }
       }
-      if (L::kParts > 1) break;   // every wave has had its one part
     }
     __syncthreads();
     // P = a I + b A + c A A
-    for (int tile = wave; tile < L::kTiles; tile += 8) {
+    if (wave < L::kTiles) {
       int ti, tj;
-      tile_at(tile, ti, tj);
-      float16v acc;
+      tile_at(wave, ti, tj);
+      float16v acc, acc2;
       zero(acc);
+      zero(acc2);
+      const char *pl = A + (32 * ti + row) * L::kRow + 16 * half, *pr = A + (32 * tj + row) * L::kRow + 16 * half;
 #pragma unroll
-      for (int k = 0; k < 2 * NB; ++k)
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8 *)(A + (32 * ti + row) * L::kRow + 16 * half + 32 * k),
-                                                     *(const half8 *)(A + (32 * tj + row) * L::kRow + 16 * half + 32 * k),
-                                                     acc, 0, 0, 0);
+      for (int k = 0; k < NB; ++k) {
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8 *)(pl + 64 * k), *(const half8 *)(pr + 64 * k), acc, 0, 0, 0);
+        acc2 = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8 *)(pl + 64 * k + 32), *(const half8 *)(pr + 64 * k + 32),
+                                                      acc2, 0, 0, 0);
+      }
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int n = 32 * tj + row, m = 32 * ti + 8 * q + 4 * half;
@@ -921,7 +1021,8 @@ __global__ __launch_bounds__(512) void muon_small_kernel(MuonInput I, MuonRun ru
         half4 h;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float o = (kb * (kScaleP / kScaleX)) * (float)s[e] + (kc * (kScaleP / (kScaleX * kScaleX))) * acc[4 * q + e];
+          float o = (kb * (kScaleP / kScaleX)) * (float)s[e] +
+                    (kc * (kScaleP / (kScaleX * kScaleX))) * (acc[4 * q + e] + acc2[4 * q + e]);
           if (n == m + e) o += ka * kScaleP;
           h[e] = (_Float16)o;
         }
@@ -929,52 +1030,80 @@ __global__ __launch_bounds__(512) void muon_small_kernel(MuonInput I, MuonRun ru
       }
     }
     __syncthreads();
+    if (t + 1 == S.steps) break;
     // X <- P X, 32 columns at a time
-    const bool last = t + 1 == S.steps;
-    for (int jp = wave; jp < S.mp / 32; jp += 8) {
+    const float unit = left * (1.f / kScaleP);
+    for (int jp = wave; jp < S.mp / 32; jp += kSmallWaves) {
       half8 x[2 * NB];
-      const int s = lane & 15, col = 32 * jp + (lane & 16) + 4 * (s & 3);
-#pragma unroll
-      for (int k = 0; k < 2 * NB; ++k) {
-        union { short4v s[2]; half8 h; } u;
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          u.s[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_short4 *)(X + (16 * k + 8 * half + 4 * e + (s >> 2)) * xrow + col * 2));
-        x[k] = u.h;
-      }
-      wave_lds_fence();   // the whole panel is in registers before any of it is written
+      panel(jp, x);
 #pragma unroll
       for (int ib = 0; ib < NB; ++ib) {
         float16v acc;
         zero(acc);
         const char *pp = P + (32 * ib + row) * L::kRow + 16 * half;
-        if (last && S.tall) {
 #pragma unroll
-          for (int k = 0; k < 2 * NB; ++k)
-            acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8 *)(pp + 32 * k), x[k], acc, 0, 0, 0);
-        } else {
-#pragma unroll
-          for (int k = 0; k < 2 * NB; ++k)
-            acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[k], *(const half8 *)(pp + 32 * k), acc, 0, 0, 0);
-        }
+        for (int k = 0; k < 2 * NB; ++k)
+          acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[k], *(const half8 *)(pp + 32 * k), acc, 0, 0, 0);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int m = 8 * q + 4 * half;
-          if (last) {
-            const float v[4] = {acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
-            if (S.tall) write_out(out, b, 32 * jp + row, 32 * ib + m, v);
-            else write_out(out, b, 32 * ib + row, 32 * jp + m, v);
-          } else {
-            half4 h;
+          half4 h;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = (_Float16)(acc[4 * q + e] * (1.f / kScaleP));
-            *(half4 *)(X + (32 * ib + row) * xrow + (32 * jp + m) * 2) = h;
-          }
+          for (int e = 0; e < 4; ++e) h[e] = (_Float16)(acc[4 * q + e] * unit);
+          *(half4 *)(X + (32 * ib + row) * xrow + (32 * jp + 8 * q + 4 * half) * 2) = h;
         }
       }
     }
     __syncthreads();
+  }
+
+  // the last P X goes to memory
+  const float left = S.steps == 1 ? rest : 1.f;
+  for (int jp = wave; jp < S.mp / 32; jp += kSmallWaves) {
+    half8 x[2 * NB];
+    panel(jp, x);
+    for (int ib = 0; ib < NB; ++ib) {
+      float16v acc;
+      zero(acc);
+      const char *pp = P + (32 * ib + row) * L::kRow + 16 * half;
+      if (S.tall) {
+        // rows of the result are columns of X: a lane has four consecutive elements of one
+#pragma unroll
+        for (int k = 0; k < 2 * NB; ++k)
+          acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8 *)(pp + 32 * k), x[k], acc, 0, 0, 0);
+        float v[4][4];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e >> 2][e & 3] = left * acc[e];
+        const int i = 32 * jp + row, j = 32 * ib + 4 * half;
+        write_out<4>(out, b * out.batch + i * out.row + j, 8, (int)out.rows - i, (int)out.cols - j, 0, 8, v);
+        continue;
+      }
+#pragma unroll
+      for (int k = 0; k < 2 * NB; ++k)
+        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[k], *(const half8 *)(pp + 32 * k), acc, 0, 0, 0);
+      // the panel's place in LDS (32 NB rows of 64 bytes) takes 16 rows of 32
+      // fp32 results at a time: row r of them in its rows 2r and 2r + 1, so
+      // that memory is written in whole rows of the panel
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        if (row >> 4 == p) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *(float4 *)(X + (2 * (row & 15) + (q >> 1)) * xrow + 64 * jp + ((q & 1) * 8 + 4 * half) * 4) =
+                make_float4(left * acc[4 * q], left * acc[4 * q + 1], left * acc[4 * q + 2], left * acc[4 * q + 3]);
+        }
+        wave_lds_fence();
+        float v[2][4];
+        const int r = lane >> 3, c = lane & 7;   // rows r and r + 8, columns 4c..
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float4 w = *(const float4 *)(X + (2 * (r + 8 * e) + (c >> 2)) * xrow + 64 * jp + (c & 3) * 16);
+          v[e][0] = w.x, v[e][1] = w.y, v[e][2] = w.z, v[e][3] = w.w;
+        }
+        const int i = 32 * ib + 16 * p + r, j = 32 * jp + 4 * c;
+        write_out<2>(out, b * out.batch + i * out.row + j, 8 * out.row, (int)out.rows - i, (int)out.cols - j, 8, 0, v);
+        wave_lds_fence();
+      }
+    }
   }
 }
 
