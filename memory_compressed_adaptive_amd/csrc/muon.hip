@@ -117,9 +117,10 @@ bool coefficients_ok(const float *k, int steps, const char **why) {
   return true;
 }
 
-using Tile64 = Tile<64, 64, 2, 2, 64, 2>;
+using Tile64 = Tile<64, 64, 2, 2, 64, 4, 2>;
 using Tile128 = Tile<128, 128, 2, 2, 64, 2>;
-using Tile192 = Tile<192, 192, 2, 2, 32, 3>;
+using Tile128Deep = Tile<128, 128, 4, 2, 64, 4>;   // alone on a CU
+using Tile192 = Tile<192, 192, 2, 2, 64, 2>;
 using Tile256 = Tile<256, 256, 4, 2, 64, 2>;
 
 template <class T, int ROLE>
@@ -130,34 +131,41 @@ void product_t(MuonProduct a, int64_t chunk, hipStream_t s) {
   hipLaunchKernelGGL((muon_product_kernel<T, ROLE>), dim3((unsigned)(a.tiles * chunk)), dim3(T::kThreads), 0, s, a);
 }
 
-// The tile with the shortest expected time: rounds of workgroups over the 256
-// CUs times what 64 of the summed index take in a round.  Measured on products
-// that fill the card: 1.88 us with 256 x 256 tiles (one workgroup on a CU),
-// 1.25 with 192 x 192 (one), 1.10 with 128 x 128 (two; 0.6 where there is only
-// one), 0.75 with 64 x 64 (four; 0.35).  Large tiles read less for each
-// product; smaller ones waste less of the last round and of the half that a
-// symmetric result leaves out (4096: 136 tiles of 256 take 1.88, 253 of 192 1.25).
-int pick_tile(int64_t m, int64_t n, int64_t chunk, bool symmetric) {
-  const struct { int side, per_cu; double one, full; } kinds[] = {
-      {256, 1, 1.88, 1.88}, {192, 1, 1.25, 1.25}, {128, 2, 0.60, 1.10}, {64, 4, 0.35, 0.75}};
+// The tile with the shortest expected time.  Workgroups go over the 256 CUs in
+// rounds; a round takes so long for 64 of the summed index and so long for its
+// beginning and end (microseconds, measured on products that fill the card and
+// on ones that do not; "alone": at most one workgroup on a CU).  Large tiles
+// read less for each product; smaller ones waste less of the last round and of
+// the half that a symmetric result leaves out (n = 4096: 136 tiles of 256 take
+// 240 us where 253 of 192 take 197).  Where parameters are read and written
+// (`out`), the end is bound by memory, and two workgroups to a CU hide it.
+int pick_tile(int64_t m, int64_t n, int64_t k, int64_t chunk, bool symmetric, bool out) {
+  const struct { int kind, side, per_cu; double alone, full, ends, out; } kinds[] = {
+      {256, 256, 1, 1.76, 1.76, 5.0, 14.0},
+      {192, 192, 1, 1.14, 1.14, 4.0, 10.0},
+      {128, 128, 2, 0.60, 1.02, 3.5, 6.0},
+      {129, 128, 1, 0.45, 0.95, 3.5, 6.0},
+      {64, 64, 2, 0.26, 0.40, 2.5, 3.5}};
   int best = 0;
   double least = 0.0;
-  for (const auto &k : kinds) {
-    const int64_t tm = (m + k.side - 1) / k.side, tn = (n + k.side - 1) / k.side;
+  for (const auto &t : kinds) {
+    const int64_t tm = (m + t.side - 1) / t.side, tn = (n + t.side - 1) / t.side;
     const int64_t tiles = (symmetric ? tn * (tn + 1) / 2 : tm * tn) * chunk;
-    const int64_t whole = tiles / (256 * k.per_cu), rest = tiles - whole * 256 * k.per_cu;
-    const double tail = rest == 0 ? 0.0 : k.one + (k.full - k.one) * (double)((rest - 1) / 256) / std::max(1, k.per_cu - 1);
-    const double t = (double)whole * k.full + tail;
-    if (!best || t < least) best = k.side, least = t;
+    const int64_t whole = tiles / (256 * t.per_cu), rest = tiles - whole * 256 * t.per_cu;
+    const double its = (double)k / 64, ends = out ? t.out : t.ends;
+    const double time = (double)whole * (its * t.full + ends) +
+                        (rest == 0 ? 0.0 : its * (rest > 256 || whole > 0 ? t.full : t.alone) + ends);
+    if (!best || time < least) best = t.kind, least = time;
   }
   return best;
 }
 
 template <int ROLE>
 void product(const MuonProduct &a, int64_t chunk, hipStream_t s) {
-  switch (pick_tile(a.m, a.n, chunk, ROLE <= kPoly)) {
+  switch (pick_tile(a.m, a.n, a.k, chunk, ROLE <= kPoly, ROLE >= kOut)) {
     case 256: return product_t<Tile256, ROLE>(a, chunk, s);
     case 192: return product_t<Tile192, ROLE>(a, chunk, s);
+    case 129: return product_t<Tile128Deep, ROLE>(a, chunk, s);
     case 128: return product_t<Tile128, ROLE>(a, chunk, s);
     default: return product_t<Tile64, ROLE>(a, chunk, s);
   }

@@ -460,15 +460,17 @@ struct MuonProduct {
 // chunk c of row k lies at c ^ k modulo the chunks in 256 bytes, so that the
 // four rows of a transposing read do.  The copies to LDS write their lanes one
 // after the other; the order is made by which chunk a lane loads.
-template <int BM_, int BN_, int WM_, int WN_, int BK_, int S_>
+template <int BM_, int BN_, int WM_, int WN_, int BK_, int S_, int G_ = 1>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, BK = BK_, S = S_;
+  static constexpr int G = G_, kGroups = BK / 16 / G;   // fragments are read for 16 G of the summed index at a time
+  static_assert(kGroups % 2 == 0 && kGroups * 16 * G == BK, "the two sets of fragments take turns");
   static constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
   static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 32, FN = TN / 32;   // a wave's part, in 32 x 32 products
   static constexpr int LI = BM * BK / 512 / kWaves, RI = BN * BK / 512 / kWaves; // 1 KiB copies of a wave
   static constexpr int kStageBytes = (BM + BN) * BK * 2;
   static_assert(LI * 512 * kWaves == BM * BK && RI * 512 * kWaves == BN * BK, "copies divide evenly among the waves");
-  static_assert(BK == 32 || BK == 64, "LDS orders are made for these");
+  static_assert(BK == 32 || BK == 64 || BK == 128, "LDS orders are made for these");
   static constexpr int kOutBytes = kWaves * 32 * (TM * 4 + 16);   // the epilogue's part of LDS
   static constexpr int kLds = S * kStageBytes > kOutBytes ? S * kStageBytes : kOutBytes;
   static_assert(kLds <= 160 * 1024, "LDS of a CU");
@@ -478,13 +480,13 @@ typedef int int4v __attribute__((ext_vector_type(4)));
 typedef short short4v __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) short4v lds_short4;
 
-// A buffer resource over `bytes` bytes at p (uniform); loads past them give 0.
-__device__ __forceinline__ int4v buffer_of(const char *p, int64_t bytes) {
-  const uint64_t a = (uint64_t)p;
+// A buffer resource over `bytes` bytes at p (uniform); loads past them give 0
+// and touch no memory.
+__device__ __forceinline__ int4v buffer_of(uint64_t p, uint64_t bytes) {
   int4v r;
-  r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
-  r[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32) & 0xffff);
-  r[2] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(bytes < 0xffffffffll ? bytes : 0xffffffffll));
+  r[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)p);
+  r[1] = __builtin_amdgcn_readfirstlane((int)((uint32_t)(p >> 32) & 0xffff));
+  r[2] = __builtin_amdgcn_readfirstlane((int)((uint32_t)(bytes >> 32) ? 0xffffffffu : (uint32_t)bytes));
   r[3] = 0x00020000;
   return r;
 }
@@ -631,73 +633,104 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
 
-  half8 x[2][T::FM], y[2][T::FN];
-  auto fragments = [&](int stage, int ks, half8 *fx, half8 *fy) {
+  constexpr int G = T::G;
+  half8 x[2][T::FM * G], y[2][T::FN * G];
+  auto fragments = [&](int stage, int group, half8 *fx, half8 *fy) {
     const char *p = smem + stage * T::kStageBytes;
 #pragma unroll
-    for (int i = 0; i < T::FM; ++i) fx[i] = panel_read<LC, T::BM, T::BK>(p, wm + 32 * i, ks, lane);
+    for (int g = 0; g < G; ++g) {
 #pragma unroll
-    for (int j = 0; j < T::FN; ++j) fy[j] = panel_read<RC, T::BN, T::BK>(p + T::BM * T::BK * 2, wn + 32 * j, ks, lane);
+      for (int i = 0; i < T::FM; ++i) fx[g * T::FM + i] = panel_read<LC, T::BM, T::BK>(p, wm + 32 * i, group * G + g, lane);
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j)
+        fy[g * T::FN + j] = panel_read<RC, T::BN, T::BK>(p + T::BM * T::BK * 2, wn + 32 * j, group * G + g, lane);
+    }
+  };
+  constexpr int kReads = G * (T::FM * (LC ? 2 : 1) + T::FN * (RC ? 2 : 1)), kProducts = G * T::FM * T::FN;
+  auto product = [&](int at, const half8 *fx, const half8 *fy) {
+    const int g = at / (T::FM * T::FN), j = at / T::FM % T::FN, i = at % T::FM;
+    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fx[g * T::FM + i], fy[g * T::FN + j], acc[i][j], 0, 0, 0);
   };
 
+  // Copies past the last step go to an empty buffer, so that the loop has one
+  // shape and a wait counts the same copies at every step.
   const int nk = (int)(A.k / T::BK);
-  constexpr int kSteps = T::BK / 16;
+  uint64_t al = (uint64_t)pl, ar = (uint64_t)pr, el = (uint64_t)nl, er = (uint64_t)nr;   // of the next step to copy
+  int to_copy = nk;
+  int4v bl, br;
+  auto next_copy = [&]() {
+    bl = buffer_of(al, to_copy > 0 ? el : 0);
+    br = buffer_of(ar, to_copy > 0 ? er : 0);
+    --to_copy;
+    al += (uint64_t)sl, el -= (uint64_t)sl;
+    ar += (uint64_t)sr, er -= (uint64_t)sr;
+  };
 #pragma unroll
-  for (int t = 0; t < T::S; ++t)
-    if (t < nk) {
-      const int4v bl = buffer_of(pl + t * sl, nl - t * sl), br = buffer_of(pr + t * sr, nr - t * sr);
+  for (int t = 0; t < T::S; ++t) {
+    next_copy();
 #pragma unroll
-      for (int i = 0; i < kCopies; ++i) copy(i, bl, br, t);
-    }
-  if (nk >= T::S) stage_wait<(T::S - 1) * kCopies>();
-  else stage_wait<0>();
+    for (int i = 0; i < kCopies; ++i) copy(i, bl, br, t);
+  }
+  stage_wait<(T::S - 1) * kCopies>();
   fragments(0, 0, x[0], y[0]);
   int stage = 0;
   for (int t = 0; t < nk; ++t) {
-#pragma unroll
-    for (int ks = 0; ks < kSteps - 1; ++ks) {
-      // in this order: left alone, the compiler moves the reads behind the products
-      fragments(stage, ks + 1, x[(ks + 1) & 1], y[(ks + 1) & 1]);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int j = 0; j < T::FN; ++j)
-#pragma unroll
-        for (int i = 0; i < T::FM; ++i)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[ks & 1][i], y[ks & 1][j], acc[i][j], 0, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
-    }
     const int next = stage + 1 == T::S ? 0 : stage + 1;
-    const bool refill = t + T::S < nk;
-    if (t + 1 < nk) {
-      // the next stage is whole, and nobody reads this one any more
-      if (t + T::S <= nk) stage_wait<(T::S - 2) * kCopies>();
-      else stage_wait<0>();
-      fragments(next, 0, x[0], y[0]);
+#pragma unroll
+    for (int g = 0; g < T::kGroups; ++g) {
       __builtin_amdgcn_sched_barrier(0);
-    }
-    const int64_t ol = (t + T::S) * sl, orr = (t + T::S) * sr;
-    const int4v bl = buffer_of(pl + ol, nl - ol), br = buffer_of(pr + orr, nr - orr);
+      if (g + 1 < T::kGroups) {
+        fragments(stage, g + 1, x[(g + 1) & 1], y[(g + 1) & 1]);
 #pragma unroll
-    for (int j = 0; j < T::FN; ++j)
+        for (int q = 0; q < kProducts; ++q) product(q, x[g & 1], y[g & 1]);
+        // products and reads in turn; left alone, the compiler moves the reads
+        // behind the products
+        constexpr int kEach = (kReads + kProducts - 1) / kProducts;
 #pragma unroll
-      for (int i = 0; i < T::FM; ++i) {
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[1][i], y[1][j], acc[i][j], 0, 0, 0);
-        // the copies are spread over the products
-        constexpr int kEach = (kCopies + T::FM * T::FN - 1) / (T::FM * T::FN);
-        const int q = j * T::FM + i;
-        if (refill) {
-#pragma unroll
-          for (int c = q * kEach; c < (q + 1) * kEach && c < kCopies; ++c) copy(c, bl, br, stage);
+        for (int q = 0; q < kReads; q += kEach) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);
         }
+        continue;
       }
-    __builtin_amdgcn_sched_barrier(0);
+      // the next stage is whole, and nobody reads this one any more
+      stage_wait<(T::S - 2) * kCopies>();
+      fragments(next, 0, x[0], y[0]);
+      next_copy();
+      __builtin_amdgcn_sched_barrier(0);
+      constexpr int kEach = (kCopies + kProducts - 1) / kProducts;
+#pragma unroll
+      for (int q = 0; q < kProducts; ++q) {
+        product(q, x[1], y[1]);
+        // the copies that refill this stage are spread over the products
+#pragma unroll
+        for (int c = q * kEach; c < (q + 1) * kEach && c < kCopies; ++c) copy(c, bl, br, stage);
+      }
+    }
     stage = next;
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();   // the stages' LDS is the epilogue's now
 
   // Each wave brings 32 rows (n) x TM of its part through LDS at a time, so
   // that memory is written in whole runs of a row.
   char *mine = smem + wave * (32 * (T::TM * 4 + 16));
+  // kPoly: A's part of the tile, whole rows at a time and all reads under way
+  // together (read four elements at a time by the lanes that need them, it
+  // took 20 000 cycles of a 192 x 192 tile's 150 000)
+  constexpr int kRowChunks = T::TM / 8, kATrips = ROLE == kPoly ? 32 * kRowChunks / 64 : 1;
+  half8 olda[ROLE == kPoly ? T::FN : 1][kATrips];
+  if (ROLE == kPoly) {
+#pragma unroll
+    for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+      for (int g = 0; g < kATrips; ++g) {
+        const int row = (g * 64 + lane) / kRowChunks, c = (g * 64 + lane) % kRowChunks;
+        const int64_t nn = n0 + wn + 32 * j + row, mm = m0 + wm + 8 * c;
+        olda[j][g] = half8{0, 0, 0, 0, 0, 0, 0, 0};
+        if (nn < A.n && mm < A.m) olda[j][g] = *(const half8 *)(A.l + lb * A.l_mat + nn * A.m + mm);
+      }
+  }
 #pragma unroll
   for (int j = 0; j < T::FN; ++j) {
     const int64_t nb = n0 + wn + 32 * j, mb = m0 + wm;
@@ -744,6 +777,14 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
     constexpr int kStride = T::TM * 2 + 16;
     const int64_t dn = A.m;   // elements of a row of D
     _Float16 *d = A.d + lb * A.m * A.n;
+    if (ROLE == kPoly) {
+#pragma unroll
+      for (int g = 0; g < kATrips; ++g) {
+        const int row = (g * 64 + lane) / kRowChunks, c = (g * 64 + lane) % kRowChunks;
+        *(half8 *)(mine + row * kStride + c * 16) = olda[j][g];
+      }
+      wave_lds_fence();
+    }
 #pragma unroll
     for (int i = 0; i < T::FM; ++i)
 #pragma unroll
@@ -751,7 +792,7 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
         const int r = 32 * i + 8 * q + 4 * (lane >> 5);
         const int64_t nn = nb + (lane & 31), mm = mb + r;   // and the next three
         half4 h, s = {0, 0, 0, 0};
-        if (ROLE == kPoly && nn < A.n && mm < A.m) s = *(const half4 *)(A.l + lb * A.l_mat + nn * dn + mm);
+        if (ROLE == kPoly) s = *(const half4 *)(mine + (lane & 31) * kStride + r * 2);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float v = acc[i][j][4 * q + e];
@@ -767,10 +808,9 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
         *(half4 *)(mine + (lane & 31) * kStride + r * 2) = h;
       }
     wave_lds_fence();
-    constexpr int kChunks = T::TM / 8;
 #pragma unroll
-    for (int g = lane; g < 32 * kChunks; g += 64) {
-      const int row = g / kChunks, c = g % kChunks;
+    for (int g = lane; g < 32 * kRowChunks; g += 64) {
+      const int row = g / kRowChunks, c = g % kRowChunks;
       const half8 h = *(const half8 *)(mine + row * kStride + c * 16);
       if (nb + row < A.n && mb + 8 * c < A.m) *(half8 *)(d + (nb + row) * dn + mb + 8 * c) = h;
     }
