@@ -219,14 +219,14 @@ hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonTarg
     hipLaunchKernelGGL((muon_norm_kernel<MOM>), dim3((unsigned)p.nparts, (unsigned)cb), dim3(256), 0, s, in,
                        p.run, b0, part, p.nparts);
     const int64_t sp = p.tall ? p.np : p.mp, tp = p.tall ? p.mp : p.np;
-    const dim3 lg((unsigned)((sp + 4 * p.run.lanes - 1) / (4 * p.run.lanes)), (unsigned)((tp + kLoadRows - 1) / kLoadRows), (unsigned)cb);
     _Float16 *x = x0, *nx = x1;
-    if (p.tall)
-      hipLaunchKernelGGL((muon_load_kernel<MOM, true>), lg, dim3(256), 0, s, in, p.run, b0, part, p.nparts, eps, x,
-                         sp, tp);
-    else
-      hipLaunchKernelGGL((muon_load_kernel<MOM, false>), lg, dim3(256), 0, s, in, p.run, b0, part, p.nparts, eps, x,
-                         sp, tp);
+    const int64_t across = (sp + 4 * p.run.lanes - 1) / (4 * p.run.lanes);
+    const bool few = across * ((tp + 63) / 64) * cb < 512;
+    const int rows = few ? 16 : 64;
+    const dim3 lg((unsigned)across, (unsigned)((tp + rows - 1) / rows), (unsigned)cb);
+    const auto load = p.tall ? (few ? muon_load_kernel<MOM, true, 16> : muon_load_kernel<MOM, true, 64>)
+                             : (few ? muon_load_kernel<MOM, false, 16> : muon_load_kernel<MOM, false, 64>);
+    hipLaunchKernelGGL(load, lg, dim3(256), 0, s, in, p.run, b0, part, p.nparts, eps, x, sp, tp);
     for (int t = 0; t < steps; ++t) {
       MuonProduct a = {};
       a.a = k.v[t][0], a.b = k.v[t][1], a.c = k.v[t][2];

@@ -142,6 +142,29 @@ __device__ __forceinline__ void muon_elems(const MuonInput &I, const MuonRaw &R,
   }
 }
 
+// Another lane's value by data-parallel primitives (a permute through LDS would
+// take ten times as long).  kCtrl: 0xb1 and 0x4e exchange lanes within four,
+// 0x141 and 0x140 mirror eight and sixteen.
+template <int kCtrl>
+__device__ __forceinline__ double dpp_f64(double v) {
+  union { double d; int i[2]; } a, b;
+  a.d = v;
+  b.i[0] = __builtin_amdgcn_mov_dpp(a.i[0], kCtrl, 0xf, 0xf, true);
+  b.i[1] = __builtin_amdgcn_mov_dpp(a.i[1], kCtrl, 0xf, 0xf, true);
+  return b.d;
+}
+
+// The largest of `lanes` consecutive lanes' values (a power of two), in all of them.
+__device__ __forceinline__ double lanes_max(double v, int lanes) {
+  if (lanes > 1) v = fmax(v, dpp_f64<0xb1>(v));
+  if (lanes > 2) v = fmax(v, dpp_f64<0x4e>(v));
+  if (lanes > 4) v = fmax(v, dpp_f64<0x141>(v));
+  if (lanes > 8) v = fmax(v, dpp_f64<0x140>(v));
+  if (lanes > 16) v = fmax(v, __shfl_xor(v, 16, 64));
+  if (lanes > 32) v = fmax(v, __shfl_xor(v, 32, 64));
+  return v;
+}
+
 // Writes their new momentum.  kMom8: `lanes` consecutive lanes hold a block of
 // 256 (or the row's short last one, or the whole of a shorter row), and `first`
 // is true in the one that holds its first element.  All lanes of a wave call it.
@@ -166,10 +189,20 @@ __device__ __forceinline__ void muon_store_momentum(const MuonInput &I, const Mu
   double top = 0.0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) top = fmax(top, m64[e] == m64[e] ? fabs(m64[e]) : (double)__builtin_inff());
-  for (int o = lanes >> 1; o >= 1; o >>= 1) top = fmax(top, __shfl_xor(top, o, 64));
+  top = lanes_max(top, lanes);
   const bool bad = !(top < (double)__builtin_inff());
-  const float step = bad ? __builtin_nanf("") : (float)(top / 127.0);
-  const double inv = step > 0.f ? 1.0 / (double)step : 0.0;
+  // top / 127 and 1 / step by a reciprocal and corrections; the operands are far
+  // from the ends of fp64's range, so a division's scaling is not needed
+  double quot = top * (1.0 / 127.0);
+  quot = fma(fma(-127.0, quot, top), 1.0 / 127.0, quot);
+  const float step = bad ? __builtin_nanf("") : (float)quot;
+  double inv = 0.0;
+  if (step > 0.f) {
+    const double d = (double)step;
+    inv = __builtin_amdgcn_rcp(d);
+    inv = fma(fma(-d, inv, 1.0), inv, inv);
+    inv = fma(fma(-d, inv, 1.0), inv, inv);
+  }
   uint32_t w = 0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
@@ -282,11 +315,10 @@ __device__ __forceinline__ double muon_scale(double squares, float eps) {
 // ------------------------------------------------------------------ momentum, X0
 // Writes the new momentum, and X0 in its wide orientation with zeros in the
 // padding: as the matrix is stored, or transposed if that is tall.  A block of
-// 256 threads takes 64 rows x 4 * run.lanes columns of the stored matrix.  sp,
-// tp: the stored orientation's padded columns and rows.
-constexpr int kLoadRows = 64;
-
-template <int MOM, bool TALL>
+// 256 threads takes kLoadRows rows x 4 * run.lanes columns of the stored
+// matrix: 64, or 16 where that gives few blocks (768 x 768: 36 blocks take 11
+// us, 144 take 5).  sp, tp: the stored orientation's padded columns and rows.
+template <int MOM, bool TALL, int kLoadRows>
 __global__ __launch_bounds__(256) void muon_load_kernel(MuonInput I, MuonRun run, int64_t b0, const double *part, int nparts,
                                                         float eps, _Float16 *X, int64_t sp, int64_t tp) {
   __shared__ double s4[4];
@@ -333,9 +365,10 @@ __global__ __launch_bounds__(256) void muon_load_kernel(MuonInput I, MuonRun run
   }
   if (!TALL) return;
   __syncthreads();
-  // transposed: 8 consecutive rows of a column to a lane, 8 lanes to a column
-  const int rg = (int)(threadIdx.x & 7u);
-  for (int cc = (int)(threadIdx.x >> 3); cc < 4 * run.lanes; cc += 32) {
+  // transposed: 8 consecutive rows of a column to a lane
+  constexpr int kOcts = kLoadRows / 8;
+  const int rg = (int)threadIdx.x % kOcts;
+  for (int cc = (int)threadIdx.x / kOcts; cc < 4 * run.lanes; cc += 256 / kOcts) {
     half8 h;
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[e] = tile[8 * rg + e][cc];
@@ -352,66 +385,73 @@ struct MuonTarget {
   float decay, rate;
 };
 
-// Four consecutive sums of the last product, v[e], to the elements from
-// at + e step on, for e < N: as many as lie inside the matrix, left - e dj
-// columns of them if fewer than `rows` rows e di have gone by.  All old values
-// are read before the first is written, so that the reads are under way
-// together.
-template <int N>
-__device__ __forceinline__ void write_out(const MuonTarget &T, int64_t at, int64_t step, int rows, int left, int di, int dj,
-                                          const float (*v)[4]) {
-  constexpr float kUnit = 1.f / (kScaleX * kScaleP);
-  float old[N][4];
-  if (T.update) {
+// Four consecutive elements of it: where, how many are inside the matrix (n, as
+// in MuonSpot), and what they held (32-bit values, or 16-bit ones in pairs).
+// Reading and writing are apart, so that the reads are under way while other
+// elements are written.
+struct MuonOld {
+  int64_t at;
+  int n;
+  uint32_t w[4];
+};
+
+__device__ __forceinline__ MuonOld read_out(const MuonTarget &T, int64_t at, int n) {
+  MuonOld o = {at, n, {0u, 0u, 0u, 0u}};
+  if (!T.update) return o;
+  if (T.bf16) {
+    const uint16_t *p = (const uint16_t *)T.out + at;
+    if (T.vec && n >= 4) {
+      const uint2 w = *(const uint2 *)p;
+      o.w[0] = w.x, o.w[1] = w.y;
+    } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const int n = e * di < rows ? left - e * dj : 0;
-      if (T.bf16) {
-        const uint16_t *p = (const uint16_t *)T.out + (at + e * step);
-        if (T.vec && n >= 4) {
-          const uint2 w = *(const uint2 *)p;
-          old[e][0] = __uint_as_float(w.x << 16), old[e][1] = __uint_as_float(w.x & 0xffff0000u);
-          old[e][2] = __uint_as_float(w.y << 16), old[e][3] = __uint_as_float(w.y & 0xffff0000u);
-        } else {
+      for (int f = 0; f < 4; ++f)
+        if (f < n) o.w[f >> 1] |= (uint32_t)p[f] << (16 * (f & 1));
+    }
+  } else {
+    const uint32_t *p = (const uint32_t *)T.out + at;
+    if (T.vec && n >= 4) {
+      const uint4 w = *(const uint4 *)p;
+      o.w[0] = w.x, o.w[1] = w.y, o.w[2] = w.z, o.w[3] = w.w;
+    } else {
 #pragma unroll
-          for (int f = 0; f < 4; ++f) old[e][f] = f < n ? bf16_f32(p[f]) : 0.f;
-        }
-      } else {
-        const float *p = (const float *)T.out + (at + e * step);
-        if (T.vec && n >= 4) {
-          const float4 w = *(const float4 *)p;
-          old[e][0] = w.x, old[e][1] = w.y, old[e][2] = w.z, old[e][3] = w.w;
-        } else {
-#pragma unroll
-          for (int f = 0; f < 4; ++f) old[e][f] = f < n ? p[f] : 0.f;
-        }
-      }
+      for (int f = 0; f < 4; ++f)
+        if (f < n) o.w[f] = p[f];
     }
   }
+  return o;
+}
+
+// Four consecutive sums of the last product go there.
+__device__ __forceinline__ void write_out(const MuonTarget &T, const MuonOld &o, float4 sums) {
+  constexpr float kUnit = 1.f / (kScaleX * kScaleP);
+  const float v[4] = {sums.x * kUnit, sums.y * kUnit, sums.z * kUnit, sums.w * kUnit};
+  float x[4];
+  if (T.bf16) {
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
-    const int n = e * di < rows ? left - e * dj : 0;
-    float x[4];
-#pragma unroll
-    for (int f = 0; f < 4; ++f) x[f] = T.update ? old[e][f] * T.decay - T.rate * (v[e][f] * kUnit) : v[e][f] * kUnit;
-    if (T.bf16) {
-      uint16_t *p = (uint16_t *)T.out + (at + e * step);
-      if (T.vec && n >= 4) {
-        *(uint2 *)p = make_uint2(f32x2_bf16(x[0], x[1]), f32x2_bf16(x[2], x[3]));
-      } else {
-#pragma unroll
-        for (int f = 0; f < 4; ++f)
-          if (f < n) p[f] = (uint16_t)f32x2_bf16(x[f], 0.f);
-      }
+    for (int f = 0; f < 4; ++f) {
+      const float old = __uint_as_float(f & 1 ? o.w[f >> 1] & 0xffff0000u : o.w[f >> 1] << 16);
+      x[f] = T.update ? old * T.decay - T.rate * v[f] : v[f];
+    }
+    uint16_t *p = (uint16_t *)T.out + o.at;
+    const uint32_t lo = f32x2_bf16(x[0], x[1]), hi = f32x2_bf16(x[2], x[3]);
+    if (T.vec && o.n >= 4) {
+      *(uint2 *)p = make_uint2(lo, hi);
     } else {
-      float *p = (float *)T.out + (at + e * step);
-      if (T.vec && n >= 4) {
-        *(float4 *)p = make_float4(x[0], x[1], x[2], x[3]);
-      } else {
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
-          if (f < n) p[f] = x[f];
-      }
+      for (int f = 0; f < 4; ++f)
+        if (f < o.n) p[f] = (uint16_t)((f < 2 ? lo : hi) >> (16 * (f & 1)));
+    }
+  } else {
+#pragma unroll
+    for (int f = 0; f < 4; ++f) x[f] = __uint_as_float(o.w[f]) * T.decay - T.rate * v[f];
+    float *p = (float *)T.out + o.at;
+    if (T.vec && o.n >= 4) {
+      *(float4 *)p = make_float4(x[0], x[1], x[2], x[3]);
+    } else {
+#pragma unroll
+      for (int f = 0; f < 4; ++f)
+        if (f < o.n) p[f] = x[f];
     }
   }
 }
@@ -731,10 +771,22 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
         if (nn < A.n && mm < A.m) olda[j][g] = *(const half8 *)(A.l + lb * A.l_mat + nn * A.m + mm);
       }
   }
+  constexpr int kOutChunks = T::TM / 4, kOutTrips = 32 * kOutChunks / 64;
+  auto out_spot = [&](int j, int g) {
+    const int row = (g * 64 + lane) / kOutChunks, c = (g * 64 + lane) % kOutChunks;
+    const int64_t nn = n0 + wn + 32 * j + row, mm = m0 + wm + 4 * c;
+    return read_out(A.out, (A.b0 + lb) * A.out.batch + nn * A.out.row + mm, nn < A.out.rows ? (int)(A.out.cols - mm) : 0);
+  };
+  MuonOld old[OUT ? kOutTrips : 1];
+  if (OUT) {
+#pragma unroll
+    for (int g = 0; g < kOutTrips; ++g) old[g] = out_spot(0, g);
+  }
 #pragma unroll
   for (int j = 0; j < T::FN; ++j) {
     const int64_t nb = n0 + wn + 32 * j, mb = m0 + wm;
     if (OUT) {
+      float4 v[kOutTrips];
       constexpr int kStride = T::TM * 4 + 16;
 #pragma unroll
       for (int i = 0; i < T::FM; ++i)
@@ -743,33 +795,17 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
           *(float4 *)(mine + (lane & 31) * kStride + (32 * i + 8 * q + 4 * (lane >> 5)) * 4) =
               make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
       wave_lds_fence();
-      // a row's TM / 4 chunks lie beside each other; 64 lanes take whole rows
-      constexpr int kChunks = T::TM / 4, kTrips = 32 * kChunks / 64, kOnce = kTrips % 4 == 0 ? 4 : 2;
-      static_assert(kTrips % kOnce == 0, "whole groups");
 #pragma unroll
-      for (int g = 0; g < kTrips; g += kOnce) {
-        float v[kOnce][4];
-        // chunks of one lane: kOnce rows apart by the same step where a trip is whole rows
-        if (64 % kChunks == 0) {
-          const int row = (g * 64 + lane) / kChunks, c = lane % kChunks;
-          const int64_t to = (A.b0 + lb) * A.out.batch + (nb + row) * A.out.row + mb + 4 * c;
+      for (int g = 0; g < kOutTrips; ++g) {
+        const int row = (g * 64 + lane) / kOutChunks, c = (g * 64 + lane) % kOutChunks;
+        v[g] = *(const float4 *)(mine + row * kStride + c * 16);
+      }
+      // the old values of the next 32 rows are read before these are written
 #pragma unroll
-          for (int e = 0; e < kOnce; ++e) {
-            const float4 w = *(const float4 *)(mine + (row + e * (64 / kChunks)) * kStride + c * 16);
-            v[e][0] = w.x, v[e][1] = w.y, v[e][2] = w.z, v[e][3] = w.w;
-          }
-          write_out<kOnce>(A.out, to, (64 / kChunks) * A.out.row, (int)(A.out.rows - nb) - row, (int)(A.out.cols - mb) - 4 * c,
-                           64 / kChunks, 0, v);
-        } else {
-#pragma unroll
-          for (int e = 0; e < kOnce; ++e) {
-            const int at = (g + e) * 64 + lane, row = at / kChunks, c = at % kChunks;
-            const float4 w = *(const float4 *)(mine + row * kStride + c * 16);
-            v[0][0] = w.x, v[0][1] = w.y, v[0][2] = w.z, v[0][3] = w.w;
-            write_out<1>(A.out, (A.b0 + lb) * A.out.batch + (nb + row) * A.out.row + mb + 4 * c, 0,
-                         (int)(A.out.rows - nb) - row, (int)(A.out.cols - mb) - 4 * c, 0, 0, v);
-          }
-        }
+      for (int g = 0; g < kOutTrips; ++g) {
+        const MuonOld o = old[g];
+        if (j + 1 < T::FN) old[g] = out_spot(j + 1, g);
+        write_out(A.out, o, v[g]);
       }
       wave_lds_fence();
       continue;
@@ -1107,15 +1143,26 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonInput 
       const char *pp = P + (32 * ib + row) * L::kRow + 16 * half;
       if (S.tall) {
         // rows of the result are columns of X: a lane has four consecutive elements of one
+        MuonOld old[4];
+        const int i = 32 * jp + row, j = 32 * ib + 4 * half;
+        const int n = i < (int)out.rows ? (int)out.cols - j : 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) old[q] = read_out(out, b * out.batch + i * out.row + j + 8 * q, n - 8 * q);
 #pragma unroll
         for (int k = 0; k < 2 * NB; ++k)
           acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8 *)(pp + 32 * k), x[k], acc, 0, 0, 0);
-        float v[4][4];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) v[e >> 2][e & 3] = left * acc[e];
-        const int i = 32 * jp + row, j = 32 * ib + 4 * half;
-        write_out<4>(out, b * out.batch + i * out.row + j, 8, (int)out.rows - i, (int)out.cols - j, 0, 8, v);
+        for (int q = 0; q < 4; ++q)
+          write_out(out, old[q], make_float4(left * acc[4 * q], left * acc[4 * q + 1], left * acc[4 * q + 2], left * acc[4 * q + 3]));
         continue;
+      }
+      // of the 32 rows of this block a lane writes r, r + 8, .., columns 4c..
+      const int r = lane >> 3, c = lane & 7;
+      MuonOld old[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = 32 * ib + r + 8 * e, j = 32 * jp + 4 * c;
+        old[e] = read_out(out, b * out.batch + i * out.row + j, i < (int)out.rows ? (int)out.cols - j : 0);
       }
 #pragma unroll
       for (int k = 0; k < 2 * NB; ++k)
@@ -1132,15 +1179,9 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonInput 
                 make_float4(left * acc[4 * q], left * acc[4 * q + 1], left * acc[4 * q + 2], left * acc[4 * q + 3]);
         }
         wave_lds_fence();
-        float v[2][4];
-        const int r = lane >> 3, c = lane & 7;   // rows r and r + 8, columns 4c..
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float4 w = *(const float4 *)(X + (2 * (r + 8 * e) + (c >> 2)) * xrow + 64 * jp + (c & 3) * 16);
-          v[e][0] = w.x, v[e][1] = w.y, v[e][2] = w.z, v[e][3] = w.w;
-        }
-        const int i = 32 * ib + 16 * p + r, j = 32 * jp + 4 * c;
-        write_out<2>(out, b * out.batch + i * out.row + j, 8 * out.row, (int)out.rows - i, (int)out.cols - j, 8, 0, v);
+        for (int e = 0; e < 2; ++e)
+          write_out(out, old[2 * p + e], *(const float4 *)(X + (2 * (r + 8 * e) + (c >> 2)) * xrow + 64 * jp + (c & 3) * 16));
         wave_lds_fence();
       }
     }
