@@ -44,6 +44,56 @@ bool fits_small(int64_t n, int64_t m, uint32_t runs) {
   return bytes > 0 && bytes <= 160 * 1024 && runs <= (uint32_t)(kSmallWaves * (n <= 32 ? SmallLds<1>::kRuns : SmallLds<4>::kRuns));
 }
 
+using Tile64 = Tile<64, 64, 2, 2, 64, 4, 2>;
+using Tile128 = Tile<128, 128, 2, 2, 64, 2>;
+using Tile128Deep = Tile<128, 128, 4, 2, 64, 4>;   // alone on a CU
+using Tile192 = Tile<192, 192, 2, 2, 64, 2>;
+using Tile256 = Tile<256, 256, 4, 2, 64, 2>;
+
+// How a product is made: which tile, and (X X^T) in how many parts.
+struct Choice {
+  int kind;
+  int parts;
+  size_t bytes;   // the parts' sums
+};
+
+// The tile with the shortest expected time.  Workgroups go over the 256 CUs in
+// rounds; a round takes so long for 64 of the summed index and so long for its
+// beginning and end (microseconds, measured on products that fill the card and
+// on ones that do not; "alone": at most one workgroup on a CU).  Large tiles
+// read less for each product; smaller ones waste less of the last round and of
+// the half that a symmetric result leaves out (n = 4096: 136 tiles of 256 take
+// 240 us where 253 of 192 take 197).  Where parameters are read and written
+// (`out`), the end is bound by memory, and two workgroups to a CU hide it.
+// Parts of the summed index fill the card where there are few tiles; their sums
+// cost another launch and their way through memory.
+Choice pick(int64_t m, int64_t n, int64_t k, int64_t chunk, bool symmetric, bool out, bool may_split) {
+  const struct { int kind, side, per_cu; double alone, full, ends, out; } kinds[] = {
+      {256, 256, 1, 1.76, 1.76, 5.0, 14.0},
+      {192, 192, 1, 1.14, 1.14, 4.0, 10.0},
+      {128, 128, 2, 0.60, 1.02, 3.5, 6.0},
+      {129, 128, 1, 0.45, 0.95, 3.5, 6.0},
+      {64, 64, 2, 0.26, 0.40, 2.5, 3.5}};
+  Choice best = {0, 1, 0};
+  double least = 0.0;
+  for (const auto &t : kinds) {
+    const int64_t tm = (m + t.side - 1) / t.side, tn = (n + t.side - 1) / t.side;
+    const int64_t tiles = (symmetric ? tn * (tn + 1) / 2 : tm * tn) * chunk;
+    for (int parts = 1; parts <= (may_split && t.side <= 128 ? 32 : 1) && (parts == 1 || k / 64 >= 4 * parts); parts *= 2) {
+      const int64_t groups = tiles * parts, whole = groups / (256 * t.per_cu), rest = groups - whole * 256 * t.per_cu;
+      const double its = (double)((k / 64 + parts - 1) / parts), ends = out ? t.out : t.ends;
+      const size_t bytes = parts > 1 ? (size_t)groups * t.side * t.side * 4 : 0;
+      if (bytes > (size_t)64 << 20) break;
+      double time = (double)whole * (its * t.full + ends) +
+                    (rest == 0 ? 0.0 : its * (rest > 256 || whole > 0 ? t.full : t.alone) + ends);
+      // their sums are written and read at 3 TB/s, by a tile's workgroup at 0.1
+      if (parts > 1) time += 4.0 + (double)bytes / 3e6 + std::max((double)bytes / 3e6, (double)bytes / (double)tiles / 1e5);
+      if (!best.kind || time < least) best = {t.kind, parts, bytes}, least = time;
+    }
+  }
+  return best;
+}
+
 // How a batch of r x c matrices is cut and laid out in the workspace.
 struct Plan {
   int64_t r, c, n, m;       // n <= m: the wide orientation's sides
@@ -54,7 +104,8 @@ struct Plan {
   MuonRun run;              // how waves go over the stored matrix
   uint32_t runs;
   int nparts;
-  size_t x_bytes, a_bytes, part_bytes, bytes;
+  Choice gram, poly, update, last;   // tiles of the products of `chunk` matrices
+  size_t x_bytes, a_bytes, part_bytes, sum_bytes, bytes;
 
   Plan(int64_t batch, int64_t rows, int64_t cols) : r(rows), c(cols) {
     tall = r > c;
@@ -62,10 +113,13 @@ struct Plan {
     m = std::max(r, c);
     np = round_up(n, 64);
     mp = round_up(m, 64);
-    run.lanes = 64;
-    while (run.lanes > 1 && 2 * run.lanes >= c) run.lanes /= 2;   // 4 columns to a lane
-    run.segs = (uint32_t)((c + 4 * run.lanes - 1) / (4 * run.lanes));
-    runs = (uint32_t)((r + 64 / run.lanes - 1) / (64 / run.lanes)) * run.segs;
+    run.log_lanes = 6;
+    while (run.log_lanes > 0 && (2 << run.log_lanes) >= c) --run.log_lanes;   // 4 columns to a lane
+    const int64_t wide = 4 << run.log_lanes, at_once = 64 >> run.log_lanes;
+    run.segs = (int)((c + wide - 1) / wide);
+    run.groups = (int)((r + at_once - 1) / at_once);
+    run.blocks = (int)((c + kMomentumBlock - 1) / kMomentumBlock);
+    runs = (uint32_t)run.groups * (uint32_t)run.segs;
     nparts = (int)std::min<int64_t>(kNormParts, (runs + 15) / 16);   // four runs to a wave
     const size_t one = 2 * 2 * (size_t)(np * mp) + 2 * 2 * (size_t)(np * np) + 8 * (size_t)nparts;
     chunk = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(batch, 65535), (int64_t)(kWorkspaceAim / one)));
@@ -73,7 +127,12 @@ struct Plan {
     a_bytes = (size_t)round_up(2 * chunk * np * np, 256);
     part_bytes = (size_t)round_up(8 * chunk * nparts, 256);
     small = fits_small(n, m, runs);
-    bytes = small ? 256 : 2 * x_bytes + 2 * a_bytes + part_bytes;
+    gram = pick(np, np, mp, chunk, true, false, true);
+    poly = pick(np, np, np, chunk, true, false, false);
+    update = pick(mp, np, np, chunk, false, false, false);
+    last = pick(mp, np, np, chunk, false, true, false);
+    sum_bytes = (size_t)round_up((int64_t)gram.bytes, 256);
+    bytes = small ? 256 : 2 * x_bytes + 2 * a_bytes + part_bytes + sum_bytes;
   }
 };
 
@@ -117,54 +176,25 @@ bool coefficients_ok(const float *k, int steps, const char **why) {
   return true;
 }
 
-using Tile64 = Tile<64, 64, 2, 2, 64, 4, 2>;
-using Tile128 = Tile<128, 128, 2, 2, 64, 2>;
-using Tile128Deep = Tile<128, 128, 4, 2, 64, 4>;   // alone on a CU
-using Tile192 = Tile<192, 192, 2, 2, 64, 2>;
-using Tile256 = Tile<256, 256, 4, 2, 64, 2>;
-
 template <class T, int ROLE>
 void product_t(MuonProduct a, int64_t chunk, hipStream_t s) {
   a.tiles_m = (int)((a.m + T::BM - 1) / T::BM);
   a.tiles_n = (int)((a.n + T::BN - 1) / T::BN);
-  a.tiles = ROLE <= kPoly ? a.tiles_n * (a.tiles_n + 1) / 2 : a.tiles_m * a.tiles_n;
-  hipLaunchKernelGGL((muon_product_kernel<T, ROLE>), dim3((unsigned)(a.tiles * chunk)), dim3(T::kThreads), 0, s, a);
-}
-
-// The tile with the shortest expected time.  Workgroups go over the 256 CUs in
-// rounds; a round takes so long for 64 of the summed index and so long for its
-// beginning and end (microseconds, measured on products that fill the card and
-// on ones that do not; "alone": at most one workgroup on a CU).  Large tiles
-// read less for each product; smaller ones waste less of the last round and of
-// the half that a symmetric result leaves out (n = 4096: 136 tiles of 256 take
-// 240 us where 253 of 192 take 197).  Where parameters are read and written
-// (`out`), the end is bound by memory, and two workgroups to a CU hide it.
-int pick_tile(int64_t m, int64_t n, int64_t k, int64_t chunk, bool symmetric, bool out) {
-  const struct { int kind, side, per_cu; double alone, full, ends, out; } kinds[] = {
-      {256, 256, 1, 1.76, 1.76, 5.0, 14.0},
-      {192, 192, 1, 1.14, 1.14, 4.0, 10.0},
-      {128, 128, 2, 0.60, 1.02, 3.5, 6.0},
-      {129, 128, 1, 0.45, 0.95, 3.5, 6.0},
-      {64, 64, 2, 0.26, 0.40, 2.5, 3.5}};
-  int best = 0;
-  double least = 0.0;
-  for (const auto &t : kinds) {
-    const int64_t tm = (m + t.side - 1) / t.side, tn = (n + t.side - 1) / t.side;
-    const int64_t tiles = (symmetric ? tn * (tn + 1) / 2 : tm * tn) * chunk;
-    const int64_t whole = tiles / (256 * t.per_cu), rest = tiles - whole * 256 * t.per_cu;
-    const double its = (double)k / 64, ends = out ? t.out : t.ends;
-    const double time = (double)whole * (its * t.full + ends) +
-                        (rest == 0 ? 0.0 : its * (rest > 256 || whole > 0 ? t.full : t.alone) + ends);
-    if (!best || time < least) best = t.kind, least = time;
-  }
-  return best;
+  a.tiles = ROLE == kUpdate || ROLE == kOut || ROLE == kOutTall ? a.tiles_m * a.tiles_n : a.tiles_n * (a.tiles_n + 1) / 2;
+  const int64_t groups = (int64_t)a.tiles * (ROLE == kGramPart ? a.parts : 1);
+  if (ROLE != kGramPart && ROLE != kGramSum) a.parts = 1;
+  // small tiles: a row of the grid for each matrix; else the kernel divides
+  const dim3 grid = T::BM == 64 ? dim3((unsigned)groups, (unsigned)chunk) : dim3((unsigned)(groups * chunk));
+  hipLaunchKernelGGL((muon_product_kernel<T, ROLE>), grid, dim3(T::kThreads), 0, s, a);
 }
 
 template <int ROLE>
-void product(const MuonProduct &a, int64_t chunk, hipStream_t s) {
-  switch (pick_tile(a.m, a.n, a.k, chunk, ROLE <= kPoly, ROLE >= kOut)) {
-    case 256: return product_t<Tile256, ROLE>(a, chunk, s);
-    case 192: return product_t<Tile192, ROLE>(a, chunk, s);
+void product(const MuonProduct &a, int64_t chunk, int kind, hipStream_t s) {
+  if constexpr (ROLE != kGramPart && ROLE != kGramSum) {
+    if (kind == 256) return product_t<Tile256, ROLE>(a, chunk, s);
+    if (kind == 192) return product_t<Tile192, ROLE>(a, chunk, s);
+  }
+  switch (kind) {
     case 129: return product_t<Tile128Deep, ROLE>(a, chunk, s);
     case 128: return product_t<Tile128, ROLE>(a, chunk, s);
     default: return product_t<Tile64, ROLE>(a, chunk, s);
@@ -213,6 +243,7 @@ hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonTarg
   _Float16 *x0 = (_Float16 *)w, *x1 = (_Float16 *)(w + p.x_bytes);
   _Float16 *ga = (_Float16 *)(w + 2 * p.x_bytes), *gp = (_Float16 *)(w + 2 * p.x_bytes + p.a_bytes);
   double *part = (double *)(w + 2 * p.x_bytes + 2 * p.a_bytes);
+  float *sums = (float *)(w + 2 * p.x_bytes + 2 * p.a_bytes + p.part_bytes);
   const int64_t nm = p.np * p.mp, nn = p.np * p.np;
   for (int64_t b0 = 0; b0 < batch; b0 += p.chunk) {
     const int64_t cb = std::min(p.chunk, batch - b0);
@@ -220,7 +251,7 @@ hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonTarg
                        p.run, b0, part, p.nparts);
     const int64_t sp = p.tall ? p.np : p.mp, tp = p.tall ? p.mp : p.np;
     _Float16 *x = x0, *nx = x1;
-    const int64_t across = (sp + 4 * p.run.lanes - 1) / (4 * p.run.lanes);
+    const int64_t wide = 4 << p.run.log_lanes, across = (sp + wide - 1) / wide;
     const bool few = across * ((tp + 63) / 64) * cb < 512;
     const int rows = few ? 16 : 64;
     const dim3 lg((unsigned)across, (unsigned)((tp + rows - 1) / rows), (unsigned)cb);
@@ -235,17 +266,24 @@ hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonTarg
       a.l_ld = a.r_ld = a.k = p.mp;
       a.m = a.n = p.np;
       a.d = ga;
-      product<kGram>(a, cb, s);
+      if (p.gram.parts > 1) {
+        a.parts = p.gram.parts;
+        a.sums = sums;
+        product<kGramPart>(a, cb, p.gram.kind, s);
+        product<kGramSum>(a, cb, p.gram.kind, s);
+      } else {
+        product<kGram>(a, cb, p.gram.kind, s);
+      }
       a.l = a.r = ga;
       a.l_mat = a.r_mat = nn;
       a.l_ld = a.r_ld = a.k = p.np;
       a.d = gp;
-      product<kPoly>(a, cb, s);
+      product<kPoly>(a, cb, p.poly.kind, s);
       a.l = x, a.l_mat = nm, a.l_ld = a.m = p.mp;
       a.r = gp;
       if (t + 1 < steps) {
         a.d = nx;
-        product<kUpdate>(a, cb, s);
+        product<kUpdate>(a, cb, p.update.kind, s);
         std::swap(x, nx);
         continue;
       }
@@ -256,9 +294,9 @@ hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonTarg
         std::swap(a.l_mat, a.r_mat);
         std::swap(a.l_ld, a.r_ld);
         std::swap(a.m, a.n);
-        product<kOutTall>(a, cb, s);
+        product<kOutTall>(a, cb, p.last.kind, s);
       } else {
-        product<kOut>(a, cb, s);
+        product<kOut>(a, cb, p.last.kind, s);
       }
     }
   }

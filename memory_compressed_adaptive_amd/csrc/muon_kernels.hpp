@@ -165,6 +165,16 @@ __device__ __forceinline__ double lanes_max(double v, int lanes) {
   return v;
 }
 
+// The sum of a wave's values, in the same order every time.
+__device__ __forceinline__ double wave_sum(double v) {
+  v += dpp_f64<0xb1>(v);
+  v += dpp_f64<0x4e>(v);
+  v += dpp_f64<0x141>(v);
+  v += dpp_f64<0x140>(v);
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
+}
+
 // Writes their new momentum.  kMom8: `lanes` consecutive lanes hold a block of
 // 256 (or the row's short last one, or the whole of a shorter row), and `first`
 // is true in the one that holds its first element.  All lanes of a wave call it.
@@ -219,47 +229,52 @@ __device__ __forceinline__ void muon_store_momentum(const MuonInput &I, const Mu
   if (first && at.n > 0) I.scales[at.scale] = step;
 }
 
-// How waves go over a stored matrix: `lanes` lanes to a row (4 columns each; 64,
-// or fewer for narrow matrices) and so 64 / lanes rows at once.
+// How waves go over a stored matrix: 2^log_lanes lanes to a row (4 columns each;
+// 64, or fewer for narrow matrices) and so 64 >> log_lanes rows at once.
 struct MuonRun {
-  uint32_t segs;   // runs along a row: ceil(c / (4 lanes))
-  int lanes;
+  int log_lanes;
+  int segs;        // runs along a row: ceil(c / (4 lanes))
+  int groups;      // of rows
+  int blocks;      // scales in a row
 };
 
 // Run `first`, then every `stride`-th.  What depends on the lane is set up once;
 // a step is a few scalar instructions.
 struct MuonWalk {
   int group, seg;              // uniform: which rows, which part of them
-  int groups, segs, rows, wide, step_group, step_seg;
+  int groups, segs, log_rows, log_wide, step_group, step_seg;
   int di, dj, r, c, blocks;
   int64_t x0, mat0, scale0, x_row;
 
   __device__ __forceinline__ MuonWalk(const MuonInput &I, const MuonRun &run, int64_t b, int lane, uint32_t first,
                                       uint32_t stride) {
-    segs = (int)run.segs;
-    rows = 64 / run.lanes;
-    wide = 4 * run.lanes;
-    di = lane / run.lanes;
-    dj = 4 * (lane & (run.lanes - 1));
+    segs = run.segs;
+    log_rows = 6 - run.log_lanes;
+    log_wide = 2 + run.log_lanes;
+    di = lane >> run.log_lanes;
+    dj = 4 * (lane & ((1 << run.log_lanes) - 1));
     r = (int)I.r;
     c = (int)I.c;
-    groups = (r + rows - 1) / rows;
-    blocks = (c + kMomentumBlock - 1) / kMomentumBlock;
-    group = (int)(first / run.segs);
-    seg = (int)(first - (uint32_t)group * run.segs);
-    step_group = (int)(stride / run.segs);
-    step_seg = (int)(stride - (uint32_t)step_group * run.segs);
+    groups = run.groups;
+    blocks = run.blocks;
+    group = (int)first, seg = 0;
+    step_group = (int)stride, step_seg = 0;
+    if (segs > 1) {
+      group = (int)(first / (uint32_t)segs);
+      seg = (int)(first - (uint32_t)group * segs);
+      step_group = (int)(stride / (uint32_t)segs);
+      step_seg = (int)(stride - (uint32_t)step_group * segs);
+    }
     x_row = I.x_row;
     x0 = b * I.x_batch + di * I.x_row + dj;
     mat0 = (b * I.r + di) * I.c + dj;
     scale0 = (b * I.r + di) * blocks;
   }
   __device__ __forceinline__ bool more() const { return group < groups; }
-  __device__ __forceinline__ int row() const { return group * rows; }   // of lane 0
-  __device__ __forceinline__ int col() const { return seg * wide; }
+  __device__ __forceinline__ int row() const { return group << log_rows; }   // of lane 0
+  __device__ __forceinline__ int col() const { return seg << log_wide; }
   __device__ __forceinline__ MuonSpot spot() const {
-    const int i = group * rows, j = seg * wide;
-    const int left = c - dj - j;
+    const int i = row(), j = col(), left = c - dj - j;
     return {x0 + ((int64_t)i * x_row + j), mat0 + ((int64_t)i * c + j), scale0 + ((int64_t)i * blocks + seg), i + di < r ? left : 0};
   }
   __device__ __forceinline__ void next() {
@@ -298,24 +313,29 @@ __global__ __launch_bounds__(256) void muon_norm_kernel(MuonInput I, MuonRun run
       for (int f = 0; f < 4; ++f) sum += (double)u[f] * (double)u[f];
     }
   }
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
+  sum = wave_sum(sum);
   __shared__ double s[4];
   if (lane == 0) s[wave] = sum;
   __syncthreads();
   if (threadIdx.x == 0) part[lb * nparts + blockIdx.x] = (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// 2^14 / max(|U|_F, eps) from the sum of squares
-__device__ __forceinline__ double muon_scale(double squares, float eps) {
-  const double norm = sqrt(squares);
-  return (double)kScaleX / (norm >= (double)eps || norm != norm ? norm : (double)eps);
+// 1 / max(|U|_F, eps) from the sum of squares; NaN if that is NaN, 0 if it is
+// infinite.  The hardware's reciprocal root has at least 14 bits; each
+// correction doubles them.
+__device__ __forceinline__ double muon_factor(double squares, float eps) {
+  const double least = (double)eps * (double)eps;
+  const double s = squares > least ? squares : least;   // (a NaN is put back below)
+  double y = __builtin_amdgcn_rsq(s);
+#pragma unroll
+  for (int e = 0; e < 3; ++e) y = fma(y * 0.5, fma(-s * y, y, 1.0), y);
+  return squares < __builtin_inf() ? y : squares == squares ? 0.0 : squares;
 }
 
 // ------------------------------------------------------------------ momentum, X0
 // Writes the new momentum, and X0 in its wide orientation with zeros in the
 // padding: as the matrix is stored, or transposed if that is tall.  A block of
-// 256 threads takes kLoadRows rows x 4 * run.lanes columns of the stored
+// 256 threads takes kLoadRows rows x 4 * lanes columns of the stored
 // matrix: 64, or 16 where that gives few blocks (768 x 768: 36 blocks take 11
 // us, 144 take 5).  sp, tp: the stored orientation's padded columns and rows.
 template <int MOM, bool TALL, int kLoadRows>
@@ -323,42 +343,41 @@ __global__ __launch_bounds__(256) void muon_load_kernel(MuonInput I, MuonRun run
                                                         float eps, _Float16 *X, int64_t sp, int64_t tp) {
   __shared__ double s4[4];
   __shared__ _Float16 tile[TALL ? kLoadRows : 1][256 + 4];
+  const int lanes = 1 << run.log_lanes;
   const int lane = (int)(threadIdx.x & 63u), wave = (int)(threadIdx.x >> 6);
   const int64_t lb = blockIdx.z, b = b0 + lb;
-  const int64_t i0 = (int64_t)blockIdx.y * kLoadRows, j0 = (int64_t)blockIdx.x * (4 * run.lanes);
-  const int col = 4 * (lane & (run.lanes - 1)), rows = 64 / run.lanes;
+  const int64_t i0 = (int64_t)blockIdx.y * kLoadRows, j0 = (int64_t)blockIdx.x * (4 * lanes);
+  const int col = 4 * (lane & (lanes - 1)), rows = 64 >> run.log_lanes;
   const int64_t j = j0 + col;
   double sum = 0.0;
   for (int p = (int)threadIdx.x; p < nparts; p += 256) sum += part[lb * nparts + p];
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
+  sum = wave_sum(sum);
   if (lane == 0) s4[wave] = sum;
   __syncthreads();
-  const double scale = muon_scale((s4[0] + s4[1]) + (s4[2] + s4[3]), eps);
+  const double scale = (double)kScaleX * muon_factor((s4[0] + s4[1]) + (s4[2] + s4[3]), eps);
   X += lb * sp * tp;
-  const int blocks = (int)((I.c + kMomentumBlock - 1) / kMomentumBlock);
   for (int q0 = wave * rows; q0 < kLoadRows; q0 += 16 * rows) {
     MuonRaw R[4];
     MuonSpot at[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int q = q0 + e * 4 * rows + lane / run.lanes;
+      const int q = q0 + e * 4 * rows + (lane >> run.log_lanes);
       const int64_t i = i0 + q;
-      at[e] = {b * I.x_batch + i * I.x_row + j, (b * I.r + i) * I.c + j, (b * I.r + i) * blocks + j / kMomentumBlock,
+      at[e] = {b * I.x_batch + i * I.x_row + j, (b * I.r + i) * I.c + j, (b * I.r + i) * run.blocks + j / kMomentumBlock,
                q < kLoadRows && i < I.r ? (int)(I.c - j) : 0};
       R[e] = muon_raw<MOM>(I, at[e]);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (q0 + e * 4 * rows >= kLoadRows) break;
-      const int q = q0 + e * 4 * rows + lane / run.lanes;
+      const int q = q0 + e * 4 * rows + (lane >> run.log_lanes);
       float u[4], m32[4];
       double m64[4] = {0, 0, 0, 0};
       muon_elems<MOM>(I, R[e], at[e].n, u, m32, m64);
       half4 h;
 #pragma unroll
       for (int f = 0; f < 4; ++f) h[f] = f < at[e].n ? (_Float16)(float)((double)u[f] * scale) : (_Float16)0.f;
-      muon_store_momentum<MOM>(I, at[e], run.lanes, j % kMomentumBlock == 0, m32, m64);
+      muon_store_momentum<MOM>(I, at[e], lanes, j % kMomentumBlock == 0, m32, m64);
       if (TALL) *(half4 *)&tile[q][col] = h;
       else if (j < sp && i0 + q < tp) *(half4 *)(X + (i0 + q) * sp + j) = h;
     }
@@ -368,7 +387,7 @@ __global__ __launch_bounds__(256) void muon_load_kernel(MuonInput I, MuonRun run
   // transposed: 8 consecutive rows of a column to a lane
   constexpr int kOcts = kLoadRows / 8;
   const int rg = (int)threadIdx.x % kOcts;
-  for (int cc = (int)threadIdx.x / kOcts; cc < 4 * run.lanes; cc += 256 / kOcts) {
+  for (int cc = (int)threadIdx.x / kOcts; cc < 4 * lanes; cc += 256 / kOcts) {
     half8 h;
 #pragma unroll
     for (int e = 0; e < 8; ++e) h[e] = tile[8 * rg + e][cc];
@@ -395,9 +414,11 @@ struct MuonOld {
   uint32_t w[4];
 };
 
+// kPlain: it is known that nothing is updated (and the result is bf16).
+template <bool kPlain>
 __device__ __forceinline__ MuonOld read_out(const MuonTarget &T, int64_t at, int n) {
   MuonOld o = {at, n, {0u, 0u, 0u, 0u}};
-  if (!T.update) return o;
+  if (kPlain || !T.update) return o;
   if (T.bf16) {
     const uint16_t *p = (const uint16_t *)T.out + at;
     if (T.vec && n >= 4) {
@@ -423,15 +444,16 @@ __device__ __forceinline__ MuonOld read_out(const MuonTarget &T, int64_t at, int
 }
 
 // Four consecutive sums of the last product go there.
+template <bool kPlain>
 __device__ __forceinline__ void write_out(const MuonTarget &T, const MuonOld &o, float4 sums) {
   constexpr float kUnit = 1.f / (kScaleX * kScaleP);
   const float v[4] = {sums.x * kUnit, sums.y * kUnit, sums.z * kUnit, sums.w * kUnit};
   float x[4];
-  if (T.bf16) {
+  if (kPlain || T.bf16) {
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
       const float old = __uint_as_float(f & 1 ? o.w[f >> 1] & 0xffff0000u : o.w[f >> 1] << 16);
-      x[f] = T.update ? old * T.decay - T.rate * v[f] : v[f];
+      x[f] = !kPlain && T.update ? old * T.decay - T.rate * v[f] : v[f];
     }
     uint16_t *p = (uint16_t *)T.out + o.at;
     const uint32_t lo = f32x2_bf16(x[0], x[1]), hi = f32x2_bf16(x[2], x[3]);
@@ -464,6 +486,10 @@ enum {
   kUpdate = 2,   // X' = P X:                L = X^T, R = P
   kOut = 3,      // the last X', with L and R as in kUpdate, written where the caller wants it
   kOutTall = 4,  // the same for a tall matrix, whose rows are the columns of X': L = P, R = X^T
+  // A where X is so wide that its few tiles would leave most CUs idle: the
+  // summed index is cut into parts, whose sums are added in their order
+  kGramPart = 5,
+  kGramSum = 6,
 };
 
 struct MuonProduct {
@@ -474,6 +500,8 @@ struct MuonProduct {
   _Float16 *d;              // [N][M]
   int64_t m, n;
   int tiles_m, tiles_n, tiles;   // of one matrix
+  int parts;                // kGramPart, kGramSum
+  float *sums;              // their fp32 sums: [matrix][tile][part][a tile's elements as its waves hold them]
   float a, b, c;
   MuonTarget out;           // kOut: element (n, m) of matrix b0 + i goes to its row n, column m
   int64_t b0;
@@ -556,13 +584,36 @@ __device__ __forceinline__ void wave_lds_fence() {
 // Workgroups go to the eight XCDs in turn; each XCD gets one run of tiles,
 // taken in blocks of 4 x 4, so that the panels its 32 CUs read at a time fit
 // its L2.  SYM: only tiles with ti <= tj, the others are their mirror images.
-template <bool SYM>
-__device__ __forceinline__ void tile_of(const MuonProduct &A, int &lb, int &ti, int &tj) {
-  const uint32_t total = gridDim.x, id = blockIdx.x, xcd = id & 7, per = total >> 3, rem = total & 7;
-  const uint32_t at = xcd * per + (xcd < rem ? xcd : rem) + (id >> 3);
-  lb = (int)(at / (uint32_t)A.tiles);
-  int r = (int)(at - (uint32_t)lb * A.tiles);
-  if (SYM) {
+// Small tiles are taken as they come: their products are short, and L2 holds
+// what they read.
+template <bool SYM, bool PLAIN, bool PARTS>
+__device__ __forceinline__ void tile_of(const MuonProduct &A, int &lb, int &ti, int &tj, int &part) {
+  uint32_t at = blockIdx.x;
+  if (!PLAIN) {
+    const uint32_t total = gridDim.x, xcd = at & 7, per = total >> 3, rem = total & 7;
+    at = xcd * per + (xcd < rem ? xcd : rem) + (at >> 3);
+  }
+  part = 0;
+  if (PARTS) {
+    part = (int)(at % (uint32_t)A.parts);
+    at /= (uint32_t)A.parts;
+  }
+  lb = (int)blockIdx.y;
+  int r = (int)at;
+  if (!PLAIN) {
+    lb = (int)(at / (uint32_t)A.tiles);
+    r = (int)(at - (uint32_t)lb * A.tiles);
+  }
+  if (SYM && PLAIN) {
+    int y = (int)((sqrtf(8.f * (float)r + 1.f) - 1.f) * 0.5f);
+    while (y * (y + 1) / 2 > r) --y;
+    while ((y + 1) * (y + 2) / 2 <= r) ++y;
+    ti = r - y * (y + 1) / 2;
+    tj = y;
+  } else if (PLAIN) {
+    tj = r / A.tiles_m;
+    ti = r - tj * A.tiles_m;
+  } else if (SYM) {
     // before row block J lie 4J (4J + 1) / 2 tiles
     int J = (int)((sqrtf(4.f + 32.f * (float)r) - 2.f) * 0.0625f);
     while (8 * J * J + 2 * J > r) --J;
@@ -589,6 +640,7 @@ __device__ __forceinline__ void tile_of(const MuonProduct &A, int &lb, int &ti, 
   lb = __builtin_amdgcn_readfirstlane(lb);
   ti = __builtin_amdgcn_readfirstlane(ti);
   tj = __builtin_amdgcn_readfirstlane(tj);
+  part = __builtin_amdgcn_readfirstlane(part);
 }
 
 // Where 16-byte chunk g of a B-wide panel in LDS comes from: bytes from the
@@ -634,20 +686,26 @@ __device__ __forceinline__ half8 panel_read(const char *panel, int at, int ks, i
 
 template <class T, int ROLE>
 __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A) {
-  constexpr bool LC = ROLE == kUpdate || ROLE == kOut, RC = ROLE == kOutTall, OUT = ROLE >= kOut;
+  constexpr bool LC = ROLE == kUpdate || ROLE == kOut, RC = ROLE == kOutTall, OUT = ROLE == kOut || ROLE == kOutTall;
+  constexpr bool SYM = ROLE == kGram || ROLE == kPoly || ROLE == kGramPart || ROLE == kGramSum;
   __shared__ __attribute__((aligned(1024))) char smem[T::kLds];
   const int lane = (int)(threadIdx.x & 63u), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int wm = wave % T::WM * T::TM, wn = wave / T::WM * T::TN;
-  int lb, ti, tj;
-  tile_of<ROLE <= kPoly>(A, lb, ti, tj);
+  int lb, ti, tj, part;
+  tile_of<SYM, T::BM == 64, ROLE == kGramPart>(A, lb, ti, tj, part);
   const int64_t m0 = (int64_t)ti * T::BM, n0 = (int64_t)tj * T::BN;
+
+  constexpr int kSums = T::kWaves * T::FM * T::FN * 1024;   // of a tile
+  float *sums = A.sums + ((int64_t)lb * A.tiles + (ti + (int64_t)tj * (tj + 1) / 2)) * A.parts * kSums + wave * (T::FM * T::FN * 1024) + lane * 4;
+  const int steps = (int)(A.k / T::BK), first = ROLE == kGramPart ? (int)((int64_t)steps * part / A.parts) : 0;
+  const int nk = ROLE == kGramPart ? (int)((int64_t)steps * (part + 1) / A.parts) - first : steps;
 
   // Panels that pass the matrix: rows past its last read as zeros (the buffer
   // ends there); columns past a row's last read the next row, and only reach
   // elements of D past its sides, which are not stored.
   const int64_t l_ld = 2 * A.l_ld, r_ld = 2 * A.r_ld;   // bytes of a row; 256 rows stay under 2^31
-  const char *pl = (const char *)(A.l + lb * A.l_mat) + (LC ? 2 * m0 : m0 * l_ld);
-  const char *pr = (const char *)(A.r + lb * A.r_mat) + (RC ? 2 * n0 : n0 * r_ld);
+  const char *pl = (const char *)(A.l + lb * A.l_mat) + (LC ? 2 * m0 : m0 * l_ld) + first * (T::BK * 2);
+  const char *pr = (const char *)(A.r + lb * A.r_mat) + (RC ? 2 * n0 : n0 * r_ld) + first * (T::BK * 2);
   const int64_t nl = (const char *)(A.l + (lb + 1) * A.l_mat) - pl, nr = (const char *)(A.r + (lb + 1) * A.r_mat) - pr;
   const int64_t sl = LC ? T::BK * l_ld : T::BK * 2, sr = RC ? T::BK * r_ld : T::BK * 2;   // to the next step
   uint32_t vl[T::LI], vr[T::RI];
@@ -694,7 +752,6 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
 
   // Copies past the last step go to an empty buffer, so that the loop has one
   // shape and a wait counts the same copies at every step.
-  const int nk = (int)(A.k / T::BK);
   uint64_t al = (uint64_t)pl, ar = (uint64_t)pr, el = (uint64_t)nl, er = (uint64_t)nr;   // of the next step to copy
   int to_copy = nk;
   int4v bl, br;
@@ -705,51 +762,77 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
     al += (uint64_t)sl, el -= (uint64_t)sl;
     ar += (uint64_t)sr, er -= (uint64_t)sr;
   };
+  if (ROLE != kGramSum) {
 #pragma unroll
-  for (int t = 0; t < T::S; ++t) {
-    next_copy();
-#pragma unroll
-    for (int i = 0; i < kCopies; ++i) copy(i, bl, br, t);
-  }
-  stage_wait<(T::S - 1) * kCopies>();
-  fragments(0, 0, x[0], y[0]);
-  int stage = 0;
-  for (int t = 0; t < nk; ++t) {
-    const int next = stage + 1 == T::S ? 0 : stage + 1;
-#pragma unroll
-    for (int g = 0; g < T::kGroups; ++g) {
-      __builtin_amdgcn_sched_barrier(0);
-      if (g + 1 < T::kGroups) {
-        fragments(stage, g + 1, x[(g + 1) & 1], y[(g + 1) & 1]);
-#pragma unroll
-        for (int q = 0; q < kProducts; ++q) product(q, x[g & 1], y[g & 1]);
-        // products and reads in turn; left alone, the compiler moves the reads
-        // behind the products
-        constexpr int kEach = (kReads + kProducts - 1) / kProducts;
-#pragma unroll
-        for (int q = 0; q < kReads; q += kEach) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);
-        }
-        continue;
-      }
-      // the next stage is whole, and nobody reads this one any more
-      stage_wait<(T::S - 2) * kCopies>();
-      fragments(next, 0, x[0], y[0]);
+    for (int t = 0; t < T::S; ++t) {
       next_copy();
-      __builtin_amdgcn_sched_barrier(0);
-      constexpr int kEach = (kCopies + kProducts - 1) / kProducts;
 #pragma unroll
-      for (int q = 0; q < kProducts; ++q) {
-        product(q, x[1], y[1]);
-        // the copies that refill this stage are spread over the products
-#pragma unroll
-        for (int c = q * kEach; c < (q + 1) * kEach && c < kCopies; ++c) copy(c, bl, br, stage);
-      }
+      for (int i = 0; i < kCopies; ++i) copy(i, bl, br, t);
     }
-    stage = next;
+    stage_wait<(T::S - 1) * kCopies>();
+    fragments(0, 0, x[0], y[0]);
+    int stage = 0;
+    for (int t = 0; t < nk; ++t) {
+      const int next = stage + 1 == T::S ? 0 : stage + 1;
+#pragma unroll
+      for (int g = 0; g < T::kGroups; ++g) {
+        __builtin_amdgcn_sched_barrier(0);
+        if (g + 1 < T::kGroups) {
+          fragments(stage, g + 1, x[(g + 1) & 1], y[(g + 1) & 1]);
+#pragma unroll
+          for (int q = 0; q < kProducts; ++q) product(q, x[g & 1], y[g & 1]);
+          // products and reads in turn; left alone, the compiler moves the reads
+          // behind the products
+          constexpr int kEach = (kReads + kProducts - 1) / kProducts;
+#pragma unroll
+          for (int q = 0; q < kReads; q += kEach) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);
+          }
+          continue;
+        }
+        // the next stage is whole, and nobody reads this one any more
+        stage_wait<(T::S - 2) * kCopies>();
+        fragments(next, 0, x[0], y[0]);
+        next_copy();
+        __builtin_amdgcn_sched_barrier(0);
+        constexpr int kEach = (kCopies + kProducts - 1) / kProducts;
+#pragma unroll
+        for (int q = 0; q < kProducts; ++q) {
+          product(q, x[1], y[1]);
+          // the copies that refill this stage are spread over the products
+#pragma unroll
+          for (int c = q * kEach; c < (q + 1) * kEach && c < kCopies; ++c) copy(c, bl, br, stage);
+        }
+      }
+      stage = next;
+    }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  if (ROLE == kGramPart) {
+#pragma unroll
+    for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          *(float4 *)(sums + (int64_t)part * kSums + (i * T::FN + j) * 1024 + q * 256) =
+              make_float4(acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]);
+    return;
+  }
+  if (ROLE == kGramSum) {
+#pragma unroll 2
+    for (int p = 0; p < A.parts; ++p)
+#pragma unroll
+      for (int i = 0; i < T::FM; ++i)
+#pragma unroll
+        for (int j = 0; j < T::FN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 v = *(const float4 *)(sums + (int64_t)p * kSums + (i * T::FN + j) * 1024 + q * 256);
+            acc[i][j][4 * q] += v.x, acc[i][j][4 * q + 1] += v.y, acc[i][j][4 * q + 2] += v.z, acc[i][j][4 * q + 3] += v.w;
+          }
+  }
   __syncthreads();   // the stages' LDS is the epilogue's now
 
   // Each wave brings 32 rows (n) x TM of its part through LDS at a time, so
@@ -775,7 +858,7 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
   auto out_spot = [&](int j, int g) {
     const int row = (g * 64 + lane) / kOutChunks, c = (g * 64 + lane) % kOutChunks;
     const int64_t nn = n0 + wn + 32 * j + row, mm = m0 + wm + 4 * c;
-    return read_out(A.out, (A.b0 + lb) * A.out.batch + nn * A.out.row + mm, nn < A.out.rows ? (int)(A.out.cols - mm) : 0);
+    return read_out<false>(A.out, (A.b0 + lb) * A.out.batch + nn * A.out.row + mm, nn < A.out.rows ? (int)(A.out.cols - mm) : 0);
   };
   MuonOld old[OUT ? kOutTrips : 1];
   if (OUT) {
@@ -805,7 +888,7 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
       for (int g = 0; g < kOutTrips; ++g) {
         const MuonOld o = old[g];
         if (j + 1 < T::FN) old[g] = out_spot(j + 1, g);
-        write_out(A.out, o, v[g]);
+        write_out<false>(A.out, o, v[g]);
       }
       wave_lds_fence();
       continue;
@@ -833,7 +916,7 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
         for (int e = 0; e < 4; ++e) {
           const float v = acc[i][j][4 * q + e];
           float o = 0.f;
-          if (ROLE == kGram) o = v * (1.f / kScaleX);
+          if (ROLE == kGram || ROLE == kGramSum) o = v * (1.f / kScaleX);
           if (ROLE == kUpdate) o = v * (1.f / kScaleP);
           if (ROLE == kPoly) {
             o = (A.b * (kScaleP / kScaleX)) * (float)s[e] + (A.c * (kScaleP / (kScaleX * kScaleX))) * v;
@@ -850,7 +933,7 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
       const half8 h = *(const half8 *)(mine + row * kStride + c * 16);
       if (nb + row < A.n && mb + 8 * c < A.m) *(half8 *)(d + (nb + row) * dn + mb + 8 * c) = h;
     }
-    if (ROLE <= kPoly && ti < tj) {
+    if (SYM && ti < tj) {
       // the mirror image: lane s of 16 gets column s of 4 rows at a time
       const int s = lane & 15, oct = lane >> 4;
 #pragma unroll
@@ -920,8 +1003,10 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonInput 
   double *const red = (double *)((char *)scratch + L::kScratch);
 
   // U and its norm, the new momentum, zeros for X's padding
-  for (int at = (int)threadIdx.x * 16; at < 32 * NB * xrow; at += 1024 * kSmallWaves)
-    *(float4 *)(X + at) = make_float4(0.f, 0.f, 0.f, 0.f);
+  if ((S.tall ? I.c : I.r) != 32 * NB || (S.tall ? I.r : I.c) != S.mp) {
+    for (int at = (int)threadIdx.x * 16; at < 32 * NB * xrow; at += 1024 * kSmallWaves)
+      *(float4 *)(X + at) = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   constexpr int kGroup = MOM == kMomNone ? 4 : 2;   // reads under way in a lane (registers bound it)
   float u[L::kRuns][4];
   double sum = 0.0;
@@ -943,27 +1028,28 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonInput 
         float m32[4];
         double m64[4] = {0, 0, 0, 0};
         muon_elems<MOM>(I, R[e], at[e].n, u[g + e], m32, m64);
-        muon_store_momentum<MOM>(I, at[e], run.lanes, (lane & (run.lanes - 1)) == 0, m32, m64);
+        muon_store_momentum<MOM>(I, at[e], 1 << run.log_lanes, walk.dj == 0, m32, m64);
 #pragma unroll
         for (int f = 0; f < 4; ++f) sum += (double)u[g + e][f] * (double)u[g + e][f];
       }
     }
   }
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o, 64);
+  sum = wave_sum(sum);
   if (lane == 0) red[wave] = sum;
   __syncthreads();
   double total = red[0];
 #pragma unroll
   for (int w = 1; w < kSmallWaves; ++w) total += red[w];
   // 1 / max(|U|, eps) = rest * 2^pow, rest in [1, 2); all NaN if the norm is not finite
-  const double factor = muon_scale(total, S.eps) * (1.0 / (double)kScaleX);
+  const double factor = muon_factor(total, S.eps);
   int pow = 0;
   const double frac = frexp(factor, &pow);   // in [1/2, 1)
   const bool fine = factor > 0.0 && factor < (double)__builtin_inff();
   const float rest = fine ? (float)(2.0 * frac) : __builtin_nanf("");
   const int shift = fine ? pow - 1 + 14 : 0;
   {
+    // two factors: one could leave fp32's range
+    const float up = ldexpf(1.f, shift / 2), up2 = ldexpf(1.f, shift - shift / 2);
     MuonWalk walk(I, run, b, lane, wave, kSmallWaves);
     const int to = S.tall ? walk.dj * xrow + 2 * walk.di : walk.di * xrow + 2 * walk.dj;
 #pragma unroll
@@ -972,7 +1058,7 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonInput 
       const int i = walk.row(), j = walk.col(), n = i + walk.di < walk.r ? walk.c - walk.dj - j : 0;
       _Float16 h[4];
 #pragma unroll
-      for (int f = 0; f < 4; ++f) h[f] = (_Float16)ldexpf(u[g][f], shift);
+      for (int f = 0; f < 4; ++f) h[f] = (_Float16)(u[g][f] * up * up2);
       if (!S.tall) {
         // past the last column u is 0, and so is the padding
         if (n > 0) *(half4 *)(X + to + i * xrow + 2 * j) = half4{h[0], h[1], h[2], h[3]};
@@ -1134,57 +1220,91 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonInput 
 
   // the last P X goes to memory
   const float left = S.steps == 1 ? rest : 1.f;
-  for (int jp = wave; jp < S.mp / 32; jp += kSmallWaves) {
+  constexpr float kUnit = 1.f / (kScaleX * kScaleP);
+  const int r = lane >> 3, c = lane & 7;   // of a 32 x 32 block a lane writes rows r, r + 8, .., columns 4c..
+  auto spots = [&](int jp, int ib, MuonOld *old) {
+    const int i = S.tall ? 32 * jp + row : 32 * ib + r, j = S.tall ? 32 * ib + 4 * half : 32 * jp + 4 * c;
+    const int64_t at = b * out.batch + i * out.row + j, step = S.tall ? 8 : 8 * out.row;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      if (MOM != kMomNone && S.tall && 32 * ib + 8 * q >= (int)out.cols) continue;   // uniform: all of it is padding
+      const int n = S.tall ? (i < (int)out.rows ? (int)out.cols - j - 8 * q : 0) : i + 8 * q < (int)out.rows ? (int)out.cols - j : 0;
+      old[q] = read_out<MOM == kMomNone>(out, at + q * step, n);
+    }
+  };
+  // a panel's results; where a panel is one block, the old values of this
+  // wave's next panel are read first
+  constexpr bool kAhead = MOM != kMomNone && NB == 1;
+  auto emit = [&](int jp, MuonOld *old, MuonOld *next) {
     half8 x[2 * NB];
+    if (kAhead && jp + kSmallWaves < S.mp / 32) spots(jp + kSmallWaves, 0, next);
     panel(jp, x);
     for (int ib = 0; ib < NB; ++ib) {
       float16v acc;
       zero(acc);
       const char *pp = P + (32 * ib + row) * L::kRow + 16 * half;
+      if (MOM != kMomNone && !kAhead) spots(jp, ib, old);
       if (S.tall) {
         // rows of the result are columns of X: a lane has four consecutive elements of one
-        MuonOld old[4];
-        const int i = 32 * jp + row, j = 32 * ib + 4 * half;
-        const int n = i < (int)out.rows ? (int)out.cols - j : 0;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) old[q] = read_out(out, b * out.batch + i * out.row + j + 8 * q, n - 8 * q);
 #pragma unroll
         for (int k = 0; k < 2 * NB; ++k)
           acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8 *)(pp + 32 * k), x[k], acc, 0, 0, 0);
+        if (MOM == kMomNone) spots(jp, ib, old);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          write_out(out, old[q], make_float4(left * acc[4 * q], left * acc[4 * q + 1], left * acc[4 * q + 2], left * acc[4 * q + 3]));
-        continue;
-      }
-      // of the 32 rows of this block a lane writes r, r + 8, .., columns 4c..
-      const int r = lane >> 3, c = lane & 7;
-      MuonOld old[4];
+        for (int q = 0; q < 4; ++q) {
+          if (32 * ib + 8 * q >= (int)out.cols) continue;
+          write_out<MOM == kMomNone>(out, old[q], make_float4(left * acc[4 * q], left * acc[4 * q + 1], left * acc[4 * q + 2], left * acc[4 * q + 3]));
+        }
+      } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = 32 * ib + r + 8 * e, j = 32 * jp + 4 * c;
-        old[e] = read_out(out, b * out.batch + i * out.row + j, i < (int)out.rows ? (int)out.cols - j : 0);
-      }
-#pragma unroll
-      for (int k = 0; k < 2 * NB; ++k)
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[k], *(const half8 *)(pp + 32 * k), acc, 0, 0, 0);
-      // the panel's place in LDS (32 NB rows of 64 bytes) takes 16 rows of 32
-      // fp32 results at a time: row r of them in its rows 2r and 2r + 1, so
-      // that memory is written in whole rows of the panel
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        if (row >> 4 == p) {
+        for (int k = 0; k < 2 * NB; ++k)
+          acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[k], *(const half8 *)(pp + 32 * k), acc, 0, 0, 0);
+        // A block goes through the panel's place in LDS (32 NB rows of 64
+        // bytes), so that memory is written in whole rows of it.
+        if (MOM == kMomNone && out.vec && (out.row & 7) == 0 && (out.batch & 7) == 0 && ((uintptr_t)out.out & 15) == 0 &&
+            32 * jp + 32 <= (int)out.cols && 32 * ib + 32 <= (int)out.rows) {
+          // bf16 results, a whole block of them: 16 bytes a lane
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            *(float4 *)(X + (2 * (row & 15) + (q >> 1)) * xrow + 64 * jp + ((q & 1) * 8 + 4 * half) * 4) =
-                make_float4(left * acc[4 * q], left * acc[4 * q + 1], left * acc[4 * q + 2], left * acc[4 * q + 3]);
-        }
-        wave_lds_fence();
+            *(uint2 *)(X + row * xrow + 64 * jp + 16 * q + 8 * half) =
+                make_uint2(f32x2_bf16(left * acc[4 * q] * kUnit, left * acc[4 * q + 1] * kUnit),
+                           f32x2_bf16(left * acc[4 * q + 2] * kUnit, left * acc[4 * q + 3] * kUnit));
+          wave_lds_fence();
+          uint16_t *to = (uint16_t *)out.out + (b * out.batch + (32 * ib + (lane >> 2)) * out.row + 32 * jp + 8 * (lane & 3));
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-          write_out(out, old[2 * p + e], *(const float4 *)(X + (2 * (r + 8 * e) + (c >> 2)) * xrow + 64 * jp + (c & 3) * 16));
-        wave_lds_fence();
+          for (int e = 0; e < 2; ++e)
+            *(uint4 *)(to + 16 * e * out.row) = *(const uint4 *)(X + ((lane >> 2) + 16 * e) * xrow + 64 * jp + 16 * (lane & 3));
+          wave_lds_fence();
+        } else {
+          // 16 rows of 32 fp32 results at a time: row i of them lies in rows 2i and 2i + 1
+          if (MOM == kMomNone) spots(jp, ib, old);
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            if (row >> 4 == p) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                *(float4 *)(X + (2 * (row & 15) + (q >> 1)) * xrow + 64 * jp + ((q & 1) * 8 + 4 * half) * 4) =
+                    make_float4(left * acc[4 * q], left * acc[4 * q + 1], left * acc[4 * q + 2], left * acc[4 * q + 3]);
+            }
+            wave_lds_fence();
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+              write_out<MOM == kMomNone>(out, old[2 * p + e], *(const float4 *)(X + (2 * (r + 8 * e) + (c >> 2)) * xrow + 64 * jp + (c & 3) * 16));
+            wave_lds_fence();
+          }
+        }
       }
     }
+  };
+  MuonOld one[4], two[4];
+  if (kAhead) {
+    if (wave < S.mp / 32) spots(wave, 0, one);
+    for (int jp = wave; jp < S.mp / 32; jp += 2 * kSmallWaves) {
+      emit(jp, one, two);
+      if (jp + kSmallWaves < S.mp / 32) emit(jp + kSmallWaves, two, one);
+    }
+  } else {
+    for (int jp = wave; jp < S.mp / 32; jp += kSmallWaves) emit(jp, one, two);
   }
 }
 

@@ -38,7 +38,8 @@ def _check_orthogonal(what, got, u, **kw):
 
 
 SIZES = [(1, 1), (1, 7), (7, 1), (2, 300), (33, 65), (64, 64), (65, 64), (63, 129), (130, 70), (100, 1000), (517, 260),
-         (256, 256), (300, 300), (128, 2048), (700, 390), (512, 512), (600, 770), (1024, 1024), (1030, 1290), (1300, 1025)]
+         (256, 256), (300, 300), (128, 2048), (700, 390), (512, 512), (600, 770), (1024, 1024), (1030, 1290), (1300, 1025),
+         (40, 9000), (130, 5000), (9001, 150), (600, 8200)]
 
 
 @pytest.mark.parametrize("steps", [1, 2, 5])
