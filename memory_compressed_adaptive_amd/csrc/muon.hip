@@ -55,6 +55,7 @@ struct Choice {
   int kind;
   int parts;
   size_t bytes;   // the parts' sums
+  double time;    // expected, in microseconds
 };
 
 // The tile with the shortest expected time.  Workgroups go over the 256 CUs in
@@ -74,7 +75,7 @@ Choice pick(int64_t m, int64_t n, int64_t k, int64_t chunk, bool symmetric, bool
       {128, 128, 2, 0.60, 1.02, 3.5, 6.0},
       {129, 128, 1, 0.45, 0.95, 3.5, 6.0},
       {64, 64, 2, 0.26, 0.40, 2.5, 3.5}};
-  Choice best = {0, 1, 0};
+  Choice best = {0, 1, 0, 0.0};
   double least = 0.0;
   for (const auto &t : kinds) {
     const int64_t tm = (m + t.side - 1) / t.side, tn = (n + t.side - 1) / t.side;
@@ -88,7 +89,7 @@ Choice pick(int64_t m, int64_t n, int64_t k, int64_t chunk, bool symmetric, bool
                     (rest == 0 ? 0.0 : its * (rest > 256 || whole > 0 ? t.full : t.alone) + ends);
       // their sums are written and read at 3 TB/s, by a tile's workgroup at 0.1
       if (parts > 1) time += 4.0 + (double)bytes / 3e6 + std::max((double)bytes / 3e6, (double)bytes / (double)tiles / 1e5);
-      if (!best.kind || time < least) best = {t.kind, parts, bytes}, least = time;
+      if (!best.kind || time < least) best = {t.kind, parts, bytes, time}, least = time;
     }
   }
   return best;
@@ -99,6 +100,7 @@ struct Plan {
   int64_t r, c, n, m;       // n <= m: the wide orientation's sides
   bool tall;
   bool small;               // a workgroup for each matrix, no workspace
+  bool pairs;               // two steps are taken together
   int64_t np, mp;           // padded
   int64_t chunk;            // matrices at a time
   MuonRun run;              // how waves go over the stored matrix
@@ -121,7 +123,7 @@ struct Plan {
     run.blocks = (int)((c + kMomentumBlock - 1) / kMomentumBlock);
     runs = (uint32_t)run.groups * (uint32_t)run.segs;
     nparts = (int)std::min<int64_t>(kNormParts, (runs + 15) / 16);   // four runs to a wave
-    const size_t one = 2 * 2 * (size_t)(np * mp) + 2 * 2 * (size_t)(np * np) + 8 * (size_t)nparts;
+    const size_t one = 2 * 2 * (size_t)(np * mp) + 3 * 2 * (size_t)(np * np) + 8 * (size_t)nparts;
     chunk = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(batch, 65535), (int64_t)(kWorkspaceAim / one)));
     x_bytes = (size_t)round_up(2 * chunk * np * mp, 256);
     a_bytes = (size_t)round_up(2 * chunk * np * np, 256);
@@ -131,8 +133,10 @@ struct Plan {
     poly = pick(np, np, np, chunk, true, false, false);
     update = pick(mp, np, np, chunk, false, false, false);
     last = pick(mp, np, np, chunk, false, true, false);
+    // three products of the short side take the place of two with the long one
+    pairs = 3 * m >= 4 * n && gram.time + update.time > 1.1 * 3.0 * poly.time;
     sum_bytes = (size_t)round_up((int64_t)gram.bytes, 256);
-    bytes = small ? 256 : 2 * x_bytes + 2 * a_bytes + part_bytes + sum_bytes;
+    bytes = small ? 256 : 2 * x_bytes + 3 * a_bytes + part_bytes + sum_bytes;
   }
 };
 
@@ -224,6 +228,10 @@ hipError_t run_small(const Plan &p, int64_t batch, const MuonInput &in, const Mu
   small.tall = p.tall;
   small.mp = (int)round_up(p.m, 32);
   small.eps = eps;
+  // Two steps together save X X^T and P X once, for three short products: a
+  // quarter of the time at 64 x 768, a loss below six times as wide as high.
+  small.pairs = p.n <= 64 && p.m >= 6 * round_up(p.n, 32);
+  small.single = steps & 1 ? (steps / 2 + 1) / 2 * 2 : -1;
   // parts of at least four products of 16
   small.parts = 1;
   while (2 * small.parts <= small_parts(p.n) && small.mp / 16 / (2 * small.parts) >= 4) small.parts *= 2;
@@ -241,9 +249,11 @@ hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonTarg
                float eps, void *workspace, hipStream_t s) {
   char *w = (char *)workspace;
   _Float16 *x0 = (_Float16 *)w, *x1 = (_Float16 *)(w + p.x_bytes);
-  _Float16 *ga = (_Float16 *)(w + 2 * p.x_bytes), *gp = (_Float16 *)(w + 2 * p.x_bytes + p.a_bytes);
-  double *part = (double *)(w + 2 * p.x_bytes + 2 * p.a_bytes);
-  float *sums = (float *)(w + 2 * p.x_bytes + 2 * p.a_bytes + p.part_bytes);
+  w += 2 * p.x_bytes;
+  _Float16 *ga = (_Float16 *)w, *gp = (_Float16 *)(w + p.a_bytes), *gt = (_Float16 *)(w + 2 * p.a_bytes);
+  w += 3 * p.a_bytes;
+  double *part = (double *)w;
+  float *sums = (float *)(w + p.part_bytes);
   const int64_t nm = p.np * p.mp, nn = p.np * p.np;
   for (int64_t b0 = 0; b0 < batch; b0 += p.chunk) {
     const int64_t cb = std::min(p.chunk, batch - b0);
@@ -258,14 +268,17 @@ hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonTarg
     const auto load = p.tall ? (few ? muon_load_kernel<MOM, true, 16> : muon_load_kernel<MOM, true, 64>)
                              : (few ? muon_load_kernel<MOM, false, 16> : muon_load_kernel<MOM, false, 64>);
     hipLaunchKernelGGL(load, lg, dim3(256), 0, s, in, p.run, b0, part, p.nparts, eps, x, sp, tp);
-    for (int t = 0; t < steps; ++t) {
+    // steps in pairs, a single one (of an odd number) in the middle
+    const int single = p.pairs ? (steps & 1 ? (steps / 2 + 1) / 2 * 2 : -1) : 0;
+    for (int t = 0; t < steps;) {
+      const bool two = p.pairs && t != single;
       MuonProduct a = {};
-      a.a = k.v[t][0], a.b = k.v[t][1], a.c = k.v[t][2];
       a.l = a.r = x;
       a.l_mat = a.r_mat = nm;
       a.l_ld = a.r_ld = a.k = p.mp;
       a.m = a.n = p.np;
       a.d = ga;
+      a.unit = 1.f / kScaleX;
       if (p.gram.parts > 1) {
         a.parts = p.gram.parts;
         a.sums = sums;
@@ -274,20 +287,41 @@ hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonTarg
       } else {
         product<kGram>(a, cb, p.gram.kind, s);
       }
-      a.l = a.r = ga;
+      // l r -> d, of symmetric matrices
+      const auto square = [&](const _Float16 *l, const _Float16 *r, _Float16 *d, float unit) {
+        a.l = l, a.r = r, a.d = d, a.unit = unit;
+        product<kGram>(a, cb, p.poly.kind, s);
+      };
+      const auto poly = [&](const _Float16 *of, _Float16 *d, int step) {
+        a.l = a.r = of, a.d = d;
+        a.a = k.v[step][0], a.b = k.v[step][1], a.c = k.v[step][2];
+        product<kPoly>(a, cb, p.poly.kind, s);
+      };
       a.l_mat = a.r_mat = nn;
       a.l_ld = a.r_ld = a.k = p.np;
-      a.d = gp;
-      product<kPoly>(a, cb, p.poly.kind, s);
+      poly(ga, gp, t);
+      const _Float16 *factor = gp;
+      float unit = 1.f / kScaleP;
+      if (two) {
+        square(gp, ga, gt, 1.f / kScaleX);                        // T = P A
+        square(gt, gp, ga, kScaleX / (kScaleP * kScaleP));        // the next A
+        poly(ga, gt, t + 1);
+        square(gt, gp, ga, kScaleQ / (kScaleP * kScaleP));        // P2 P1
+        factor = ga;
+        unit = 1.f / kScaleQ;
+      }
+      t += two ? 2 : 1;
       a.l = x, a.l_mat = nm, a.l_ld = a.m = p.mp;
-      a.r = gp;
-      if (t + 1 < steps) {
+      a.r = factor;
+      if (t < steps) {
         a.d = nx;
+        a.unit = unit;
         product<kUpdate>(a, cb, p.update.kind, s);
         std::swap(x, nx);
         continue;
       }
       a.out = o;
+      a.unit = unit / kScaleX;
       a.b0 = b0;
       if (p.tall) {   // the fastest index of `out` is P's
         std::swap(a.l, a.r);

@@ -9,6 +9,15 @@
 //   P = a I + b A + c A A   (n x n, symmetric)
 //   X <- P X
 //
+// Two steps can be taken together: A and every polynomial of it commute, so
+// that with P1 = p1(A) the next A is P1 A P1, and the second step's X is
+// (P2 P1) X: the products with the long side, X X^T and P X, are made once for
+// two steps, for three more products of the short side (T = P1 A, T P1 and
+// P2 P1), all symmetric.  No intermediate X is rounded then; the roundings of T
+// and P2 P1 take its place, and the error stays what it was (simulated: within
+// a fifth).  Three steps together would not: what rounding does to small
+// eigenvalues of A grows twelvefold with each.
+//
 // Number formats.  X, A and P are held in fp16, scaled by 2^14, 2^14 and 2^12,
 // and every product is summed in fp32.  All of them are bounded: the host
 // refuses coefficients for which a singular value could pass 1.95 or an
@@ -34,7 +43,8 @@ typedef _Float16 half4 __attribute__((ext_vector_type(4)));
 typedef float float16v __attribute__((ext_vector_type(16)));
 
 constexpr float kScaleX = 16384.f;   // of X and of A
-constexpr float kScaleP = 4096.f;
+constexpr float kScaleP = 4096.f;   // of P and of P A
+constexpr float kScaleQ = 256.f;    // of a product of two P
 constexpr int kMomentumBlock = 256;  // elements of a row that share a scale
 
 enum { kMomNone = 0, kMom32 = 1, kMom8 = 2 };
@@ -445,9 +455,8 @@ __device__ __forceinline__ MuonOld read_out(const MuonTarget &T, int64_t at, int
 
 // Four consecutive sums of the last product go there.
 template <bool kPlain>
-__device__ __forceinline__ void write_out(const MuonTarget &T, const MuonOld &o, float4 sums) {
-  constexpr float kUnit = 1.f / (kScaleX * kScaleP);
-  const float v[4] = {sums.x * kUnit, sums.y * kUnit, sums.z * kUnit, sums.w * kUnit};
+__device__ __forceinline__ void write_out(const MuonTarget &T, const MuonOld &o, float unit, float4 sums) {
+  const float v[4] = {sums.x * unit, sums.y * unit, sums.z * unit, sums.w * unit};
   float x[4];
   if (kPlain || T.bf16) {
 #pragma unroll
@@ -481,7 +490,7 @@ __device__ __forceinline__ void write_out(const MuonTarget &T, const MuonOld &o,
 // ------------------------------------------------------------------ products
 // D[n][m] = sum over k of L(m, k) R(n, k), fp32 sums.
 enum {
-  kGram = 0,     // A = X X^T:               L = R = X
+  kGram = 0,     // A = X X^T:               L = R = X; and any product of symmetric matrices that commute
   kPoly = 1,     // P = a I + b A + c A A:   L = R = A
   kUpdate = 2,   // X' = P X:                L = X^T, R = P
   kOut = 3,      // the last X', with L and R as in kUpdate, written where the caller wants it
@@ -502,7 +511,8 @@ struct MuonProduct {
   int tiles_m, tiles_n, tiles;   // of one matrix
   int parts;                // kGramPart, kGramSum
   float *sums;              // their fp32 sums: [matrix][tile][part][a tile's elements as its waves hold them]
-  float a, b, c;
+  float a, b, c;            // kPoly
+  float unit;               // the others: from a sum to the result
   MuonTarget out;           // kOut: element (n, m) of matrix b0 + i goes to its row n, column m
   int64_t b0;
 };
@@ -888,7 +898,7 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
       for (int g = 0; g < kOutTrips; ++g) {
         const MuonOld o = old[g];
         if (j + 1 < T::FN) old[g] = out_spot(j + 1, g);
-        write_out<false>(A.out, o, v[g]);
+        write_out<false>(A.out, o, A.unit, v[g]);
       }
       wave_lds_fence();
       continue;
@@ -916,8 +926,7 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
         for (int e = 0; e < 4; ++e) {
           const float v = acc[i][j][4 * q + e];
           float o = 0.f;
-          if (ROLE == kGram || ROLE == kGramSum) o = v * (1.f / kScaleX);
-          if (ROLE == kUpdate) o = v * (1.f / kScaleP);
+          if (ROLE != kPoly) o = v * A.unit;
           if (ROLE == kPoly) {
             o = (A.b * (kScaleP / kScaleX)) * (float)s[e] + (A.c * (kScaleP / (kScaleX * kScaleX))) * v;
             if (nn == mm + e) o += A.a * kScaleP;
@@ -969,6 +978,11 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
 // known.  X0 is U times the power of two that puts its norm in (1/2, 1] 2^14,
 // and what is left of the factor 1 / max(|U|, eps) goes into the fp32 results
 // of the first step's products, which costs no rounding.
+//
+// P's diagonal holds most of it, the same value all along while A is small: its
+// rounding to fp16 would scale the whole of X.  What the rounding takes off is
+// kept beside P and multiplied as a diagonal matrix, two more matrix
+// instructions to a block (64 x 64: error 1.6e-3 without, 1.2e-3 with).
 constexpr int kMaxSteps = 64;
 constexpr int kSmallWaves = 16;
 
@@ -977,6 +991,7 @@ struct MuonSmall {
   int steps, tall;
   int mp;               // m rounded up to 32
   int parts;            // of the summed index of X X^T
+  int pairs, single;    // steps are taken two together, but for this one
   float eps;
   int64_t b0;           // first matrix of this launch
 };
@@ -988,7 +1003,11 @@ struct SmallLds {
   static constexpr int kParts = NB == 1 ? 8 : NB == 2 ? 4 : NB == 3 ? 2 : 1;   // at most; a power of two
   static constexpr int kScratch = kParts / 2 * kTiles * 4096;
   static constexpr int kRuns = NB == 1 ? 20 : 16;   // runs of 64 x 4 elements that a wave can keep
-  static constexpr int64_t bytes(int64_t mp) { return 32 * NB * (2 * mp + 16) + 2 * 32 * NB * kRow + kScratch + 8 * kSmallWaves; }
+  static constexpr bool kPairs = NB <= 2;                   // a wider matrix that fits is not wide enough for them
+  static constexpr int kSquares = kPairs ? 3 : 2;           // n x n matrices: A, P, and T
+  static constexpr int64_t bytes(int64_t mp) {
+    return 32 * NB * (2 * mp + 16) + kSquares * 32 * NB * kRow + kScratch + 8 * kSmallWaves + 3 * 64 * NB;
+  }
 };
 
 template <int NB, int MOM>
@@ -999,8 +1018,11 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonInput 
   const int64_t b = S.b0 + blockIdx.x;
   const int xrow = 2 * S.mp + 16;
   char *const X = sm, *const A = X + 32 * NB * xrow, *const P = A + 32 * NB * L::kRow;
-  float *const scratch = (float *)(P + 32 * NB * L::kRow);
+  char *const Tm = P + (L::kPairs ? 32 * NB * L::kRow : 0);
+  float *const scratch = (float *)(A + L::kSquares * 32 * NB * L::kRow);
   double *const red = (double *)((char *)scratch + L::kScratch);
+  // what rounding took off the diagonals of P, P2 and P2 P1, in their units
+  _Float16 *const d0 = (_Float16 *)(red + kSmallWaves), *const d1 = d0 + 32 * NB, *const dq = d1 + 32 * NB;
 
   // U and its norm, the new momentum, zeros for X's padding
   if ((S.tall ? I.c : I.r) != 32 * NB || (S.tall ? I.r : I.c) != S.mp) {
@@ -1107,8 +1129,27 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonInput 
     wave_lds_fence();
   };
 
-  for (int t = 0; t < S.steps; ++t) {
-    const float ka = S.k[t][0], kb = S.k[t][1], kc = S.k[t][2];
+  // block `blk` of a diagonal matrix as two fragments: a lane's value stands at
+  // its row's place among the 8 it holds of one of them
+  const int place = row - 8 * half;
+  auto diagonal = [&](const _Float16 *d, int blk, half8 f[2]) {
+    union { _Float16 h; uint16_t u; } v;
+    v.h = d[32 * blk + row];
+    const uint32_t w = (uint32_t)v.u << (16 * (place & 1));
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      union { uint32_t w[4]; half8 h; } to;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) to.w[e] = place >> 1 == 8 * k + e ? w : 0u;
+      f[k] = to.h;
+    }
+  };
+
+  const char *F = P;          // X <- F X, in units of `unit`
+  const _Float16 *fd = d0;    // and what F's diagonal lacks
+  float unit = 1.f / kScaleP;
+  for (int t = 0; t < S.steps;) {
+    const bool two = L::kPairs && S.pairs && t != S.single;
     const float left = t == 0 ? rest : 1.f;
     // A = X X^T: wave = part * kTiles + tile
     {
@@ -1151,50 +1192,87 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonInput 
         if (off > 1) __syncthreads();
       }
       if (part == 0) {
-        const float unit = left * left * (1.f / kScaleX);
+        const float to_a = left * left * (1.f / kScaleX);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           half4 h;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) h[e] = (_Float16)(acc[4 * q + e] * unit);
+          for (int e = 0; e < 4; ++e) h[e] = (_Float16)(acc[4 * q + e] * to_a);
           put(A, ti, tj, q, h);
         }
       }
     }
     __syncthreads();
-    // P = a I + b A + c A A
-    if (wave < L::kTiles) {
-      int ti, tj;
-      tile_at(wave, ti, tj);
-      float16v acc, acc2;
-      zero(acc);
-      zero(acc2);
-      const char *pl = A + (32 * ti + row) * L::kRow + 16 * half, *pr = A + (32 * tj + row) * L::kRow + 16 * half;
+    // phase 0: P = a I + b A + c A A.  Of a pair also 1: T = P A, 2: A = T P,
+    // 3: P2 of that, in T's place, 4: P2 P in A's.
+    for (int ph = 0; ph < (two ? 5 : 1); ++ph) {
+      if (wave < L::kTiles) {
+        const bool poly = ph == 0 || ph == 3;
+        const char *const lb = poly ? A : ph == 1 ? P : Tm, *const rb = poly || ph == 1 ? A : P;
+        char *const to = ph == 0 ? P : ph == 1 || ph == 3 ? Tm : A;
+        int ti, tj;
+        tile_at(wave, ti, tj);
+        float16v acc, acc2;
+        zero(acc);
+        zero(acc2);
+        const char *pl = lb + (32 * ti + row) * L::kRow + 16 * half, *pr = rb + (32 * tj + row) * L::kRow + 16 * half;
 #pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8 *)(pl + 64 * k), *(const half8 *)(pr + 64 * k), acc, 0, 0, 0);
-        acc2 = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8 *)(pl + 64 * k + 32), *(const half8 *)(pr + 64 * k + 32),
-                                                      acc2, 0, 0, 0);
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n = 32 * tj + row, m = 32 * ti + 8 * q + 4 * half;
-        const half4 s = *(const half4 *)(A + n * L::kRow + m * 2);
-        half4 h;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float o = (kb * (kScaleP / kScaleX)) * (float)s[e] +
-                    (kc * (kScaleP / (kScaleX * kScaleX))) * (acc[4 * q + e] + acc2[4 * q + e]);
-          if (n == m + e) o += ka * kScaleP;
-          h[e] = (_Float16)o;
+        for (int k = 0; k < NB; ++k) {
+          acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8 *)(pl + 64 * k), *(const half8 *)(pr + 64 * k), acc, 0, 0, 0);
+          acc2 = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8 *)(pl + 64 * k + 32), *(const half8 *)(pr + 64 * k + 32),
+                                                        acc2, 0, 0, 0);
         }
-        put(P, ti, tj, q, h);
+        if (L::kPairs && (ph == 1 || ph == 4)) {   // the left factor's diagonal
+          half8 f[2];
+          diagonal(ph == 1 ? d0 : d1, ti, f);
+          acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[0], *(const half8 *)(pr + 64 * ti), acc, 0, 0, 0);
+          acc2 = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[1], *(const half8 *)(pr + 64 * ti + 32), acc2, 0, 0, 0);
+        }
+        if (L::kPairs && (ph == 2 || ph == 4)) {   // the right one's
+          half8 f[2];
+          diagonal(d0, tj, f);
+          acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8 *)(pl + 64 * tj), f[0], acc, 0, 0, 0);
+          acc2 = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8 *)(pl + 64 * tj + 32), f[1], acc2, 0, 0, 0);
+        }
+        const int step = ph == 3 ? t + 1 : t;
+        const float ka = poly ? S.k[step][0] * kScaleP : 0.f, kb = poly ? S.k[step][1] * (kScaleP / kScaleX) : 0.f;
+        const float kc = poly     ? S.k[step][2] * (kScaleP / (kScaleX * kScaleX))
+                         : ph == 1 ? 1.f / kScaleX
+                         : ph == 2 ? kScaleX / (kScaleP * kScaleP)
+                                   : kScaleQ / (kScaleP * kScaleP);
+        float own = 0.f;   // this lane's element of the diagonal, if it has one
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int n = 32 * tj + row, m = 32 * ti + 8 * q + 4 * half;
+          half4 s = {0, 0, 0, 0};
+          if (poly) s = *(const half4 *)(A + n * L::kRow + m * 2);
+          half4 h;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float o = kb * (float)s[e] + kc * (acc[4 * q + e] + acc2[4 * q + e]);
+            if (n == m + e) o += ka;
+            own = n == m + e ? o : own;
+            h[e] = (_Float16)o;
+          }
+          put(to, ti, tj, q, h);
+        }
+        // (of phases 1 and 2 it is not used, and written over)
+        if (ti == tj && (row >> 2 & 1) == half)
+          (ph == 0 ? d0 : ph == 3 ? d1 : dq)[32 * tj + row] = (_Float16)(own - (float)(_Float16)own);
       }
+      __syncthreads();
     }
-    __syncthreads();
-    if (t + 1 == S.steps) break;
-    // X <- P X, 32 columns at a time
-    const float unit = left * (1.f / kScaleP);
+    F = two ? A : P;
+    fd = two ? dq : d0;
+    unit = left * (two ? 1.f / kScaleQ : 1.f / kScaleP);
+    t += two ? 2 : 1;
+    if (t >= S.steps) break;
+    // X <- F X, 32 columns at a time
+    half8 fs[NB <= 2 ? NB : 1][2];
+    if (NB <= 2) {
+#pragma unroll
+      for (int ib = 0; ib < NB; ++ib) diagonal(fd, ib, fs[NB <= 2 ? ib : 0]);
+    }
     for (int jp = wave; jp < S.mp / 32; jp += kSmallWaves) {
       half8 x[2 * NB];
       panel(jp, x);
@@ -1202,10 +1280,14 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonInput 
       for (int ib = 0; ib < NB; ++ib) {
         float16v acc;
         zero(acc);
-        const char *pp = P + (32 * ib + row) * L::kRow + 16 * half;
+        const char *pp = F + (32 * ib + row) * L::kRow + 16 * half;
+        half8 *const f = fs[NB <= 2 ? ib : 0];
+        if (NB > 2) diagonal(fd, ib, f);
 #pragma unroll
         for (int k = 0; k < 2 * NB; ++k)
           acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[k], *(const half8 *)(pp + 32 * k), acc, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[2 * ib + k], f[k], acc, 0, 0, 0);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           half4 h;
@@ -1218,9 +1300,8 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonInput 
     __syncthreads();
   }
 
-  // the last P X goes to memory
-  const float left = S.steps == 1 ? rest : 1.f;
-  constexpr float kUnit = 1.f / (kScaleX * kScaleP);
+  // the last F X goes to memory
+  const float kUnit = unit / kScaleX;
   const int r = lane >> 3, c = lane & 7;   // of a 32 x 32 block a lane writes rows r, r + 8, .., columns 4c..
   auto spots = [&](int jp, int ib, MuonOld *old) {
     const int i = S.tall ? 32 * jp + row : 32 * ib + r, j = S.tall ? 32 * ib + 4 * half : 32 * jp + 4 * c;
@@ -1239,26 +1320,33 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonInput 
     half8 x[2 * NB];
     if (kAhead && jp + kSmallWaves < S.mp / 32) spots(jp + kSmallWaves, 0, next);
     panel(jp, x);
+#pragma unroll
     for (int ib = 0; ib < NB; ++ib) {
       float16v acc;
       zero(acc);
-      const char *pp = P + (32 * ib + row) * L::kRow + 16 * half;
+      const char *pp = F + (32 * ib + row) * L::kRow + 16 * half;
+      half8 f[2];
+      diagonal(fd, ib, f);
       if (MOM != kMomNone && !kAhead) spots(jp, ib, old);
       if (S.tall) {
         // rows of the result are columns of X: a lane has four consecutive elements of one
 #pragma unroll
         for (int k = 0; k < 2 * NB; ++k)
           acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(*(const half8 *)(pp + 32 * k), x[k], acc, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[k], x[2 * ib + k], acc, 0, 0, 0);
         if (MOM == kMomNone) spots(jp, ib, old);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if (32 * ib + 8 * q >= (int)out.cols) continue;
-          write_out<MOM == kMomNone>(out, old[q], make_float4(left * acc[4 * q], left * acc[4 * q + 1], left * acc[4 * q + 2], left * acc[4 * q + 3]));
+          write_out<MOM == kMomNone>(out, old[q], kUnit, make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]));
         }
       } else {
 #pragma unroll
         for (int k = 0; k < 2 * NB; ++k)
           acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[k], *(const half8 *)(pp + 32 * k), acc, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) acc = __builtin_amdgcn_mfma_f32_32x32x16_f16(x[2 * ib + k], f[k], acc, 0, 0, 0);
         // A block goes through the panel's place in LDS (32 NB rows of 64
         // bytes), so that memory is written in whole rows of it.
         if (MOM == kMomNone && out.vec && (out.row & 7) == 0 && (out.batch & 7) == 0 && ((uintptr_t)out.out & 15) == 0 &&
@@ -1267,8 +1355,8 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonInput 
 #pragma unroll
           for (int q = 0; q < 4; ++q)
             *(uint2 *)(X + row * xrow + 64 * jp + 16 * q + 8 * half) =
-                make_uint2(f32x2_bf16(left * acc[4 * q] * kUnit, left * acc[4 * q + 1] * kUnit),
-                           f32x2_bf16(left * acc[4 * q + 2] * kUnit, left * acc[4 * q + 3] * kUnit));
+                make_uint2(f32x2_bf16(acc[4 * q] * kUnit, acc[4 * q + 1] * kUnit),
+                           f32x2_bf16(acc[4 * q + 2] * kUnit, acc[4 * q + 3] * kUnit));
           wave_lds_fence();
           uint16_t *to = (uint16_t *)out.out + (b * out.batch + (32 * ib + (lane >> 2)) * out.row + 32 * jp + 8 * (lane & 3));
 #pragma unroll
@@ -1284,12 +1372,12 @@ __global__ __launch_bounds__(64 * kSmallWaves) void muon_small_kernel(MuonInput 
 #pragma unroll
               for (int q = 0; q < 4; ++q)
                 *(float4 *)(X + (2 * (row & 15) + (q >> 1)) * xrow + 64 * jp + ((q & 1) * 8 + 4 * half) * 4) =
-                    make_float4(left * acc[4 * q], left * acc[4 * q + 1], left * acc[4 * q + 2], left * acc[4 * q + 3]);
+                    make_float4(acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]);
             }
             wave_lds_fence();
 #pragma unroll
             for (int e = 0; e < 2; ++e)
-              write_out<MOM == kMomNone>(out, old[2 * p + e], *(const float4 *)(X + (2 * (r + 8 * e) + (c >> 2)) * xrow + 64 * jp + (c & 3) * 16));
+              write_out<MOM == kMomNone>(out, old[2 * p + e], kUnit, *(const float4 *)(X + (2 * (r + 8 * e) + (c >> 2)) * xrow + 64 * jp + (c & 3) * 16));
             wave_lds_fence();
           }
         }

@@ -26,6 +26,13 @@ one of A e_ij = (b + c (s_i^2 + s_j^2)) d_ij s_j, with d symmetric.  Summed over
 entries and steps this is the expected square of the error; FOUR times its root
 is allowed.  This takes singular vectors that are spread over the entries: it is
 used for random matrices, the worst case for special ones.
+
+Two steps may be taken together: T = P1 A, the next A as T P1, Q = P2 P1 and the
+second next X as Q X, with T, A and Q rounded to fp16 and the X between them not.
+A rounding of Q acts like one of P2 would on P1 X, but with |Q| for |P2| and the
+first X's singular values; one of T moves the next A by d_ij p1_j, one of P1 by
+d_ij (A_j p1_j + A_i p1_i) (A, p1: eigenvalues), on top of its own rounding.  The
+bound counts these and the roundings of the steps one by one.
 """
 import torch
 
@@ -75,6 +82,21 @@ def _random(s, n, m, ks):
         var_p = H ** 2 / 3 * (p ** 2).sum() / n ** 2
         var_a = H ** 2 / 3 * (s ** 4).sum() / n ** 2 * (b + c * (s[:, None] ** 2 + s[None, :] ** 2)) ** 2
         total += ((var_p + var_a) * eo).sum()
+        if t + 1 < len(ks):
+            # this step and the next together
+            lam, lam2 = s ** 2, nxt ** 2
+            a2, b2, c2 = ks[t + 1]
+            p2 = a2 + b2 * lam2 + c2 * lam2 ** 2
+            after, _ = _odd(s, ks[t:t + 2])
+            even2, odd2, _ = _moves(after.abs().clamp(min=1e-300), ks[t + 2:])
+            unit = H ** 2 / 3 / n ** 2
+            var_q = unit * ((p * p2) ** 2).sum()
+            total += (var_q * ((even2 * (s[:, None] + s[None, :]) / 2) ** 2 + (odd2 * (s[None, :] - s[:, None]) / 2) ** 2)).sum()
+            var_t = unit * ((p * lam) ** 2).sum() * p[None, :] ** 2
+            var_p1 = unit * (p ** 2).sum() * ((lam * p)[:, None] + (lam * p)[None, :]) ** 2
+            moved = (var_t + var_p1) * (b2 + c2 * (lam2[:, None] + lam2[None, :])) ** 2
+            n1 = nxt.abs()
+            total += (moved * ((even2 * (n1[:, None] + n1[None, :]) / 2) ** 2 + (odd2 * (n1[None, :] - n1[:, None]) / 2) ** 2)).sum()
         s = nxt.abs().clamp(min=1e-300)
     return FOUR * float(total) ** 0.5
 

@@ -128,10 +128,18 @@ def test_orthogonalize_sparse_matrix():
         _check_orthogonal(f"sparse {b}", got[b], u[b], worst=True)
 
 
+@pytest.mark.parametrize("steps", [2, 3, 4, 6, 7])
+@pytest.mark.parametrize("rows,cols", [(16, 900), (60, 700), (140, 4100), (2600, 520)])
+def test_orthogonalize_pairs_of_steps(rows, cols, steps):
+    u = _matrix((rows, cols), 15 * steps)
+    _check_orthogonal(f"{rows}x{cols} steps={steps}", muon.orthogonalize(u.cuda(), steps=steps), u, steps=steps)
+
+
 def test_orthogonalize_coefficients_for_each_step():
     ks = ((4.0, -6.9, 2.9), (3.4445, -4.7750, 2.0315), (1.875, -1.25, 0.375))
-    u = _matrix((90, 130), 14)
-    _check_orthogonal("three triples", muon.orthogonalize(u.cuda(), steps=3, coefficients=ks), u, steps=3, coefficients=ks)
+    for shape in ((90, 130), (40, 600), (150, 4000)):
+        u = _matrix(shape, 14)
+        _check_orthogonal("three triples", muon.orthogonalize(u.cuda(), steps=3, coefficients=ks), u, steps=3, coefficients=ks)
     _check_orthogonal("cubic", muon.orthogonalize(u.cuda(), steps=12, coefficients=(1.5, -0.5, 0.0)), u, steps=12,
                       coefficients=(1.5, -0.5, 0.0))
 

@@ -135,8 +135,21 @@ def test_reference_bound_holds_for_roundings_made_on_the_cpu():
     for shape in ((64, 64), (96, 200), (16, 40)):
         u = torch.randn(shape, generator=g, dtype=torch.float64)
         want, err = R.orthogonalized(u)
-        for mistake in (False, True):
+        for mistake, pairs in ((False, False), (True, False), (False, True)):
             x = half(u / u.norm(), 2.0 ** 14)
+            if pairs:
+                a, b, c = R.COEFFICIENTS
+                eye = torch.eye(len(x), dtype=torch.float64)
+                for two in (True, False, True):
+                    gram = half(x @ x.T, 2.0 ** 14)
+                    p1 = p2 = half(a * eye + b * gram + c * gram @ gram, 2.0 ** 12)
+                    if two:
+                        t = half(p1 @ gram, 2.0 ** 12)
+                        gram = half(t @ p1, 2.0 ** 14)
+                        p2 = half(half(a * eye + b * gram + c * gram @ gram, 2.0 ** 12) @ p1, 2.0 ** 8)
+                    x = half(p2 @ x, 2.0 ** 14)
+                assert (x - want).norm().item() <= err
+                continue
             for _ in range(5):
                 a, b, c = R.COEFFICIENTS
                 gram = half(x @ x.T, 2.0 ** 14)
