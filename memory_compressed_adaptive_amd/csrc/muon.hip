@@ -107,7 +107,7 @@ struct Plan {
   uint32_t runs;
   int nparts;
   Choice gram, poly, update, last;   // tiles of the products of `chunk` matrices
-  size_t x_bytes, a_bytes, part_bytes, sum_bytes, bytes;
+  size_t x_bytes, a_bytes, part_bytes, lost_bytes, sum_bytes, bytes;
 
   Plan(int64_t batch, int64_t rows, int64_t cols) : r(rows), c(cols) {
     tall = r > c;
@@ -123,7 +123,7 @@ struct Plan {
     run.blocks = (int)((c + kMomentumBlock - 1) / kMomentumBlock);
     runs = (uint32_t)run.groups * (uint32_t)run.segs;
     nparts = (int)std::min<int64_t>(kNormParts, (runs + 15) / 16);   // four runs to a wave
-    const size_t one = 2 * 2 * (size_t)(np * mp) + 3 * 2 * (size_t)(np * np) + 8 * (size_t)nparts;
+    const size_t one = 2 * 2 * (size_t)(np * mp) + 3 * 2 * (size_t)(np * np) + 4 * (size_t)np + 8 * (size_t)nparts;
     chunk = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(batch, 65535), (int64_t)(kWorkspaceAim / one)));
     x_bytes = (size_t)round_up(2 * chunk * np * mp, 256);
     a_bytes = (size_t)round_up(2 * chunk * np * np, 256);
@@ -133,10 +133,13 @@ struct Plan {
     poly = pick(np, np, np, chunk, true, false, false);
     update = pick(mp, np, np, chunk, false, false, false);
     last = pick(mp, np, np, chunk, false, true, false);
-    // three products of the short side take the place of two with the long one
-    pairs = 3 * m >= 4 * n && gram.time + update.time > 1.1 * 3.0 * poly.time;
+    // three products of the short side take the place of two with the long one;
+    // with few rows, what rounding does to the diagonals of P1 and T does not
+    // average out (37 x 3000: error 3.0e-3 against 1.4e-3)
+    pairs = n > 128 && 3 * m >= 4 * n && gram.time + update.time > 1.1 * 3.0 * poly.time;
+    lost_bytes = (size_t)round_up(4 * chunk * np, 256);
     sum_bytes = (size_t)round_up((int64_t)gram.bytes, 256);
-    bytes = small ? 256 : 2 * x_bytes + 3 * a_bytes + part_bytes + sum_bytes;
+    bytes = small ? 256 : 2 * x_bytes + 3 * a_bytes + part_bytes + lost_bytes + sum_bytes;
   }
 };
 
@@ -231,7 +234,7 @@ hipError_t run_small(const Plan &p, int64_t batch, const MuonInput &in, const Mu
   // Two steps together save X X^T and P X once, for three short products: a
   // quarter of the time at 64 x 768, a loss below six times as wide as high.
   small.pairs = p.n <= 64 && p.m >= 6 * round_up(p.n, 32);
-  small.single = steps & 1 ? (steps / 2 + 1) / 2 * 2 : -1;
+  small.single = steps & 1 ? 0 : -1;   // first: A is most nearly a multiple of I then
   // parts of at least four products of 16
   small.parts = 1;
   while (2 * small.parts <= small_parts(p.n) && small.mp / 16 / (2 * small.parts) >= 4) small.parts *= 2;
@@ -253,7 +256,8 @@ hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonTarg
   _Float16 *ga = (_Float16 *)w, *gp = (_Float16 *)(w + p.a_bytes), *gt = (_Float16 *)(w + 2 * p.a_bytes);
   w += 3 * p.a_bytes;
   double *part = (double *)w;
-  float *sums = (float *)(w + p.part_bytes);
+  float *lost = (float *)(w + p.part_bytes);
+  float *sums = (float *)(w + p.part_bytes + p.lost_bytes);
   const int64_t nm = p.np * p.mp, nn = p.np * p.np;
   for (int64_t b0 = 0; b0 < batch; b0 += p.chunk) {
     const int64_t cb = std::min(p.chunk, batch - b0);
@@ -299,6 +303,8 @@ hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonTarg
       };
       a.l_mat = a.r_mat = nn;
       a.l_ld = a.r_ld = a.k = p.np;
+      a.lost = two ? nullptr : lost;
+      a.lost_unit = 1.f / kScaleP;
       poly(ga, gp, t);
       const _Float16 *factor = gp;
       float unit = 1.f / kScaleP;
@@ -306,6 +312,8 @@ hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonTarg
         square(gp, ga, gt, 1.f / kScaleX);                        // T = P A
         square(gt, gp, ga, kScaleX / (kScaleP * kScaleP));        // the next A
         poly(ga, gt, t + 1);
+        a.lost = lost;
+        a.lost_unit = 1.f / kScaleQ;
         square(gt, gp, ga, kScaleQ / (kScaleP * kScaleP));        // P2 P1
         factor = ga;
         unit = 1.f / kScaleQ;

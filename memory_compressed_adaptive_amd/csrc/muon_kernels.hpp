@@ -513,6 +513,13 @@ struct MuonProduct {
   float *sums;              // their fp32 sums: [matrix][tile][part][a tile's elements as its waves hold them]
   float a, b, c;            // kPoly
   float unit;               // the others: from a sum to the result
+  // What rounding takes off the diagonal of P (or of a product of two), in real
+  // units, [matrix][n]: written with it where not null, and added by kUpdate as
+  // that many times the old X.  The diagonal holds most of a P while A is
+  // small, and nearly the same value all along: its rounding would scale X as a
+  // whole (440 x 6000: error 2.1e-3 without, 1.1e-3 with).
+  float *lost;
+  float lost_unit;
   MuonTarget out;           // kOut: element (n, m) of matrix b0 + i goes to its row n, column m
   int64_t b0;
 };
@@ -848,22 +855,25 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
   // Each wave brings 32 rows (n) x TM of its part through LDS at a time, so
   // that memory is written in whole runs of a row.
   char *mine = smem + wave * (32 * (T::TM * 4 + 16));
-  // kPoly: A's part of the tile, whole rows at a time and all reads under way
-  // together (read four elements at a time by the lanes that need them, it
-  // took 20 000 cycles of a 192 x 192 tile's 150 000)
-  constexpr int kRowChunks = T::TM / 8, kATrips = ROLE == kPoly ? 32 * kRowChunks / 64 : 1;
-  half8 olda[ROLE == kPoly ? T::FN : 1][kATrips];
-  if (ROLE == kPoly) {
+  // A's part of the tile (kPoly) or the old X's (kUpdate), whole rows at a time
+  // and 32 rows ahead (read four elements at a time by the lanes that need
+  // them, A took 20 000 cycles of a 192 x 192 tile's 150 000)
+  constexpr bool kBeside = ROLE == kPoly || ROLE == kUpdate;
+  constexpr int kRowChunks = T::TM / 8, kTrips = kBeside ? 32 * kRowChunks / 64 : 1;
+  half8 beside[2][kTrips];
+  float keep[2] = {0.f, 0.f};   // kUpdate: what P's diagonal lacks at this lane's row
+  auto read_beside = [&](int j) {
 #pragma unroll
-    for (int j = 0; j < T::FN; ++j)
-#pragma unroll
-      for (int g = 0; g < kATrips; ++g) {
-        const int row = (g * 64 + lane) / kRowChunks, c = (g * 64 + lane) % kRowChunks;
-        const int64_t nn = n0 + wn + 32 * j + row, mm = m0 + wm + 8 * c;
-        olda[j][g] = half8{0, 0, 0, 0, 0, 0, 0, 0};
-        if (nn < A.n && mm < A.m) olda[j][g] = *(const half8 *)(A.l + lb * A.l_mat + nn * A.m + mm);
-      }
-  }
+    for (int g = 0; g < kTrips; ++g) {
+      const int row = (g * 64 + lane) / kRowChunks, c = (g * 64 + lane) % kRowChunks;
+      const int64_t nn = n0 + wn + 32 * j + row, mm = m0 + wm + 8 * c;
+      beside[j & 1][g] = half8{0, 0, 0, 0, 0, 0, 0, 0};
+      if (nn < A.n && mm < A.m) beside[j & 1][g] = *(const half8 *)(A.l + lb * A.l_mat + nn * A.l_ld + mm);
+    }
+    const int64_t nn = n0 + wn + 32 * j + (lane & 31);
+    if (ROLE == kUpdate) keep[j & 1] = nn < A.n ? A.lost[lb * A.n + nn] : 0.f;
+  };
+  if (kBeside) read_beside(0);
   constexpr int kOutChunks = T::TM / 4, kOutTrips = 32 * kOutChunks / 64;
   auto out_spot = [&](int j, int g) {
     const int row = (g * 64 + lane) / kOutChunks, c = (g * 64 + lane) % kOutChunks;
@@ -906,35 +916,41 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
     constexpr int kStride = T::TM * 2 + 16;
     const int64_t dn = A.m;   // elements of a row of D
     _Float16 *d = A.d + lb * A.m * A.n;
-    if (ROLE == kPoly) {
+    if (kBeside) {
 #pragma unroll
-      for (int g = 0; g < kATrips; ++g) {
+      for (int g = 0; g < kTrips; ++g) {
         const int row = (g * 64 + lane) / kRowChunks, c = (g * 64 + lane) % kRowChunks;
-        *(half8 *)(mine + row * kStride + c * 16) = olda[j][g];
+        *(half8 *)(mine + row * kStride + c * 16) = beside[j & 1][g];
       }
+      if (j + 1 < T::FN) read_beside(j + 1);
       wave_lds_fence();
     }
 #pragma unroll
-    for (int i = 0; i < T::FM; ++i)
+    for (int i = 0; i < T::FM; ++i) {
+      const bool diagonal = SYM && nb == mb + 32 * i;   // uniform: this 32 x 32 block holds the diagonal
+      float own = 0.f;                                  // and this lane, if it does, this element of it
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int r = 32 * i + 8 * q + 4 * (lane >> 5);
-        const int64_t nn = nb + (lane & 31), mm = mb + r;   // and the next three
         half4 h, s = {0, 0, 0, 0};
-        if (ROLE == kPoly) s = *(const half4 *)(mine + (lane & 31) * kStride + r * 2);
+        if (kBeside) s = *(const half4 *)(mine + (lane & 31) * kStride + r * 2);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float v = acc[i][j][4 * q + e];
-          float o = 0.f;
-          if (ROLE != kPoly) o = v * A.unit;
+          float o = v * A.unit;
+          if (ROLE == kUpdate) o += keep[j & 1] * (float)s[e];
           if (ROLE == kPoly) {
             o = (A.b * (kScaleP / kScaleX)) * (float)s[e] + (A.c * (kScaleP / (kScaleX * kScaleX))) * v;
-            if (nn == mm + e) o += A.a * kScaleP;
+            if (diagonal && (lane & 31) == 8 * q + 4 * (lane >> 5) + e) o += A.a * kScaleP;
           }
+          if (SYM) own = (lane & 31) == 8 * q + 4 * (lane >> 5) + e ? o : own;
           h[e] = (_Float16)o;
         }
         *(half4 *)(mine + (lane & 31) * kStride + r * 2) = h;
       }
+      if (SYM && diagonal && A.lost && (lane >> 2 & 1) == lane >> 5 && nb + (lane & 31) < A.n)
+        A.lost[lb * A.n + nb + (lane & 31)] = (own - (float)(_Float16)own) * A.lost_unit;
+    }
     wave_lds_fence();
 #pragma unroll
     for (int g = lane; g < 32 * kRowChunks; g += 64) {
