@@ -1,0 +1,134 @@
+"""torch_optim.Muon: its steps are those of the operators on the stacked
+parameters, alone and beside MicroAdamW, and its state round-trips."""
+import pytest
+import torch
+
+from gpu_harness import say
+from memory_compressed_adaptive_amd import muon
+from memory_compressed_adaptive_amd.torch_optim import MicroAdamW, Muon
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+SHAPES = [(40, 70), (300, 130), (40, 70), (3, 20, 90), (40, 70)]
+
+
+def _params(seed, dtype=torch.float32):
+    g = torch.Generator().manual_seed(seed)
+    return [torch.nn.Parameter((0.02 * torch.randn(s, generator=g)).to(dtype).cuda()) for s in SHAPES]
+
+
+def _grads(seed):
+    g = torch.Generator().manual_seed(seed)
+    return [1e-3 * torch.randn(s, generator=g).cuda() for s in SHAPES]
+
+
+@pytest.mark.parametrize("dtype,bits", [(torch.float32, 32), (torch.float32, 8), (torch.bfloat16, 32), (torch.bfloat16, 8)])
+def test_steps_are_the_operators(dtype, bits):
+    ps, ref = _params(1, dtype), [p.detach().clone() for p in _params(1, dtype)]
+    opt = Muon(ps, lr=0.01, weight_decay=0.1, momentum_bits=bits)
+    mom = [torch.zeros(p.shape, device="cuda") for p in ref]
+    codes = [torch.zeros(p.shape, dtype=torch.int8, device="cuda") for p in ref]
+    scales = [torch.zeros(muon.scales_shape(p.shape), device="cuda") for p in ref]
+    for t in range(4):
+        gs = _grads(10 + t)
+        missing = {1: {0}, 2: {2, 3}}.get(t, set())   # parameters without a gradient: left alone
+        for i, (p, g) in enumerate(zip(ps, gs)):
+            p.grad = None if i in missing else g.to(dtype)
+        if t == 3:
+            opt.param_groups[0]["lr"] = 0.003
+        lr = opt.param_groups[0]["lr"]
+        say(f"[torch muon] step {t} {dtype} bits={bits}")
+        opt.step()
+        for i, p in enumerate(ref):
+            if i in missing:
+                continue
+            g = gs[i].to(dtype).bfloat16()
+            if bits == 8:
+                muon.muon8_step(p, g, codes[i], scales[i], lr=lr, wd=0.1)
+            else:
+                muon.muon_step(p, g, mom[i], lr=lr, wd=0.1)
+        for i, (p, q) in enumerate(zip(ps, ref)):
+            assert torch.equal(p.detach(), q), (t, i)
+    assert ps[0].data_ptr() == opt.param_groups[0]["_stacks"][0]["params"].data_ptr()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_state_dict_resume(bits):
+    def run(split):
+        ps = _params(5)
+        opt = Muon(ps, lr=0.01, momentum_bits=bits)
+        for t in range(6):
+            if t == split:
+                sd = opt.state_dict()
+                ps2 = _params(6)
+                for a, b in zip(ps2, ps):
+                    a.data.copy_(b.data)
+                opt = Muon(ps2, lr=0.5, momentum_bits=bits)
+                opt.load_state_dict(sd)
+                assert opt.param_groups[0]["lr"] == 0.01
+                ps = ps2
+            for p, g in zip(ps, _grads(20 + t)):
+                p.grad = g
+            opt.step()
+        return ps
+
+    for a, b in zip(run(3), run(-1)):
+        assert torch.equal(a, b)
+
+
+def test_load_refuses_another_momentum():
+    a, b = Muon(_params(1)), Muon(_params(1), momentum_bits=8)
+    with pytest.raises(ValueError):
+        b.load_state_dict(a.state_dict())
+    with pytest.raises(ValueError):
+        Muon(_params(1)[:2]).load_state_dict(a.state_dict())
+
+
+def test_added_group_and_refusals():
+    ps = _params(1)
+    opt = Muon(ps[:2])
+    opt.add_param_group({"params": ps[2:], "lr": 0.02})
+    for p, g in zip(ps, _grads(1)):
+        p.grad = g
+    before = [p.detach().clone() for p in ps]
+    opt.step()
+    assert all(not torch.equal(p, q) for p, q in zip(ps, before))
+    with pytest.raises(ValueError):
+        opt.add_param_group({"params": [torch.nn.Parameter(torch.zeros(4, device="cuda"))]})
+    with pytest.raises(ValueError):
+        opt.add_param_group({"params": [torch.nn.Parameter(torch.zeros(4, 4, dtype=torch.float16, device="cuda"))]})
+    assert len(opt.param_groups) == 2
+    opt.step()
+
+
+def test_a_model_trained_by_both_optimizers():
+    """Matrices to Muon (8-bit momentum), the rest to MicroAdamW, as a user sets
+    them up; each update is checked against the operators' own."""
+    torch.manual_seed(0)
+    model = torch.nn.Sequential(torch.nn.Linear(48, 96), torch.nn.Tanh(), torch.nn.Linear(96, 96), torch.nn.Tanh(),
+                                torch.nn.Linear(96, 8)).cuda()
+    matrices = [p for p in model.parameters() if p.dim() == 2]
+    rest = [p for p in model.parameters() if p.dim() != 2]
+    opts = [Muon(matrices, lr=1e-2, momentum_bits=8), MicroAdamW(rest, lr=1e-3, density=0.05, m=4, block=256)]
+    x, y = torch.randn(64, 48, device="cuda"), torch.randn(64, 8, device="cuda")
+    codes = [torch.zeros(p.shape, dtype=torch.int8, device="cuda") for p in matrices]
+    scales = [torch.zeros(muon.scales_shape(p.shape), device="cuda") for p in matrices]
+    for _ in range(5):
+        for o in opts:
+            o.zero_grad()
+        loss = torch.nn.functional.mse_loss(model(x), y)
+        loss.backward()
+        want = [p.detach().clone() for p in matrices]
+        for p, q, c, s in zip(want, matrices, codes, scales):
+            muon.muon8_step(p, q.grad.bfloat16(), c, s, lr=1e-2)
+        for o in opts:
+            o.step()
+        assert all(torch.equal(p.detach(), q) for p, q in zip(matrices, want))
+        assert all(bool(p.isfinite().all()) for p in model.parameters())
