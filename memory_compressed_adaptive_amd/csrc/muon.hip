@@ -48,6 +48,7 @@ using Tile64 = Tile<64, 64, 2, 2, 64, 4, 2>;
 using Tile128 = Tile<128, 128, 2, 2, 64, 2>;
 using Tile128Deep = Tile<128, 128, 4, 2, 64, 4>;   // alone on a CU
 using Tile192 = Tile<192, 192, 2, 2, 64, 2>;
+using Tile256x192 = Tile<256, 192, 4, 2, 64, 2>;
 using Tile256 = Tile<256, 256, 4, 2, 64, 2>;
 
 // How a product is made: which tile, and (X X^T) in how many parts.
@@ -57,6 +58,14 @@ struct Choice {
   size_t bytes;   // the parts' sums
   double time;    // expected, in microseconds
 };
+
+int64_t count_tiles(int64_t m, int64_t n, int bm, int bn, bool symmetric) {
+  const int64_t tm = (m + bm - 1) / bm, tn = (n + bn - 1) / bn;
+  if (!symmetric) return tm * tn;
+  int64_t tiles = 0;
+  for (int64_t j = 0; j < tn; ++j) tiles += tiles_beside((int)j, bm, bn, (int)tm);
+  return tiles;
+}
 
 // The tile with the shortest expected time.  Workgroups go over the 256 CUs in
 // rounds; a round takes so long for 64 of the summed index and so long for its
@@ -69,21 +78,21 @@ struct Choice {
 // Parts of the summed index fill the card where there are few tiles; their sums
 // cost another launch and their way through memory.
 Choice pick(int64_t m, int64_t n, int64_t k, int64_t chunk, bool symmetric, bool out, bool may_split) {
-  const struct { int kind, side, per_cu; double alone, full, ends, out; } kinds[] = {
-      {256, 256, 1, 1.76, 1.76, 5.0, 14.0},
-      {192, 192, 1, 1.14, 1.14, 4.0, 10.0},
-      {128, 128, 2, 0.60, 1.02, 3.5, 6.0},
-      {129, 128, 1, 0.45, 0.95, 3.5, 6.0},
-      {64, 64, 2, 0.26, 0.40, 2.5, 3.5}};
+  const struct { int kind, bm, bn, per_cu; double alone, full, ends, out; } kinds[] = {
+      {256, 256, 256, 1, 1.76, 1.76, 5.0, 14.0},
+      {250, 256, 192, 1, 1.38, 1.38, 4.5, 12.0},
+      {192, 192, 192, 1, 1.14, 1.14, 4.0, 10.0},
+      {128, 128, 128, 2, 0.60, 1.02, 3.5, 6.0},
+      {129, 128, 128, 1, 0.45, 0.95, 3.5, 6.0},
+      {64, 64, 64, 2, 0.26, 0.40, 2.5, 3.5}};
   Choice best = {0, 1, 0, 0.0};
   double least = 0.0;
   for (const auto &t : kinds) {
-    const int64_t tm = (m + t.side - 1) / t.side, tn = (n + t.side - 1) / t.side;
-    const int64_t tiles = (symmetric ? tn * (tn + 1) / 2 : tm * tn) * chunk;
-    for (int parts = 1; parts <= (may_split && t.side <= 128 ? 32 : 1) && (parts == 1 || k / 64 >= 4 * parts); parts *= 2) {
+    const int64_t tiles = count_tiles(m, n, t.bm, t.bn, symmetric) * chunk;
+    for (int parts = 1; parts <= (may_split && t.bm <= 128 ? 32 : 1) && (parts == 1 || k / 64 >= 4 * parts); parts *= 2) {
       const int64_t groups = tiles * parts, whole = groups / (256 * t.per_cu), rest = groups - whole * 256 * t.per_cu;
       const double its = (double)((k / 64 + parts - 1) / parts), ends = out ? t.out : t.ends;
-      const size_t bytes = parts > 1 ? (size_t)groups * t.side * t.side * 4 : 0;
+      const size_t bytes = parts > 1 ? (size_t)groups * t.bm * t.bn * 4 : 0;
       if (bytes > (size_t)64 << 20) break;
       double time = (double)whole * (its * t.full + ends) +
                     (rest == 0 ? 0.0 : its * (rest > 256 || whole > 0 ? t.full : t.alone) + ends);
@@ -101,6 +110,7 @@ struct Plan {
   bool tall;
   bool small;               // a workgroup for each matrix, no workspace
   bool pairs;               // two steps are taken together
+  bool diagonal;            // what rounding takes off P's diagonal is added back
   int64_t np, mp;           // padded
   int64_t chunk;            // matrices at a time
   MuonRun run;              // how waves go over the stored matrix
@@ -137,6 +147,9 @@ struct Plan {
     // with few rows, what rounding does to the diagonals of P1 and T does not
     // average out (37 x 3000: error 3.0e-3 against 1.4e-3)
     pairs = n > 128 && 3 * m >= 4 * n && gram.time + update.time > 1.1 * 3.0 * poly.time;
+    // where A stays near a multiple of I; it takes a tenth of P X's time (768 x
+    // 768: error 1.25e-3 without, 0.85e-3 with)
+    diagonal = m >= 2 * n;
     lost_bytes = (size_t)round_up(4 * chunk * np, 256);
     sum_bytes = (size_t)round_up((int64_t)gram.bytes, 256);
     bytes = small ? 256 : 2 * x_bytes + 3 * a_bytes + part_bytes + lost_bytes + sum_bytes;
@@ -187,7 +200,7 @@ template <class T, int ROLE>
 void product_t(MuonProduct a, int64_t chunk, hipStream_t s) {
   a.tiles_m = (int)((a.m + T::BM - 1) / T::BM);
   a.tiles_n = (int)((a.n + T::BN - 1) / T::BN);
-  a.tiles = ROLE == kUpdate || ROLE == kOut || ROLE == kOutTall ? a.tiles_m * a.tiles_n : a.tiles_n * (a.tiles_n + 1) / 2;
+  a.tiles = (int)count_tiles(a.m, a.n, T::BM, T::BN, ROLE != kUpdate && ROLE != kOut && ROLE != kOutTall);
   const int64_t groups = (int64_t)a.tiles * (ROLE == kGramPart ? a.parts : 1);
   if (ROLE != kGramPart && ROLE != kGramSum) a.parts = 1;
   // small tiles: a row of the grid for each matrix; else the kernel divides
@@ -199,6 +212,7 @@ template <int ROLE>
 void product(const MuonProduct &a, int64_t chunk, int kind, hipStream_t s) {
   if constexpr (ROLE != kGramPart && ROLE != kGramSum) {
     if (kind == 256) return product_t<Tile256, ROLE>(a, chunk, s);
+    if (kind == 250) return product_t<Tile256x192, ROLE>(a, chunk, s);
     if (kind == 192) return product_t<Tile192, ROLE>(a, chunk, s);
   }
   switch (kind) {
@@ -303,7 +317,8 @@ hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonTarg
       };
       a.l_mat = a.r_mat = nn;
       a.l_ld = a.r_ld = a.k = p.np;
-      a.lost = two ? nullptr : lost;
+      float *const keep = p.diagonal ? lost : nullptr;
+      a.lost = two ? nullptr : keep;
       a.lost_unit = 1.f / kScaleP;
       poly(ga, gp, t);
       const _Float16 *factor = gp;
@@ -312,7 +327,7 @@ hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonTarg
         square(gp, ga, gt, 1.f / kScaleX);                        // T = P A
         square(gt, gp, ga, kScaleX / (kScaleP * kScaleP));        // the next A
         poly(ga, gt, t + 1);
-        a.lost = lost;
+        a.lost = keep;
         a.lost_unit = 1.f / kScaleQ;
         square(gt, gp, ga, kScaleQ / (kScaleP * kScaleP));        // P2 P1
         factor = ga;

@@ -597,13 +597,21 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
+// How many tiles of row tj of a symmetric result are made: those that hold an
+// element (n, m) with m <= n.
+__host__ __device__ __forceinline__ int tiles_beside(int tj, int bm, int bn, int tiles_m) {
+  const int n = (bn * (tj + 1) + bm - 1) / bm;
+  return n < tiles_m ? n : tiles_m;
+}
+
 // Which tile (ti along M, tj along N) of which matrix a workgroup makes.
 // Workgroups go to the eight XCDs in turn; each XCD gets one run of tiles,
 // taken in blocks of 4 x 4, so that the panels its 32 CUs read at a time fit
 // its L2.  SYM: only tiles with ti <= tj, the others are their mirror images.
+// (Not so where tiles are not square, which are used where one round takes all.)
 // Small tiles are taken as they come: their products are short, and L2 holds
 // what they read.
-template <bool SYM, bool PLAIN, bool PARTS>
+template <bool SYM, bool PLAIN, bool PARTS, int BM, int BN>
 __device__ __forceinline__ void tile_of(const MuonProduct &A, int &lb, int &ti, int &tj, int &part) {
   uint32_t at = blockIdx.x;
   if (!PLAIN) {
@@ -621,7 +629,11 @@ __device__ __forceinline__ void tile_of(const MuonProduct &A, int &lb, int &ti, 
     lb = (int)(at / (uint32_t)A.tiles);
     r = (int)(at - (uint32_t)lb * A.tiles);
   }
-  if (SYM && PLAIN) {
+  if (SYM && BM != BN) {
+    tj = 0;
+    for (int n; (n = tiles_beside(tj, BM, BN, A.tiles_m)) <= r; ++tj) r -= n;
+    ti = r;
+  } else if (SYM && PLAIN) {
     int y = (int)((sqrtf(8.f * (float)r + 1.f) - 1.f) * 0.5f);
     while (y * (y + 1) / 2 > r) --y;
     while ((y + 1) * (y + 2) / 2 <= r) ++y;
@@ -709,7 +721,7 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
   const int lane = (int)(threadIdx.x & 63u), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
   const int wm = wave % T::WM * T::TM, wn = wave / T::WM * T::TN;
   int lb, ti, tj, part;
-  tile_of<SYM, T::BM == 64, ROLE == kGramPart>(A, lb, ti, tj, part);
+  tile_of<SYM, T::BM == 64, ROLE == kGramPart, T::BM, T::BN>(A, lb, ti, tj, part);
   const int64_t m0 = (int64_t)ti * T::BM, n0 = (int64_t)tj * T::BN;
 
   constexpr int kSums = T::kWaves * T::FM * T::FN * 1024;   // of a tile
@@ -767,6 +779,26 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fx[g * T::FM + i], fy[g * T::FN + j], acc[i][j], 0, 0, 0);
   };
 
+  // A's part of the tile (kPoly) or the old X's (kUpdate), whole rows at a time
+  // and 32 rows ahead, the first of them before the main loop (read four elements at a time by the lanes that need
+  // them, A took 20 000 cycles of a 192 x 192 tile's 150 000)
+  constexpr bool kBeside = ROLE == kPoly || ROLE == kUpdate;
+  constexpr int kRowChunks = T::TM / 8, kTrips = kBeside ? 32 * kRowChunks / 64 : 1;
+  half8 beside[2][kTrips];
+  float keep[2] = {0.f, 0.f};   // kUpdate: what P's diagonal lacks at this lane's row
+  const bool use_beside = ROLE == kPoly || (ROLE == kUpdate && A.lost != nullptr);   // uniform
+  auto read_beside = [&](int j) {
+#pragma unroll
+    for (int g = 0; g < kTrips; ++g) {
+      const int row = (g * 64 + lane) / kRowChunks, c = (g * 64 + lane) % kRowChunks;
+      const int64_t nn = n0 + wn + 32 * j + row, mm = m0 + wm + 8 * c;
+      beside[j & 1][g] = half8{0, 0, 0, 0, 0, 0, 0, 0};
+      if (nn < A.n && mm < A.m) beside[j & 1][g] = *(const half8 *)(A.l + lb * A.l_mat + nn * A.l_ld + mm);
+    }
+    const int64_t nn = n0 + wn + 32 * j + (lane & 31);
+    if (ROLE == kUpdate) keep[j & 1] = nn < A.n ? A.lost[lb * A.n + nn] : 0.f;
+  };
+  if (use_beside) read_beside(0);
   // Copies past the last step go to an empty buffer, so that the loop has one
   // shape and a wait counts the same copies at every step.
   uint64_t al = (uint64_t)pl, ar = (uint64_t)pr, el = (uint64_t)nl, er = (uint64_t)nr;   // of the next step to copy
@@ -855,25 +887,6 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
   // Each wave brings 32 rows (n) x TM of its part through LDS at a time, so
   // that memory is written in whole runs of a row.
   char *mine = smem + wave * (32 * (T::TM * 4 + 16));
-  // A's part of the tile (kPoly) or the old X's (kUpdate), whole rows at a time
-  // and 32 rows ahead (read four elements at a time by the lanes that need
-  // them, A took 20 000 cycles of a 192 x 192 tile's 150 000)
-  constexpr bool kBeside = ROLE == kPoly || ROLE == kUpdate;
-  constexpr int kRowChunks = T::TM / 8, kTrips = kBeside ? 32 * kRowChunks / 64 : 1;
-  half8 beside[2][kTrips];
-  float keep[2] = {0.f, 0.f};   // kUpdate: what P's diagonal lacks at this lane's row
-  auto read_beside = [&](int j) {
-#pragma unroll
-    for (int g = 0; g < kTrips; ++g) {
-      const int row = (g * 64 + lane) / kRowChunks, c = (g * 64 + lane) % kRowChunks;
-      const int64_t nn = n0 + wn + 32 * j + row, mm = m0 + wm + 8 * c;
-      beside[j & 1][g] = half8{0, 0, 0, 0, 0, 0, 0, 0};
-      if (nn < A.n && mm < A.m) beside[j & 1][g] = *(const half8 *)(A.l + lb * A.l_mat + nn * A.l_ld + mm);
-    }
-    const int64_t nn = n0 + wn + 32 * j + (lane & 31);
-    if (ROLE == kUpdate) keep[j & 1] = nn < A.n ? A.lost[lb * A.n + nn] : 0.f;
-  };
-  if (kBeside) read_beside(0);
   constexpr int kOutChunks = T::TM / 4, kOutTrips = 32 * kOutChunks / 64;
   auto out_spot = [&](int j, int g) {
     const int row = (g * 64 + lane) / kOutChunks, c = (g * 64 + lane) % kOutChunks;
@@ -916,7 +929,7 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
     constexpr int kStride = T::TM * 2 + 16;
     const int64_t dn = A.m;   // elements of a row of D
     _Float16 *d = A.d + lb * A.m * A.n;
-    if (kBeside) {
+    if (use_beside) {
 #pragma unroll
       for (int g = 0; g < kTrips; ++g) {
         const int row = (g * 64 + lane) / kRowChunks, c = (g * 64 + lane) % kRowChunks;
@@ -933,7 +946,7 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
       for (int q = 0; q < 4; ++q) {
         const int r = 32 * i + 8 * q + 4 * (lane >> 5);
         half4 h, s = {0, 0, 0, 0};
-        if (kBeside) s = *(const half4 *)(mine + (lane & 31) * kStride + r * 2);
+        if (use_beside) s = *(const half4 *)(mine + (lane & 31) * kStride + r * 2);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float v = acc[i][j][4 * q + e];
@@ -956,13 +969,15 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
     for (int g = lane; g < 32 * kRowChunks; g += 64) {
       const int row = g / kRowChunks, c = g % kRowChunks;
       const half8 h = *(const half8 *)(mine + row * kStride + c * 16);
-      if (nb + row < A.n && mb + 8 * c < A.m) *(half8 *)(d + (nb + row) * dn + mb + 8 * c) = h;
+      // of a symmetric result the 32 x 32 blocks with m <= n
+      if (nb + row < A.n && mb + 8 * c < A.m && (!SYM || mb + 8 * c < nb + 32)) *(half8 *)(d + (nb + row) * dn + mb + 8 * c) = h;
     }
-    if (SYM && ti < tj) {
-      // the mirror image: lane s of 16 gets column s of 4 rows at a time
+    if (SYM && mb < nb) {
+      // their mirror image: lane s of 16 gets column s of 4 rows at a time
       const int s = lane & 15, oct = lane >> 4;
 #pragma unroll
       for (int c = 0; c < T::TM / 16; ++c) {
+        if (mb + 16 * c >= nb) continue;
         union { short4v s[2]; half8 h; } u;
 #pragma unroll
         for (int e = 0; e < 2; ++e)

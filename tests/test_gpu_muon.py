@@ -52,7 +52,7 @@ def test_orthogonalize_sizes(rows, cols, steps):
     _check_orthogonal(f"{rows}x{cols} steps={steps}", got, u, steps=steps)
 
 
-@pytest.mark.parametrize("rows,cols,batch", [(64, 64, 5), (40, 200, 3), (200, 40, 70), (260, 300, 3), (300, 20, 300)])
+@pytest.mark.parametrize("rows,cols,batch", [(64, 64, 5), (40, 200, 3), (200, 40, 70), (260, 300, 3), (300, 20, 300), (1024, 1020, 15)])
 def test_orthogonalize_batch(rows, cols, batch):
     u = _matrix((batch, rows, cols), rows, torch.bfloat16)
     u *= torch.logspace(-6, 6, batch).bfloat16()[:, None, None]   # each matrix has its own norm
