@@ -280,7 +280,8 @@ hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonTarg
     const int64_t sp = p.tall ? p.np : p.mp, tp = p.tall ? p.mp : p.np;
     _Float16 *x = x0, *nx = x1;
     const int64_t wide = 4 << p.run.log_lanes, across = (sp + wide - 1) / wide;
-    const bool few = across * ((tp + 63) / 64) * cb < 512;
+    // (a wave that goes over more than 16 rows at once would pass a block of 16)
+    const bool few = p.run.log_lanes >= 2 && across * ((tp + 63) / 64) * cb < 512;
     const int rows = few ? 16 : 64;
     const dim3 lg((unsigned)across, (unsigned)((tp + rows - 1) / rows), (unsigned)cb);
     const auto load = p.tall ? (few ? muon_load_kernel<MOM, true, 16> : muon_load_kernel<MOM, true, 64>)

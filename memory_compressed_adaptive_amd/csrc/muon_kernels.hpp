@@ -347,7 +347,8 @@ __device__ __forceinline__ double muon_factor(double squares, float eps) {
 // padding: as the matrix is stored, or transposed if that is tall.  A block of
 // 256 threads takes kLoadRows rows x 4 * lanes columns of the stored
 // matrix: 64, or 16 where that gives few blocks (768 x 768: 36 blocks take 11
-// us, 144 take 5).  sp, tp: the stored orientation's padded columns and rows.
+// us, 144 take 5; 64 >> log_lanes rows, what a wave goes over at once, must fit
+// in it).  sp, tp: the stored orientation's padded columns and rows.
 template <int MOM, bool TALL, int kLoadRows>
 __global__ __launch_bounds__(256) void muon_load_kernel(MuonInput I, MuonRun run, int64_t b0, const double *part, int nparts,
                                                         float eps, _Float16 *X, int64_t sp, int64_t tp) {

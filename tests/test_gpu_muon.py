@@ -52,6 +52,14 @@ def test_orthogonalize_sizes(rows, cols, steps):
     _check_orthogonal(f"{rows}x{cols} steps={steps}", got, u, steps=steps)
 
 
+@pytest.mark.parametrize("rows,cols", [(2500, 8), (3900, 5), (2300, 4), (2600, 2), (4500, 8)])
+def test_orthogonalize_long_and_very_narrow(rows, cols):
+    """A wave of the load kernel goes over 32 or 64 rows of these at once, and the
+    matrices are too long for one workgroup's LDS."""
+    u = _matrix((rows, cols), rows + cols)
+    _check_orthogonal(f"{rows}x{cols}", muon.orthogonalize(u.cuda()), u)
+
+
 @pytest.mark.parametrize("rows,cols,batch", [(64, 64, 5), (40, 200, 3), (200, 40, 70), (260, 300, 3), (300, 20, 300), (1024, 1020, 15)])
 def test_orthogonalize_batch(rows, cols, batch):
     u = _matrix((batch, rows, cols), rows, torch.bfloat16)
