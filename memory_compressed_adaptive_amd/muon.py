@@ -6,9 +6,10 @@ on one matrix [rows, cols] or on a batch of equally shaped ones [..., rows,
 cols] in one go (ma_orthogonalize, ma_muon_step, ma_muon8_step and
 ma_momentum8_values of include/microadam.h; the formulas and their rounding
 stand there).  Calls are asynchronous on `stream` (default: the current stream
-of the tensors' device), allocate their workspace through torch on that stream
-and can be captured into a graph.  A tensor that another stream made must be
-ordered before `stream` by the caller, as for any kernel.
+of the tensors' device), allocate their workspace and new results through torch
+on that stream and can be captured into a graph.  A tensor that another stream
+made must be ordered before `stream` by the caller, as for any kernel, and so
+must what another stream does with a result.
 """
 from __future__ import annotations
 
@@ -69,16 +70,22 @@ def _type(t, what: str) -> int:
     return _L.MA_TYPE_F32 if t.dtype == torch.float32 else _L.MA_TYPE_BF16
 
 
-def _stream_and_workspace(device, nbytes: int, stream):
-    """The stream to use, and a workspace that torch's allocator gave to it."""
+def _place(device, stream):
+    """The stream to use, and a context for allocations and the call: in it torch
+    allocates on that stream, and its device is the current one (a device's
+    default stream has no other mark)."""
     import torch
     current = torch.cuda.current_stream(device)
     s = current if stream is None else stream
     _L.require(s.device == device, "the stream must be of the tensors' device")
-    ctx = contextlib.nullcontext() if s == current else torch.cuda.stream(s)
-    with ctx:
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return s, ws
+    if s == current and torch.cuda.current_device() == device.index:
+        return s, contextlib.nullcontext()
+    return s, torch.cuda.stream(s)
+
+
+def _workspace(nbytes: int, device):
+    import torch
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
 def orthogonalize(x, steps: int = 5, coefficients=COEFFICIENTS, eps: float = 1e-7, out=None, stream=None):
@@ -89,17 +96,19 @@ def orthogonalize(x, steps: int = 5, coefficients=COEFFICIENTS, eps: float = 1e-
     import torch
     batch, rows, cols, sr, sb = _batched(x, "x")
     kind = _type(x, "x")
-    if out is None:
-        out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-    _L.require(out.device == x.device and out.shape == x.shape and out.dtype == torch.bfloat16,
-               "out must be a bf16 tensor of x's shape and device")
-    _, _, _, osr, osb = _batched(out, "out")
     k = _coefficients(coefficients, steps)
     L = _L.lib()
     nbytes = L.ma_orthogonalize_workspace(batch, rows, cols)
-    s, ws = _stream_and_workspace(x.device, nbytes, stream)
-    _L.check(L.ma_orthogonalize(batch, rows, cols, x.data_ptr(), kind, sr, sb, out.data_ptr(), osr, osb, steps, k, eps,
-                                ws.data_ptr(), nbytes, s.cuda_stream))
+    s, place = _place(x.device, stream)
+    with place:
+        if out is None:
+            out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        _L.require(out.device == x.device and out.shape == x.shape and out.dtype == torch.bfloat16,
+                   "out must be a bf16 tensor of x's shape and device")
+        _, _, _, osr, osb = _batched(out, "out")
+        ws = _workspace(nbytes, x.device)
+        _L.check(L.ma_orthogonalize(batch, rows, cols, x.data_ptr(), kind, sr, sb, out.data_ptr(), osr, osb, steps, k, eps,
+                                    ws.data_ptr(), nbytes, s.cuda_stream))
     return out
 
 
@@ -129,9 +138,11 @@ def muon_step(params, grads, momentum, lr: float = 1e-3, beta: float = 0.95, wd:
     k = _coefficients(coefficients, steps)
     L = _L.lib()
     nbytes = L.ma_orthogonalize_workspace(batch, rows, cols)
-    s, ws = _stream_and_workspace(params.device, nbytes, stream)
-    _L.check(L.ma_muon_step(batch, rows, cols, *arrays, momentum.data_ptr(), *hyper, int(nesterov), steps, k, eps,
-                            ws.data_ptr(), nbytes, s.cuda_stream))
+    s, place = _place(params.device, stream)
+    with place:
+        ws = _workspace(nbytes, params.device)
+        _L.check(L.ma_muon_step(batch, rows, cols, *arrays, momentum.data_ptr(), *hyper, int(nesterov), steps, k, eps,
+                                ws.data_ptr(), nbytes, s.cuda_stream))
 
 
 def scales_shape(shape):
@@ -160,9 +171,11 @@ def muon8_step(params, grads, codes, scales, lr: float = 1e-3, beta: float = 0.9
     k = _coefficients(coefficients, steps)
     L = _L.lib()
     nbytes = L.ma_orthogonalize_workspace(batch, rows, cols)
-    s, ws = _stream_and_workspace(params.device, nbytes, stream)
-    _L.check(L.ma_muon8_step(batch, rows, cols, *arrays, codes.data_ptr(), scales.data_ptr(), *hyper, int(nesterov), steps,
-                             k, eps, ws.data_ptr(), nbytes, s.cuda_stream))
+    s, place = _place(params.device, stream)
+    with place:
+        ws = _workspace(nbytes, params.device)
+        _L.check(L.ma_muon8_step(batch, rows, cols, *arrays, codes.data_ptr(), scales.data_ptr(), *hyper, int(nesterov),
+                                 steps, k, eps, ws.data_ptr(), nbytes, s.cuda_stream))
 
 
 def momentum8_values(codes, scales, out=None, stream=None):
@@ -170,13 +183,13 @@ def momentum8_values(codes, scales, out=None, stream=None):
     import torch
     _L.require(codes.is_cuda and codes.dim() >= 1, "codes must be a CUDA tensor")
     _require_momentum8(codes, scales, codes.device)
-    if out is None:
-        out = torch.empty(codes.shape, dtype=torch.float32, device=codes.device)
-    _L.require(out.dtype == torch.float32 and out.shape == codes.shape and out.is_contiguous()
-               and out.device == codes.device, "out must be contiguous fp32 of codes' shape and device")
-    s = torch.cuda.current_stream(codes.device) if stream is None else stream
-    _L.require(s.device == codes.device, "the stream must be of the tensors' device")
-    cols = codes.shape[-1]
-    _L.check(_L.lib().ma_momentum8_values(codes.numel() // cols if cols else 0, cols, codes.data_ptr(),
-                                          scales.data_ptr(), out.data_ptr(), s.cuda_stream))
+    s, place = _place(codes.device, stream)
+    with place:
+        if out is None:
+            out = torch.empty(codes.shape, dtype=torch.float32, device=codes.device)
+        _L.require(out.dtype == torch.float32 and out.shape == codes.shape and out.is_contiguous()
+                   and out.device == codes.device, "out must be contiguous fp32 of codes' shape and device")
+        cols = codes.shape[-1]
+        _L.check(_L.lib().ma_momentum8_values(codes.numel() // cols if cols else 0, cols, codes.data_ptr(),
+                                              scales.data_ptr(), out.data_ptr(), s.cuda_stream))
     return out

@@ -280,6 +280,25 @@ def test_muon_on_another_stream():
     assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
+def test_muon_results_are_allocated_on_the_stream_that_writes_them():
+    """Memory that the current stream has given back may still be in use there:
+    a result written by another stream must not lie in it."""
+    x = _matrix((200, 300), 75, torch.bfloat16).cuda()
+    codes, scales = torch.ones(200, 300, dtype=torch.int8, device="cuda"), torch.ones(200, 2, device="cuda")
+    want = muon.orthogonalize(x), muon.momentum8_values(codes, scales)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call, ref in ((lambda: muon.orthogonalize(x, stream=side), want[0]),
+                      (lambda: muon.momentum8_values(codes, scales, stream=side), want[1])):
+        free = torch.empty_like(ref)
+        at = free.data_ptr()
+        del free
+        got = call()
+        assert got.data_ptr() != at
+        torch.cuda.synchronize()
+        assert torch.equal(got, ref)
+
+
 def test_muon_same_inputs_give_the_same_bits():
     u = _matrix((3, 390, 520), 81).cuda()
     first = muon.orthogonalize(u)

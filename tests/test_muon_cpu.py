@@ -112,6 +112,41 @@ def test_python_checks_need_no_device():
     assert muon.rms_scale(100, 400) == pytest.approx(4.0)
 
 
+@pytest.mark.parametrize("current_device,given,switched", [(0, None, False), (1, None, True), (0, 7, True), (1, 7, True)])
+def test_the_streams_device_is_current_during_a_call(monkeypatch, current_device, given, switched):
+    """The default stream of a device is the null stream there: the call has to be
+    made with that device current."""
+    class Stream:
+        def __init__(self, device, number):
+            self.device, self.number = device, number
+
+        def __eq__(self, other):
+            return (self.device, self.number) == (other.device, other.number)
+
+    device = torch.device("cuda", 0)
+    entered = []
+
+    class Context:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            entered.append(self.s)
+
+        def __exit__(self, *a):
+            entered.append(None)
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: Stream(device, 0))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current_device)
+    monkeypatch.setattr(torch.cuda, "stream", Context)
+    s, place = muon._place(device, None if given is None else Stream(device, given))
+    assert s == Stream(device, given or 0)
+    with place:
+        assert entered == ([s] if switched else [])
+    with pytest.raises(ValueError):
+        muon._place(device, Stream(torch.device("cuda", 1), 0))
+
+
 def test_reference_agrees_with_the_singular_values():
     """The reference's products against its meaning: the same scalar polynomial on
     every singular value, with the singular vectors kept."""
