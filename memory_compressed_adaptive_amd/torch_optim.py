@@ -120,13 +120,12 @@ class Muon(torch.optim.Optimizer):
     serves this and MicroAdamW).  lr, weight_decay, momentum, nesterov and scale
     may be changed between steps.  A parameter without a gradient is left alone,
     its momentum too.  Gradients are rounded to bfloat16, as MicroAdamW rounds
-    them.
+    them.  The parameters are moved into one buffer for each shape and type here:
+    a model is moved or converted before this, not after (step refuses then).
     """
 
     def __init__(self, params, lr=1e-3, momentum=0.95, weight_decay=0.0, nesterov=True, scale="rms", steps=5,
                  coefficients=_muon.COEFFICIENTS, eps=1e-7, momentum_bits=32):
-        if momentum_bits not in (8, 32):
-            raise ValueError("momentum_bits must be 32 or 8")
         defaults = dict(lr=lr, momentum=momentum, weight_decay=weight_decay, nesterov=nesterov, scale=scale, steps=steps,
                         coefficients=coefficients, eps=eps, momentum_bits=momentum_bits)
         super().__init__(params, defaults)
@@ -146,6 +145,10 @@ class Muon(torch.optim.Optimizer):
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        for st in (st for group in self.param_groups for st in group["_stacks"]):
+            if any(p.data_ptr() != at for p, at in zip(st["of"], st["at"])):
+                raise RuntimeError("a parameter was moved or converted after it was given to Muon, which keeps "
+                                   "equally shaped ones in one buffer: make the optimizer afterwards")
         for group in self.param_groups:
             for st in group["_stacks"]:
                 rows, cols = st["params"].shape[-2:]
@@ -198,6 +201,10 @@ class Muon(torch.optim.Optimizer):
 def _stacks(group):
     """The group's parameters in one buffer for each shape and type, in the order
     of the list, with their bf16 gradients and momentum beside them."""
+    if group["momentum_bits"] not in (8, 32):
+        raise ValueError("momentum_bits must be 32 or 8")
+    if len(set(map(id, group["params"]))) < len(group["params"]):
+        raise ValueError("a parameter appears twice in a group")
     by = {}
     for p in group["params"]:
         if p.dim() not in (2, 3):
@@ -215,7 +222,8 @@ def _stacks(group):
         for i, p in enumerate(ps):
             flat[i].copy_(p.detach())
             p.data = flat[i]
-        st = {"of": ps, "params": flat, "grads": torch.zeros(flat.shape, dtype=torch.bfloat16, device=flat.device)}
+        st = {"of": ps, "at": [p.data_ptr() for p in ps], "params": flat,
+              "grads": torch.zeros(flat.shape, dtype=torch.bfloat16, device=flat.device)}
         if group["momentum_bits"] == 8:
             st["codes"] = torch.zeros(flat.shape, dtype=torch.int8, device=flat.device)
             st["scales"] = torch.zeros(_muon.scales_shape(flat.shape), device=flat.device)

@@ -91,6 +91,18 @@ def test_load_refuses_another_momentum():
         Muon(_params(1)[:2]).load_state_dict(a.state_dict())
 
 
+def test_step_refuses_parameters_that_were_moved():
+    ps = _params(9)
+    opt = Muon(ps)
+    for p, g in zip(ps, _grads(9)):
+        p.grad = g
+    before = ps[0].detach().clone()
+    ps[1].data = ps[1].data.clone()
+    with pytest.raises(RuntimeError, match="moved"):
+        opt.step()
+    assert torch.equal(ps[0].detach(), before)
+
+
 def test_added_group_and_refusals():
     ps = _params(1)
     opt = Muon(ps[:2])
