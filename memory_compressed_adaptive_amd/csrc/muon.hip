@@ -76,7 +76,8 @@ int64_t count_tiles(int64_t m, int64_t n, int bm, int bn, bool symmetric) {
 // 240 us where 253 of 192 take 197).  Where parameters are read and written
 // (`out`), the end is bound by memory, and two workgroups to a CU hide it.
 // Parts of the summed index fill the card where there are few tiles; their sums
-// cost another launch and their way through memory.
+// cost another launch and their way through memory (five steps of 2048 x 8192:
+// 729 us without, 700 with).
 Choice pick(int64_t m, int64_t n, int64_t k, int64_t chunk, bool symmetric, bool out, bool may_split) {
   const struct { int kind, bm, bn, per_cu; double alone, full, ends, out; } kinds[] = {
       {256, 256, 256, 1, 1.76, 1.76, 5.0, 14.0},
@@ -108,7 +109,9 @@ Choice pick(int64_t m, int64_t n, int64_t k, int64_t chunk, bool symmetric, bool
 struct Plan {
   int64_t r, c, n, m;       // n <= m: the wide orientation's sides
   bool tall;
-  bool small;               // a workgroup for each matrix, no workspace
+  // a workgroup for each matrix, no workspace: wherever LDS holds it (144 of 64 x
+  // 768: 117 us as separate launches, 32 so; 64 x 64: 55 and 15)
+  bool small;
   bool pairs;               // two steps are taken together
   bool diagonal;            // what rounding takes off P's diagonal is added back
   int64_t np, mp;           // padded
@@ -134,25 +137,27 @@ struct Plan {
     runs = (uint32_t)run.groups * (uint32_t)run.segs;
     nparts = (int)std::min<int64_t>(kNormParts, (runs + 15) / 16);   // four runs to a wave
     const size_t one = 2 * 2 * (size_t)(np * mp) + 3 * 2 * (size_t)(np * np) + 4 * (size_t)np + 8 * (size_t)nparts;
+    small = fits_small(n, m, runs);
+    if (small) { bytes = 256; return; }
     chunk = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(batch, 65535), (int64_t)(kWorkspaceAim / one)));
     x_bytes = (size_t)round_up(2 * chunk * np * mp, 256);
     a_bytes = (size_t)round_up(2 * chunk * np * np, 256);
     part_bytes = (size_t)round_up(8 * chunk * nparts, 256);
-    small = fits_small(n, m, runs);
     gram = pick(np, np, mp, chunk, true, false, true);
     poly = pick(np, np, np, chunk, true, false, false);
     update = pick(mp, np, np, chunk, false, false, false);
     last = pick(mp, np, np, chunk, false, true, false);
-    // three products of the short side take the place of two with the long one;
-    // with few rows, what rounding does to the diagonals of P1 and T does not
-    // average out (37 x 3000: error 3.0e-3 against 1.4e-3)
+    // three products of the short side take the place of two with the long one
+    // (11008 x 4096: 3.19 ms for five steps one by one, 2.66 two together; 2048 x
+    // 8192: 726 and 627 us); with few rows, what rounding does to the diagonals
+    // of P1 and T does not average out (37 x 3000: error 3.0e-3 against 1.4e-3)
     pairs = n > 128 && 3 * m >= 4 * n && gram.time + update.time > 1.1 * 3.0 * poly.time;
     // where A stays near a multiple of I; it takes a tenth of P X's time (768 x
     // 768: error 1.25e-3 without, 0.85e-3 with)
     diagonal = m >= 2 * n;
     lost_bytes = (size_t)round_up(4 * chunk * np, 256);
     sum_bytes = (size_t)round_up((int64_t)gram.bytes, 256);
-    bytes = small ? 256 : 2 * x_bytes + 3 * a_bytes + part_bytes + lost_bytes + sum_bytes;
+    bytes = 2 * x_bytes + 3 * a_bytes + part_bytes + lost_bytes + sum_bytes;
   }
 };
 

@@ -540,8 +540,8 @@ struct MuonProduct {
 // block of 16-bit values among 16 lanes.  So X is kept in one orientation.
 //
 // Banks (64 of 4 bytes; a read serves 256 bytes a cycle).  Rows: 16-byte chunk
-// c of row r lies at c ^ (r / (rows in 256 bytes)), so that 16 lanes (rows) of
-// a b128 read take different banks (with c ^ (r & 7) at BK = 64 every read
+// c of row r lies at c ^ (r / 2 & 7), two rows being 256 bytes, so that 16 lanes
+// (rows) of a b128 read take different banks (with c ^ (r & 7) every read
 // counted four cycles of conflicts on top of its four).  Columns: 64-byte
 // chunk c of row k lies at c ^ k modulo the chunks in 256 bytes, so that the
 // four rows of a transposing read do.  The copies to LDS write their lanes one
@@ -556,7 +556,7 @@ struct Tile {
   static constexpr int LI = BM * BK / 512 / kWaves, RI = BN * BK / 512 / kWaves; // 1 KiB copies of a wave
   static constexpr int kStageBytes = (BM + BN) * BK * 2;
   static_assert(LI * 512 * kWaves == BM * BK && RI * 512 * kWaves == BN * BK, "copies divide evenly among the waves");
-  static_assert(BK == 32 || BK == 64 || BK == 128, "LDS orders are made for these");
+  static_assert(BK == 64, "LDS orders are made for it");
   static constexpr int kOutBytes = kWaves * 32 * (TM * 4 + 16);   // the epilogue's part of LDS
   static constexpr int kLds = S * kStageBytes > kOutBytes ? S * kStageBytes : kOutBytes;
   static_assert(kLds <= 160 * 1024, "LDS of a CU");
@@ -675,7 +675,7 @@ __device__ __forceinline__ void tile_of(const MuonProduct &A, int &lb, int &ti, 
 
 // Where 16-byte chunk g of a B-wide panel in LDS comes from: bytes from the
 // panel's start in memory, with rows of ld bytes.
-template <bool COLS, int B, int BK>
+template <bool COLS, int B>
 __device__ __forceinline__ uint32_t panel_source(int g, uint32_t ld) {
   if (COLS) {
     constexpr int kRow = B / 8;   // chunks in a row
@@ -684,14 +684,13 @@ __device__ __forceinline__ uint32_t panel_source(int g, uint32_t ld) {
     const int x = kIn == 4 ? row & 3 : row >> 1 & 1;
     return (uint32_t)row * ld + (uint32_t)(p ^ (x << 2)) * 16;
   }
-  constexpr int kRow = BK / 8, kRows256 = 16 / kRow;
-  const int row = g / kRow, p = g % kRow;
-  return (uint32_t)row * ld + (uint32_t)(p ^ (row / kRows256 & (kRow - 1))) * 16;
+  const int row = g / 8, p = g % 8;
+  return (uint32_t)row * ld + (uint32_t)(p ^ (row / 2 & 7)) * 16;
 }
 
 // A lane's 8 values for the product at 16 * ks: index `at` + (lane & 31) of the
 // panel, summed index 16 * ks + 8 * (lane / 32) + 0..7.
-template <bool COLS, int B, int BK>
+template <bool COLS, int B>
 __device__ __forceinline__ half8 panel_read(const char *panel, int at, int ks, int lane) {
   if (COLS) {
     // lanes 16q..16q+15 transpose 4 rows of 16 columns: lane s of them points
@@ -709,9 +708,8 @@ __device__ __forceinline__ half8 panel_read(const char *panel, int at, int ks, i
     }
     return u.h;
   }
-  constexpr int kRow = BK / 8, kRows256 = 16 / kRow;
   const int row = at + (lane & 31);
-  return *(const half8 *)(panel + row * (BK * 2) + (((2 * ks + (lane >> 5)) ^ (row / kRows256 & (kRow - 1))) * 16));
+  return *(const half8 *)(panel + row * 128 + (((2 * ks + (lane >> 5)) ^ (row / 2 & 7)) * 16));
 }
 
 template <class T, int ROLE>
@@ -740,9 +738,9 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
   const int64_t sl = LC ? T::BK * l_ld : T::BK * 2, sr = RC ? T::BK * r_ld : T::BK * 2;   // to the next step
   uint32_t vl[T::LI], vr[T::RI];
 #pragma unroll
-  for (int i = 0; i < T::LI; ++i) vl[i] = panel_source<LC, T::BM, T::BK>((wave + i * T::kWaves) * 64 + lane, (uint32_t)l_ld);
+  for (int i = 0; i < T::LI; ++i) vl[i] = panel_source<LC, T::BM>((wave + i * T::kWaves) * 64 + lane, (uint32_t)l_ld);
 #pragma unroll
-  for (int i = 0; i < T::RI; ++i) vr[i] = panel_source<RC, T::BN, T::BK>((wave + i * T::kWaves) * 64 + lane, (uint32_t)r_ld);
+  for (int i = 0; i < T::RI; ++i) vr[i] = panel_source<RC, T::BN>((wave + i * T::kWaves) * 64 + lane, (uint32_t)r_ld);
   const uint32_t lds0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char *)smem + wave * 1024;
 
   // copy i of step t into stage `to`
@@ -768,10 +766,10 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
 #pragma unroll
     for (int g = 0; g < G; ++g) {
 #pragma unroll
-      for (int i = 0; i < T::FM; ++i) fx[g * T::FM + i] = panel_read<LC, T::BM, T::BK>(p, wm + 32 * i, group * G + g, lane);
+      for (int i = 0; i < T::FM; ++i) fx[g * T::FM + i] = panel_read<LC, T::BM>(p, wm + 32 * i, group * G + g, lane);
 #pragma unroll
       for (int j = 0; j < T::FN; ++j)
-        fy[g * T::FN + j] = panel_read<RC, T::BN, T::BK>(p + T::BM * T::BK * 2, wn + 32 * j, group * G + g, lane);
+        fy[g * T::FN + j] = panel_read<RC, T::BN>(p + T::BM * T::BK * 2, wn + 32 * j, group * G + g, lane);
     }
   };
   constexpr int kReads = G * (T::FM * (LC ? 2 : 1) + T::FN * (RC ? 2 : 1)), kProducts = G * T::FM * T::FN;
@@ -781,8 +779,9 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
   };
 
   // A's part of the tile (kPoly) or the old X's (kUpdate), whole rows at a time
-  // and 32 rows ahead, the first of them before the main loop (read four elements at a time by the lanes that need
-  // them, A took 20 000 cycles of a 192 x 192 tile's 150 000)
+  // and 32 rows ahead, the first of them before the main loop (read four elements
+  // at a time by the lanes that need them, A took 20 000 cycles of a 192 x 192
+  // tile's 150 000)
   constexpr bool kBeside = ROLE == kPoly || ROLE == kUpdate;
   constexpr int kRowChunks = T::TM / 8, kTrips = kBeside ? 32 * kRowChunks / 64 : 1;
   half8 beside[2][kTrips];
