@@ -761,16 +761,16 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
 
   constexpr int G = T::G;
   half8 x[2][T::FM * G], y[2][T::FN * G];
-  auto fragments = [&](int stage, int group, half8 *fx, half8 *fy) {
+  constexpr int kFragments = G * (T::FM + T::FN);
+  auto fragment = [&](int at, int stage, int group, half8 *fx, half8 *fy) {
     const char *p = smem + stage * T::kStageBytes;
+    const int g = at / (T::FM + T::FN), i = at % (T::FM + T::FN), j = i - T::FM;
+    if (j < 0) fx[g * T::FM + i] = panel_read<LC, T::BM>(p, wm + 32 * i, group * G + g, lane);
+    else fy[g * T::FN + j] = panel_read<RC, T::BN>(p + T::BM * T::BK * 2, wn + 32 * j, group * G + g, lane);
+  };
+  auto fragments = [&](int stage, int group, half8 *fx, half8 *fy) {
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-#pragma unroll
-      for (int i = 0; i < T::FM; ++i) fx[g * T::FM + i] = panel_read<LC, T::BM>(p, wm + 32 * i, group * G + g, lane);
-#pragma unroll
-      for (int j = 0; j < T::FN; ++j)
-        fy[g * T::FN + j] = panel_read<RC, T::BN>(p + T::BM * T::BK * 2, wn + 32 * j, group * G + g, lane);
-    }
+    for (int at = 0; at < kFragments; ++at) fragment(at, stage, group, fx, fy);
   };
   constexpr int kReads = G * (T::FM * (LC ? 2 : 1) + T::FN * (RC ? 2 : 1)), kProducts = G * T::FM * T::FN;
   auto product = [&](int at, const half8 *fx, const half8 *fy) {
@@ -842,14 +842,16 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
         }
         // the next stage is whole, and nobody reads this one any more
         stage_wait<(T::S - 2) * kCopies>();
-        fragments(next, 0, x[0], y[0]);
         next_copy();
-        __builtin_amdgcn_sched_barrier(0);
-        constexpr int kEach = (kCopies + kProducts - 1) / kProducts;
+        // the next fragments' reads and the copies that refill this stage are
+        // spread over the products
+        constexpr int kEach = (kCopies + kProducts - 1) / kProducts, kEachRead = (kFragments + kProducts - 1) / kProducts;
 #pragma unroll
         for (int q = 0; q < kProducts; ++q) {
+          __builtin_amdgcn_sched_barrier(0);
           product(q, x[1], y[1]);
-          // the copies that refill this stage are spread over the products
+#pragma unroll
+          for (int c = q * kEachRead; c < (q + 1) * kEachRead && c < kFragments; ++c) fragment(c, next, 0, x[0], y[0]);
 #pragma unroll
           for (int c = q * kEach; c < (q + 1) * kEach && c < kCopies; ++c) copy(c, bl, br, stage);
         }
