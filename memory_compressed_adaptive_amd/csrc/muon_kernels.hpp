@@ -531,7 +531,8 @@ struct MuonProduct {
 // way.  A wave holds the fragments for the next 16 in registers, so that LDS
 // reads run under the matrix instructions; the only barrier of a step stands
 // before its last 16, when all fragments of the stage are in registers, and
-// the copies that refill the stage are issued between that last 16's products.
+// the copies that refill the stage are issued between that last 16's products
+// and the next step's first.
 //
 // Panels come in two kinds.  Rows: the summed index is contiguous in memory; a
 // panel is B rows of BK, and a lane's 8 values are one b128 read.  Columns:
@@ -772,7 +773,7 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
 #pragma unroll
     for (int at = 0; at < kFragments; ++at) fragment(at, stage, group, fx, fy);
   };
-  constexpr int kReads = G * (T::FM * (LC ? 2 : 1) + T::FN * (RC ? 2 : 1)), kProducts = G * T::FM * T::FN;
+  constexpr int kProducts = G * T::FM * T::FN;
   auto product = [&](int at, const half8 *fx, const half8 *fy) {
     const int g = at / (T::FM * T::FN), j = at / T::FM % T::FN, i = at % T::FM;
     acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fx[g * T::FM + i], fy[g * T::FN + j], acc[i][j], 0, 0, 0);
@@ -811,51 +812,48 @@ __global__ __launch_bounds__(T::kThreads) void muon_product_kernel(MuonProduct A
     al += (uint64_t)sl, el -= (uint64_t)sl;
     ar += (uint64_t)sr, er -= (uint64_t)sr;
   };
+  // The copies that refill a stage are issued in the last group of its step and
+  // the first of the next.  All in one group, 64 KiB for a 256 x 256 tile in a
+  // quarter of a step, was twice what a CU takes in (2048 x 8192: 597 us against
+  // 572); over three groups the last of them come late (2% slower).
+  constexpr int kShare = (kCopies + 1) / 2;
   if (ROLE != kGramSum) {
 #pragma unroll
     for (int t = 0; t < T::S; ++t) {
       next_copy();
 #pragma unroll
-      for (int i = 0; i < kCopies; ++i) copy(i, bl, br, t);
+      for (int i = 0; i < (t + 1 < T::S ? kCopies : kShare); ++i) copy(i, bl, br, t);
     }
-    stage_wait<(T::S - 1) * kCopies>();
+    stage_wait<(T::S - 2) * kCopies + kShare>();
     fragments(0, 0, x[0], y[0]);
-    int stage = 0;
+    int stage = 0, before = T::S - 1;
     for (int t = 0; t < nk; ++t) {
       const int next = stage + 1 == T::S ? 0 : stage + 1;
 #pragma unroll
       for (int g = 0; g < T::kGroups; ++g) {
-        __builtin_amdgcn_sched_barrier(0);
-        if (g + 1 < T::kGroups) {
-          fragments(stage, g + 1, x[(g + 1) & 1], y[(g + 1) & 1]);
-#pragma unroll
-          for (int q = 0; q < kProducts; ++q) product(q, x[g & 1], y[g & 1]);
-          // products and reads in turn; left alone, the compiler moves the reads
-          // behind the products
-          constexpr int kEach = (kReads + kProducts - 1) / kProducts;
-#pragma unroll
-          for (int q = 0; q < kReads; q += kEach) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, kEach, 0);
-          }
-          continue;
+        const bool last = g + 1 == T::kGroups;
+        if (last) {
+          // the next stage is whole, and nobody reads this one any more
+          __builtin_amdgcn_sched_barrier(0);
+          stage_wait<(T::S - 2) * kCopies>();
+          next_copy();
         }
-        // the next stage is whole, and nobody reads this one any more
-        stage_wait<(T::S - 2) * kCopies>();
-        next_copy();
-        // the next fragments' reads and the copies that refill this stage are
-        // spread over the products
-        constexpr int kEach = (kCopies + kProducts - 1) / kProducts, kEachRead = (kFragments + kProducts - 1) / kProducts;
+        // the next fragments' reads and the copies are spread over the products
+        const int from = last ? 0 : kShare, to = last ? kShare : g == 0 ? kCopies : kShare;
+        constexpr int kEach = (kShare + kProducts - 1) / kProducts, kEachRead = (kFragments + kProducts - 1) / kProducts;
 #pragma unroll
         for (int q = 0; q < kProducts; ++q) {
           __builtin_amdgcn_sched_barrier(0);
-          product(q, x[1], y[1]);
+          product(q, x[g & 1], y[g & 1]);
 #pragma unroll
-          for (int c = q * kEachRead; c < (q + 1) * kEachRead && c < kFragments; ++c) fragment(c, next, 0, x[0], y[0]);
+          for (int c = q * kEachRead; c < (q + 1) * kEachRead && c < kFragments; ++c)
+            fragment(c, last ? next : stage, last ? 0 : g + 1, x[(g + 1) & 1], y[(g + 1) & 1]);
 #pragma unroll
-          for (int c = q * kEach; c < (q + 1) * kEach && c < kCopies; ++c) copy(c, bl, br, stage);
+          for (int c = from + q * kEach; c < from + (q + 1) * kEach; ++c)
+            if (c < to) copy(c, bl, br, last ? stage : before);
         }
       }
+      before = stage;
       stage = next;
     }
   }
