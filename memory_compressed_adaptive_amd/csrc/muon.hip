@@ -47,7 +47,7 @@ bool fits_small(int64_t n, int64_t m, uint32_t runs) {
 using Tile64 = Tile<64, 64, 2, 2, 64, 4, 2>;
 using Tile128 = Tile<128, 128, 2, 2, 64, 2>;
 using Tile128Deep = Tile<128, 128, 4, 2, 64, 4>;   // alone on a CU
-using Tile192 = Tile<192, 192, 2, 2, 64, 2>;
+using Tile192 = Tile<192, 192, 2, 2, 64, 3>;
 using Tile256x192 = Tile<256, 192, 4, 2, 64, 2>;
 using Tile256 = Tile<256, 256, 4, 2, 64, 2>;
 
