@@ -17,7 +17,9 @@ namespace {
 constexpr int64_t kMaxElems = int64_t(1) << 33;     // of one matrix: keeps every launch's grid in range
 constexpr int64_t kMaxSide = int64_t(1) << 21;      // 256 rows' bytes stay under 2^31
 constexpr int kNormParts = 2048;                    // most partial sums of squares for one matrix
-constexpr size_t kWorkspaceAim = size_t(512) << 20; // a batch is cut into runs of matrices of about this much workspace
+// A batch is cut into runs of matrices of at most this much workspace (with 256
+// MiB 48 of 768 x 768 take 820 us instead of 770; 1 GiB is no better).
+constexpr size_t kWorkspaceAim = size_t(512) << 20;
 
 struct Coefficients { float v[kMaxSteps][3]; };
 
@@ -140,6 +142,8 @@ struct Plan {
     small = fits_small(n, m, runs);
     if (small) { bytes = 256; return; }
     chunk = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(batch, 65535), (int64_t)(kWorkspaceAim / one)));
+    const int64_t calls = (batch + chunk - 1) / chunk;
+    chunk = (batch + calls - 1) / calls;   // runs of one length (4 of 4096 x 4096 as 2 + 2: 5.46 ms, as 3 + 1: 5.54)
     x_bytes = (size_t)round_up(2 * chunk * np * mp, 256);
     a_bytes = (size_t)round_up(2 * chunk * np * np, 256);
     part_bytes = (size_t)round_up(8 * chunk * nparts, 256);
