@@ -75,11 +75,11 @@ int64_t count_tiles(int64_t m, int64_t n, int bm, int bn, bool symmetric) {
 // on ones that do not; "alone": at most one workgroup on a CU).  Large tiles
 // read less for each product; smaller ones waste less of the last round and of
 // the half that a symmetric result leaves out (n = 4096: 136 tiles of 256 or 253
-// of 192; 11008 x 4096 takes 2.64 ms without the 192 tile, 2.58 with it).  Where parameters are read and written
-// (`out`), the end is bound by memory, and two workgroups to a CU hide it.
-// Parts of the summed index fill the card where there are few tiles; their sums
-// cost another launch and their way through memory (five steps of 2048 x 8192:
-// 729 us without, 700 with).
+// of 192; 11008 x 4096 takes 2.64 ms without the 192 tile, 2.58 with it).
+// Where parameters are read and written (`out`), the end is bound by memory, and
+// two workgroups to a CU hide it.  Parts of the summed index fill the card where
+// there are few tiles; their sums cost another launch and their way through
+// memory (five steps of 2048 x 8192: 729 us without, 700 with).
 Choice pick(int64_t m, int64_t n, int64_t k, int64_t chunk, bool symmetric, bool out, bool may_split) {
   const struct { int kind, bm, bn, per_cu; double alone, full, ends, out; } kinds[] = {
       {256, 256, 256, 1, 1.76, 1.76, 5.0, 14.0},
