@@ -92,7 +92,7 @@ def orthogonalize(x, steps: int = 5, coefficients=COEFFICIENTS, eps: float = 1e-
     """x [..., rows, cols] (fp32 or bf16) orthogonalized, as bf16: X = x /
     max(|x|_F, eps), then `steps` times X <- (a I + b A + c A A) X with A = X X^T
     on the shorter side.  out: a bf16 tensor of x's shape (x itself if it is
-    bf16); by default a new one."""
+    bf16); by default a new one.  The result carries no gradient."""
     import torch
     batch, rows, cols, sr, sb = _batched(x, "x")
     kind = _type(x, "x")

@@ -267,6 +267,24 @@ def test_muon_captured_graphs_replay_as_eager_steps():
         assert torch.equal(p[1], q[1]) and torch.equal(codes, codes2) and torch.equal(scales, scales2)
 
 
+@pytest.mark.parametrize("shape", [(3, 40, 200), (2, 700, 390), (1, 200, 5000)])
+def test_orthogonalize_captured_and_replayed(shape):
+    """One workgroup to a matrix; launches of a tall batch; pairs of steps with
+    the long sums in parts."""
+    x = _matrix(shape, 53, torch.bfloat16).cuda()
+    out = torch.zeros_like(x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        muon.orthogonalize(x, out=out)
+    for t in range(4):
+        x.copy_(_matrix(shape, 54 + t, torch.bfloat16))
+        want = muon.orthogonalize(x)
+        graph.replay()
+        other = muon.orthogonalize(x.float())     # eager work beside the replay
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(other, want)
+
+
 def test_muon_on_another_stream():
     x = [_matrix((200, 300), 71 + k, torch.bfloat16).cuda() for k in range(4)]
     want = [muon.orthogonalize(t) for t in x]
@@ -304,6 +322,51 @@ def test_muon_same_inputs_give_the_same_bits():
     first = muon.orthogonalize(u)
     for _ in range(3):
         assert torch.equal(muon.orthogonalize(u), first)
+
+
+def test_muon_offsets_past_32_bits():
+    """The longest side with more than 2^31 elements.  The formula is taken on the
+    short side in 64 bits, X = U F(U^T U), and compared on rows at both ends and
+    in between.  Tolerance: five steps of three roundings of 2^-11, each grown at
+    most fivefold (s f'(s) / f(s) of a step's f on 0..1.2), and the result's 2^-8;
+    an offset that lost its upper bits would be off by the whole value."""
+    rows, cols = 1 << 21, 1040
+    gen = torch.Generator(device="cuda").manual_seed(91)
+    u = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    a = torch.zeros(cols, cols, dtype=torch.float64, device="cuda")
+    for part in u.split(1 << 17):
+        part.normal_(generator=gen)
+        wide = part.double()
+        a += wide.T.contiguous() @ wide
+    say("[muon] 2^21 x 1040: inputs made")
+    got = muon.orthogonalize(u)
+    norm = a.trace().sqrt()
+    a = (a / norm ** 2).cpu()
+    f = torch.eye(cols, dtype=torch.float64)
+    for _ in range(5):
+        ka, kb, kc = muon.COEFFICIENTS
+        p = ka * torch.eye(cols, dtype=torch.float64) + kb * a + kc * a @ a
+        f, a = p @ f, p @ a @ p
+    f /= norm.cpu()
+    tol = 15 * 5 * 2.0 ** -11 + R.BF16
+    for at in (0, 1 << 20, (1 << 31) // cols, rows - 64):
+        want = u[at:at + 64].cpu().double() @ f
+        off = (got[at:at + 64].cpu().double() - want).norm() / want.norm()
+        say(f"[muon] rows {at}..: off {off:.2e}, allowed {tol:.2e}")
+        assert off <= tol
+    # a step from nothing, with the whole gradient as its momentum, gives the same
+    params = torch.zeros_like(u)
+    codes = torch.zeros(rows, cols, dtype=torch.int8, device="cuda")
+    scales = torch.zeros(muon.scales_shape(codes.shape), device="cuda")
+    muon.muon8_step(params, u, codes, scales, lr=1.0, beta=0.0, nesterov=False, scale=-1.0)
+    for x, y in zip(params.split(1 << 17), got.split(1 << 17)):
+        assert torch.equal(x, y)
+    for at in (0, (1 << 31) // cols, rows - 8):
+        qc, qs = R.quantized(u[at:at + 8].cpu().double())
+        assert torch.equal(codes[at:at + 8].cpu(), qc) and torch.equal(scales[at:at + 8].cpu(), qs)
+    values = muon.momentum8_values(codes, scales)
+    want = codes[-8:].float() * scales[-8:].repeat_interleave(256, 1)[:, :cols]
+    assert torch.equal(values[-8:], want)
 
 
 def test_muon_refusals_on_the_gpu():
