@@ -72,6 +72,17 @@ def test_orthogonalize_batch(rows, cols, batch):
     assert torch.equal(one, got[batch - 1])
 
 
+def test_orthogonalize_more_matrices_than_one_launch_takes():
+    """2^21 of them go into one launch."""
+    batch = (1 << 21) + 3
+    u = _matrix((1, 2, 3), 6, torch.bfloat16).cuda().repeat(batch, 1, 1)
+    u[-1] *= -1
+    got = muon.orthogonalize(u)
+    want = muon.orthogonalize(u[0])
+    _check_orthogonal("2x3", want, u[0])
+    assert bool((got[:-1] == want).all()) and torch.equal(got[-1], -want)
+
+
 def test_orthogonalize_leading_dimensions_and_zero_sizes():
     u = _matrix((2, 3, 20, 50), 5)
     got = muon.orthogonalize(u.cuda())
