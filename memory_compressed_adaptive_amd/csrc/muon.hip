@@ -180,15 +180,13 @@ bool coefficients_ok(const float *k, int steps, const char **why) {
     if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) { *why = "not finite"; return false; }
     double xs[5] = {0.0, hi * hi, 0.0, 0.0, 0.0};
     int nx = 2;
-    if (c != 0.0) {
-      xs[nx++] = -b / (2 * c);                       // of a + b x + c x^2
-      const double disc = 9 * b * b - 20 * a * c;    // of s (a + b s^2 + c s^4): a + 3 b x + 5 c x^2 = 0
-      if (disc >= 0) {
-        xs[nx++] = (-3 * b + std::sqrt(disc)) / (10 * c);
-        xs[nx++] = (-3 * b - std::sqrt(disc)) / (10 * c);
-      }
-    } else if (b != 0.0) {
-      xs[nx++] = -a / (3 * b);
+    if (c != 0.0) xs[nx++] = -b / (2 * c);           // of a + b x + c x^2
+    const double disc = 9 * b * b - 20 * a * c;      // of s (a + b s^2 + c s^4): a + 3 b x + 5 c x^2 = 0
+    if (disc >= 0) {
+      // both roots from the sum that cannot cancel, so that none is lost where c is tiny beside b
+      const double q = -0.5 * (3 * b + std::copysign(std::sqrt(disc), b));
+      if (c != 0.0) xs[nx++] = q / (5 * c);
+      if (q != 0.0) xs[nx++] = a / q;
     }
     double top = 0.0;
     for (int q = 0; q < nx; ++q) {

@@ -55,6 +55,13 @@ def test_coefficients_are_checked_through_every_step():
     assert _orth(rows=0, k=_k((5.4, -5.4, 0.0))) == L.MA_EINVAL
 
 
+@pytest.mark.parametrize("a,b,ok", [(6.0, -5.0, False), (14.0, -13.0, False), (2.8, -2.8, True), (-6.0, 5.0, False)])
+@pytest.mark.parametrize("c", [0.0, 1e-12, 1e-16, -1e-16, 1e-18, -1e-18, 1e-20, -1e-20, 1e-30, -1e-30])
+def test_a_tiny_last_coefficient_hides_no_extreme(a, b, ok, c):
+    """s (6 - 5 s^2 + c s^4) reaches 2.53 at s = 0.632, however small c is."""
+    assert _orth(rows=0, k=_k((a, b, c))) == (L.MA_OK if ok else L.MA_EINVAL)
+
+
 @pytest.mark.parametrize("kw", [dict(batch=0), dict(rows=0), dict(cols=0)])
 def test_empty_batches_do_nothing(kw):
     assert _orth(x=None, out=None, ws=None, ws_bytes=0, **kw) == L.MA_OK
