@@ -176,7 +176,10 @@ int ma_adamw8_step(int64_t n, int64_t t, float beta1, float beta2, float eps, fl
  * the matrices of a model, beside MicroAdam for the rest of it.  All take a
  * batch of `batch` equally shaped rows x cols matrices; element (b, i, j) of an
  * array with strides (row, bat) is at b*bat + i*row + j, strides in elements.
- * The momentum arrays are contiguous.
+ * In an array that is written the matrices lie one after the other (bat >=
+ * (rows-1)*row + cols, row >= cols) or their rows side by side, as the column
+ * blocks of one matrix do (row >= (batch-1)*bat + cols, bat >= cols); one that
+ * is only read may have any strides >= 0.  The momentum arrays are contiguous.
  *
  * Orthogonalizing U (n = the shorter side, X its orientation of n rows):
  *   X <- U / max(|U|_F, eps);  `steps` times, with its own (a, b, c) each:
@@ -199,8 +202,8 @@ int ma_adamw8_step(int64_t n, int64_t t, float beta1, float beta2, float eps, fl
  * every launch goes to `stream`, and a call can be captured into a HIP graph.
  * A matrix has at most 2^33 elements and sides of 2^21 (MA_EUNSUPPORTED).  steps: 1..64.
  * batch = 0, rows = 0 or cols = 0: MA_OK, nothing done.  MA_EINVAL: null or
- * misaligned pointers (each array to its elements), negative sizes, a small
- * workspace, strides of a written array that overlap.
+ * misaligned pointers (each array to its elements), negative sizes or strides, a
+ * small workspace, other strides of a written array.
  */
 #define MA_TYPE_F32 0
 #define MA_TYPE_BF16 1

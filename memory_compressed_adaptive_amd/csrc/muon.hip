@@ -388,13 +388,17 @@ int check(const char *who, int64_t batch, int64_t rows, int64_t cols, int steps,
 }
 
 // Strides count up; what is written must not overlap (what is read may: a
-// stride of 0 reads one matrix or one row again).
+// stride of 0 reads one matrix or one row again).  Either the matrices lie one
+// after the other, or their rows side by side (column blocks of one matrix).
 bool strides_ok(int64_t batch, int64_t rows, int64_t cols, int64_t row, int64_t bat, bool written) {
   if (row < 0 || bat < 0) return false;
   if (!written) return true;
   if (rows > 1 && row < cols) return false;
-  return batch <= 1 || (__int128)bat >= (__int128)(rows - 1) * row + cols;
+  if (batch <= 1 || (__int128)bat >= (__int128)(rows - 1) * row + cols) return true;
+  return bat >= cols && (__int128)row >= (__int128)(batch - 1) * bat + cols;
 }
+
+constexpr const char *kStrides = "negative strides, or a written array's rows or matrices overlap";
 
 int aligned_runs(const void *p, int elem, int64_t row, int64_t bat, int64_t rows, int64_t batch) {
   return ((uintptr_t)p & (uintptr_t)(4 * elem - 1)) == 0 && (rows == 1 || row % 4 == 0) && (batch == 1 || bat % 4 == 0);
@@ -445,7 +449,7 @@ int check_step(const char *who, int64_t batch, int64_t rows, int64_t cols, const
   if (!std::isfinite(lr) || !std::isfinite(scale) || !(wd >= 0.0) || !std::isfinite(wd))
     return fail(MA_EINVAL, "%s: lr, scale and wd must be finite, wd >= 0", who);
   if (!strides_ok(batch, rows, cols, p_row, p_batch, true) || !strides_ok(batch, rows, cols, g_row, g_batch, false))
-    return fail(MA_EINVAL, "%s: strides", who);
+    return fail(MA_EINVAL, "%s: %s", who, kStrides);
   return MA_OK;
 }
 
@@ -471,7 +475,7 @@ int ma_orthogonalize(int64_t batch, int64_t rows, int64_t cols, const void *x, i
   if (!x || !out) return fail(MA_EINVAL, "%s: null pointer", who);
   if (((uintptr_t)x & (uintptr_t)(elem - 1)) || ((uintptr_t)out & 1u)) return fail(MA_EINVAL, "%s: misaligned pointer", who);
   if (!strides_ok(batch, rows, cols, x_row, x_batch, false) || !strides_ok(batch, rows, cols, out_row, out_batch, true))
-    return fail(MA_EINVAL, "%s: strides", who);
+    return fail(MA_EINVAL, "%s: %s", who, kStrides);
   MuonInput in = {};
   in.x = x, in.x_bf16 = x_type == MA_TYPE_BF16, in.x_row = x_row, in.x_batch = x_batch;
   in.r = rows, in.c = cols;

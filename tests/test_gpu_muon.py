@@ -111,6 +111,29 @@ def test_orthogonalize_strided_input_and_output():
     assert torch.equal(y, muon.orthogonalize(x.contiguous()))
 
 
+@pytest.mark.parametrize("rows,heads,cols", [(96, 5, 20), (300, 3, 130), (700, 2, 72)])
+def test_heads_that_are_column_blocks_of_one_matrix(rows, heads, cols):
+    """Results and parameters written where the matrices' rows lie side by side."""
+    whole = _matrix((rows, heads * cols + 8), 17, torch.bfloat16).cuda()
+    x = whole[:, 4:4 + heads * cols].view(rows, heads, cols).transpose(0, 1)
+    hold = torch.full_like(whole, 7.0)
+    out = hold[:, 4:4 + heads * cols].view(rows, heads, cols).transpose(0, 1)
+    muon.orthogonalize(x, out=out)
+    assert torch.equal(out, muon.orthogonalize(x.contiguous()))
+    assert bool((hold[:, :4] == 7.0).all()) and bool((hold[:, 4 + heads * cols:] == 7.0).all())
+    m = torch.zeros(x.shape, device="cuda")
+    p, m2 = out.contiguous(), torch.zeros_like(m)
+    muon.muon_step(out, x, m, lr=0.1, wd=0.1)
+    muon.muon_step(p, x.contiguous(), m2, lr=0.1, wd=0.1)
+    assert torch.equal(out, p) and torch.equal(m, m2)
+    assert bool((hold[:, :4] == 7.0).all()) and bool((hold[:, 4 + heads * cols:] == 7.0).all())
+    codes, scales = torch.zeros_like(m, dtype=torch.int8), torch.zeros(muon.scales_shape(m.shape), device="cuda")
+    codes2, scales2 = codes.clone(), scales.clone()
+    muon.muon8_step(out, x, codes, scales, lr=0.1, wd=0.1)
+    muon.muon8_step(p, x.contiguous(), codes2, scales2, lr=0.1, wd=0.1)
+    assert torch.equal(out, p) and torch.equal(codes, codes2) and torch.equal(scales, scales2)
+
+
 @pytest.mark.parametrize("size", [1e-30, 1e-19, 1e19, 3e36])
 def test_orthogonalize_any_magnitude(size):
     u = _matrix((70, 90), 11) * size * 1e3

@@ -201,3 +201,16 @@ def test_reference_bound_holds_for_roundings_made_on_the_cpu():
                 x = half(x, 2.0 ** 14)
             off = (x - want).norm().item()
             assert (off > err) if mistake else (off <= err)
+
+
+@pytest.mark.parametrize("rows,cols,row,bat,batch,ok", [
+    (768, 64, 768, 64, 12, True), (768, 64, 767, 64, 12, False),       # heads as column blocks of one matrix
+    (5, 4, 13, 4, 3, True), (5, 4, 12, 4, 3, True), (5, 4, 11, 4, 3, False), (5, 4, 12, 3, 3, False),
+    (5, 4, 100, 7, 3, True), (1, 4, 0, 4, 3, True), (5, 4, 4, 20, 3, True), (5, 4, 4, 19, 3, False), (5, 4, 4, 0, 1, True),
+    (2, 1 << 20, 1 << 62, 1 << 40, 1 << 30, False)])
+def test_written_matrices_may_interleave_but_not_overlap(rows, cols, row, bat, batch, ok):
+    """Whole matrices one after the other, or the rows of all matrices side by
+    side.  Every call is refused in the end, for its null momentum."""
+    assert _step(L.lib().ma_muon_step, (None,), batch=batch, rows=rows, cols=cols, ps=(row, bat), gs=(0, 0), ws_bytes=1 << 60) == L.MA_EINVAL
+    assert ("momentum" in L.last_error()[1]) == ok, L.last_error()[1]
+    assert ok or "overlap" in L.last_error()[1]
