@@ -216,9 +216,9 @@ __device__ __forceinline__ void muon_store_momentum(const MuonInput &I, const Mu
   double quot = top * (1.0 / 127.0);
   quot = fma(fma(-127.0, quot, top), 1.0 / 127.0, quot);
   const float step = bad ? __builtin_nanf("") : (float)quot;
+  const double d = (double)step;
   double inv = 0.0;
   if (step > 0.f) {
-    const double d = (double)step;
     inv = __builtin_amdgcn_rcp(d);
     inv = fma(fma(-d, inv, 1.0), inv, inv);
     inv = fma(fma(-d, inv, 1.0), inv, inv);
@@ -226,7 +226,11 @@ __device__ __forceinline__ void muon_store_momentum(const MuonInput &I, const Mu
   uint32_t w = 0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    const double q8 = bad ? 0.0 : fmin(fmax(rint(m64[e] * inv), -127.0), 127.0);
+    // m / step, corrected once: the product alone falls beside a half that the
+    // quotient is exactly (73.5 / 49), and rounds to the odd code then
+    double q = m64[e] * inv;
+    q = fma(fma(-q, d, m64[e]), inv, q);
+    const double q8 = bad ? 0.0 : fmin(fmax(rint(q), -127.0), 127.0);
     w |= ((uint32_t)(int32_t)q8 & 0xffu) << (8 * e);
   }
   if (run) {

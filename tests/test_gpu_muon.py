@@ -252,6 +252,40 @@ def test_muon8_non_finite_block_and_short_block():
     assert torch.equal(v[fine], (codes.cpu().float() * qs.repeat_interleave(256, 1)[:, :cols])[fine])
 
 
+@pytest.mark.parametrize("cols", [256, 2560])
+def test_muon8_a_value_between_two_codes_takes_the_even_one(cols):
+    """With beta = 1/2 a block of scale 2 d keeps its largest code, 127, and has
+    the scale d afterwards; m = (k + 1/2) d is exactly between two codes.  The
+    sum, the scale and the quotient are exact, so the codes must be equal.  (For
+    d = 49, k = 1 the product with 1/d in 64 bits falls short of 3/2.)"""
+    scale = [49, 161, 97, 113, 1.75, 161 * 2.0 ** -12, 125, 0.921875]
+    codes, want, g = (torch.zeros(len(scale), cols, dtype=t) for t in (torch.int8, torch.int8, torch.bfloat16))
+    for r, d in enumerate(scale):
+        codes[r, ::256], want[r, ::256] = 127, 127
+        at = 1
+        for k in range(-127, 127):
+            # m = code d + g / 2
+            for code in range(-127, 128):
+                e = (2 * k + 1 - 2 * code) * d
+                if code != 0 and abs(e) <= 128 * d and float(torch.tensor(e).bfloat16()) == e:
+                    codes[r, at], g[r, at], want[r, at] = code, e, 2 * round((2 * k + 1) / 4)   # the even neighbour
+                    at += 1
+                    break
+            else:
+                continue
+            if at == 256:
+                break
+        assert at > 100
+    scales = 2 * torch.tensor(scale).repeat_interleave(cols // 256).reshape(len(scale), -1)
+    m = 0.5 * R.values(codes, scales) + 0.5 * g.double()
+    qc, qs = R.quantized(m)
+    assert torch.equal(qc, want) and torch.equal(qs, scales / 2)
+    p, codes, scales = torch.zeros(want.shape, device="cuda"), codes.cuda(), scales.cuda()
+    muon.muon8_step(p, g.cuda(), codes, scales, beta=0.5)
+    assert torch.equal(scales.cpu(), qs)
+    assert torch.equal(codes.cpu(), qc)
+
+
 @pytest.mark.parametrize("shape", [(5,), (1, 1), (3, 255), (2, 7, 512), (300, 1001)])
 def test_momentum8_values(shape):
     g = torch.Generator().manual_seed(3)
