@@ -584,10 +584,11 @@ __device__ __forceinline__ int4v buffer_of(uint64_t p, uint64_t bytes) {
 
 // 16 bytes a lane, from p + voff to LDS at `lds` + 16 * lane.  In asm, because
 // after the builtin the compiler waits for every such copy before any later
-// LDS read; here the waits are the kernel's own (stage_wait).
+// LDS read; here the waits are the kernel's own (stage_wait).  m0, which holds
+// the LDS address, is an operand: the compiler writes it and knows what it
+// holds.  A wait state belongs between that and the copy.
 __device__ __forceinline__ void copy_to_lds(int4v p, uint32_t lds, uint32_t voff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :: "s"(lds), "v"(voff), "s"(p) : "memory");   // nothing else here uses m0
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" :: "{m0}"(lds), "v"(voff), "s"(p) : "memory");
 }
 
 // This wave's copies are done but for the last N, and so are its LDS reads;
