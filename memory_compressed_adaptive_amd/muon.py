@@ -88,6 +88,13 @@ def _workspace(nbytes: int, device):
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
+def changed(*tensors) -> None:
+    """Tells autograd that a call has written them in place, so that a backward
+    pass that needs what they held before raises."""
+    import torch
+    torch.autograd.graph.increment_version(tensors)
+
+
 def orthogonalize(x, steps: int = 5, coefficients=COEFFICIENTS, eps: float = 1e-7, out=None, stream=None):
     """x [..., rows, cols] (fp32 or bf16) orthogonalized, as bf16: X = x /
     max(|x|_F, eps), then `steps` times X <- (a I + b A + c A A) X with A = X X^T
@@ -109,6 +116,7 @@ def orthogonalize(x, steps: int = 5, coefficients=COEFFICIENTS, eps: float = 1e-
         ws = _workspace(nbytes, x.device)
         _L.check(L.ma_orthogonalize(batch, rows, cols, x.data_ptr(), kind, sr, sb, out.data_ptr(), osr, osb, steps, k, eps,
                                     ws.data_ptr(), nbytes, s.cuda_stream))
+    changed(out)
     return out
 
 
@@ -143,6 +151,7 @@ def muon_step(params, grads, momentum, lr: float = 1e-3, beta: float = 0.95, wd:
         ws = _workspace(nbytes, params.device)
         _L.check(L.ma_muon_step(batch, rows, cols, *arrays, momentum.data_ptr(), *hyper, int(nesterov), steps, k, eps,
                                 ws.data_ptr(), nbytes, s.cuda_stream))
+    changed(params, momentum)
 
 
 def scales_shape(shape):
@@ -176,6 +185,7 @@ def muon8_step(params, grads, codes, scales, lr: float = 1e-3, beta: float = 0.9
         ws = _workspace(nbytes, params.device)
         _L.check(L.ma_muon8_step(batch, rows, cols, *arrays, codes.data_ptr(), scales.data_ptr(), *hyper, int(nesterov),
                                  steps, k, eps, ws.data_ptr(), nbytes, s.cuda_stream))
+    changed(params, codes, scales)
 
 
 def momentum8_values(codes, scales, out=None, stream=None):
@@ -192,4 +202,5 @@ def momentum8_values(codes, scales, out=None, stream=None):
         cols = codes.shape[-1]
         _L.check(_L.lib().ma_momentum8_values(codes.numel() // cols if cols else 0, cols, codes.data_ptr(),
                                               scales.data_ptr(), out.data_ptr(), s.cuda_stream))
+    changed(out)
     return out

@@ -168,6 +168,7 @@ class Muon(torch.optim.Optimizer):
                             _muon.muon8_step(p, g, st["codes"][at:end], st["scales"][at:end], **kw)
                         else:
                             _muon.muon_step(p, g, st["momentum"][at:end], **kw)
+                        _muon.changed(*st["of"][at:end])
                     at = end + 1
         return loss
 

@@ -309,6 +309,31 @@ def test_muon_step_writes_only_its_parameters():
     assert torch.equal(hold, keep)
 
 
+def test_autograd_sees_what_a_call_wrote():
+    x = torch.ones(20, 20, device="cuda", requires_grad=True)
+    g = _matrix((20, 20), 43, torch.bfloat16).cuda()
+    p, m = torch.ones(20, 20, device="cuda"), torch.zeros(20, 20, device="cuda")
+    codes, scales = torch.zeros(20, 20, dtype=torch.int8, device="cuda"), torch.zeros(20, 1, device="cuda")
+    out, values = torch.ones(20, 20, dtype=torch.bfloat16, device="cuda"), torch.ones(20, 20, device="cuda")
+    for t, call in ((p, lambda: muon.muon_step(p, g, m)), (m, lambda: muon.muon_step(p, g, m)),
+                    (p, lambda: muon.muon8_step(p, g, codes, scales)), (scales, lambda: muon.muon8_step(p, g, codes, scales)),
+                    (out, lambda: muon.orthogonalize(g, out=out)), (values, lambda: muon.momentum8_values(codes, scales, out=values))):
+        y = (x * t).sum()
+        before = codes._version
+        call()
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+    assert before > 0
+    # read only: as it was
+    y = (x * g).sum()
+    muon.muon_step(p, g, m)
+    muon.orthogonalize(g)
+    y.backward()
+    with torch.inference_mode():
+        q = torch.ones(20, 20, device="cuda")
+        muon.muon_step(q, g, m)
+
+
 def test_muon_captured_graphs_replay_as_eager_steps():
     """Two captured graphs (32- and 8-bit) replayed in turn with eager work
     between, each replay against an eager step from the same state."""

@@ -144,3 +144,22 @@ def test_a_model_trained_by_both_optimizers():
             o.step()
         assert all(torch.equal(p.detach(), q) for p, q in zip(matrices, want))
         assert all(bool(p.isfinite().all()) for p in model.parameters())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_kept_graph_is_not_used_with_new_parameters(bits):
+    """As with torch's own optimizers: a second backward pass over a graph that
+    kept the old parameters raises instead of using the new ones; parameters that
+    the step left alone do not hinder it."""
+    torch.manual_seed(0)
+    w, still = (torch.nn.Parameter(torch.randn(40, 40, device="cuda")) for _ in range(2))
+    x = torch.randn(8, 40, device="cuda", requires_grad=True)
+    opt = Muon([w, still], momentum_bits=bits)
+    first, second = (x @ w).sum(), (x @ still).sum()
+    first.backward(retain_graph=True)
+    opt.step()
+    second.backward(retain_graph=True)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        first.backward()
+    still.grad = None
+    (x @ w).sum().backward()
