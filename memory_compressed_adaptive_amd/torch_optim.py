@@ -135,7 +135,7 @@ class Muon(torch.optim.Optimizer):
         group = self.param_groups[-1]
         try:
             group["_stacks"] = _stacks(group)
-        except ValueError:
+        except BaseException:   # memory that runs out too
             self.param_groups.pop()
             raise
 
