@@ -156,8 +156,9 @@ struct Plan {
     // 8192: 726 and 627 us); with few rows, what rounding does to the diagonals
     // of P1 and T does not average out (37 x 3000: error 3.0e-3 against 1.4e-3)
     pairs = n > 128 && 3 * m >= 4 * n && gram.time + update.time > 1.1 * 3.0 * poly.time;
-    // where A stays near a multiple of I; it takes a tenth of P X's time (768 x
-    // 768: error 1.25e-3 without, 0.85e-3 with)
+    // where A stays near a multiple of I; it takes a tenth of P X's time, so the
+    // last product, of which nothing follows, goes without (wide matrices of 300 to
+    // 1024 rows: error 2.2e-4 to 2.9e-4 after one step, 2.9e-4 to 4.4e-4 after two)
     diagonal = m >= 2 * n;
     lost_bytes = (size_t)round_up(4 * chunk * np, 256);
     sum_bytes = (size_t)round_up((int64_t)gram.bytes, 256);
@@ -325,7 +326,8 @@ hipError_t run(const Plan &p, int64_t batch, const MuonInput &in, const MuonTarg
       };
       a.l_mat = a.r_mat = nn;
       a.l_ld = a.r_ld = a.k = p.np;
-      float *const keep = p.diagonal ? lost : nullptr;
+      // the last product has no step after it that would carry the rounding on
+      float *const keep = p.diagonal && t + (two ? 2 : 1) < steps ? lost : nullptr;
       a.lost = two ? nullptr : keep;
       a.lost_unit = 1.f / kScaleP;
       poly(ga, gp, t);

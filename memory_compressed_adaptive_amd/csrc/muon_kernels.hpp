@@ -522,7 +522,8 @@ struct MuonProduct {
   // units, [matrix][n]: written with it where not null, and added by kUpdate as
   // that many times the old X.  The diagonal holds most of a P while A is
   // small, and nearly the same value all along: its rounding would scale X as a
-  // whole (440 x 6000: error 2.1e-3 without, 1.1e-3 with).
+  // whole (440 x 6000: error 2.1e-3 without, 1.1e-3 with).  Null for the last
+  // product: that rounding, at most 2^-11 of the result, meets no further step.
   float *lost;
   float lost_unit;
   MuonTarget out;           // kOut: element (n, m) of matrix b0 + i goes to its row n, column m

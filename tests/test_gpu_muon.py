@@ -233,6 +233,22 @@ def test_muon_steps(rows, cols, dtype, nesterov, wd, bits):
             assert off <= tol, (off, tol)
 
 
+@pytest.mark.parametrize("steps", [1, 2, 3, 5])
+@pytest.mark.parametrize("rows,cols", [(300, 2400), (2400, 300), (440, 6000), (6000, 440), (130, 5000)])
+def test_muon_step_on_wide_matrices_of_few_steps(rows, cols, steps):
+    """fp32 parameters show the products' roundings, those of the last product's
+    diagonal too: nothing of them is hidden by a result in bf16."""
+    p = _matrix((rows, cols), 45, size=0.02)
+    g = _matrix((rows, cols), 46, torch.bfloat16)
+    want, err = R.orthogonalized(g, steps=steps)
+    got, m = p.cuda(), torch.zeros(rows, cols, device="cuda")
+    muon.muon_step(got, g.cuda(), m, lr=0.5, wd=0.1, beta=0.0, nesterov=False, scale=2.0, steps=steps)
+    want = p.double() * 0.95 - want
+    off, tol = (got.cpu().double() - want).norm().item(), err + 4 * R.FP32 * (want.norm().item() + err)
+    say(f"[muon] {rows}x{cols} steps={steps}: off {off:.2e}, allowed {tol:.2e}")
+    assert off <= tol
+
+
 def test_muon8_non_finite_block_and_short_block():
     rows, cols = 3, 600                               # blocks of 256, 256 and 88
     g = _matrix((rows, cols), 31, torch.bfloat16)
