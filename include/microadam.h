@@ -249,6 +249,18 @@ int ma_muon8_step(int64_t batch, int64_t rows, int64_t cols, void *params, int p
 int ma_momentum8_values(int64_t rows, int64_t cols, const int8_t *codes, const float *scales, float *out,
                         hipStream_t stream);
 
+/*
+ * How the Muon calls go about a batch of these sizes, for tests and diagnosis;
+ * no device is touched.  out (host, 9 values): 1 if one workgroup takes each
+ * matrix (values 2 to 8 are 0 then); 1 if tall; matrices that are taken at a
+ * time; 1 if steps are taken two together; the tile that makes X X^T, the parts
+ * of its summed index, and the tiles of the products of the short side, of P X
+ * and of the last P X.  Tiles: 64, 128, 129 (128, alone on a CU), 192, 250 (256
+ * x 192), 256.  MA_EINVAL: null out or an empty batch; MA_EUNSUPPORTED: sizes
+ * that the calls refuse.
+ */
+int ma_debug_muon_plan(int64_t batch, int64_t rows, int64_t cols, int64_t *out);
+
 /* Optimizer-state bytes the second paragraph of the MicroAdam page counts:
  * ceil(d/2) + 4*m*k (0.9d at m = 10, k = d/100).  0 for NULL. */
 size_t ma_state_bytes(const ma_ctx *h);

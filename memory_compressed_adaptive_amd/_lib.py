@@ -39,6 +39,7 @@ EXPORTS = (
     "ma_set_lr", "ma_read_state", "ma_write_state", "ma_export_state", "ma_import_state", "ma_debug_moments", "ma_debug_residual", "ma_set_timing",
     "ma_kernel_times", "ma_set_pipeline", "ma_get_pipeline", "ma_set_count_touched", "ma_touched_count",
     "ma_orthogonalize_workspace", "ma_orthogonalize", "ma_muon_step", "ma_muon8_step", "ma_momentum8_values",
+    "ma_debug_muon_plan",
 )
 
 _lib = None
@@ -128,6 +129,8 @@ def lib():
                                 C.c_int, p, f32, p, size, p]
     L.ma_momentum8_values.restype = C.c_int
     L.ma_momentum8_values.argtypes = [i64, i64, p, p, p, p]
+    L.ma_debug_muon_plan.restype = C.c_int
+    L.ma_debug_muon_plan.argtypes = [i64, i64, i64, C.POINTER(i64)]
     _lib = L
     return L
 

@@ -464,6 +464,27 @@ size_t ma_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols) {
   return Plan(batch, rows, cols).bytes;
 }
 
+int ma_debug_muon_plan(int64_t batch, int64_t rows, int64_t cols, int64_t *out) {
+  clear_error();
+  const char *who = "ma_debug_muon_plan";
+  if (!out) return fail(MA_EINVAL, "%s: null pointer", who);
+  if (batch < 1 || rows < 1 || cols < 1) return fail(MA_EINVAL, "%s: batch, rows and cols must be >= 1", who);
+  if (!sizes_ok(batch, rows, cols)) return fail(MA_EUNSUPPORTED, "%s: a matrix of more than 2^33 elements or a side over 2^21", who);
+  const Plan p(batch, rows, cols);
+  for (int e = 0; e < 9; ++e) out[e] = 0;
+  out[0] = p.small;
+  out[1] = p.tall;
+  if (p.small) return MA_OK;
+  out[2] = p.chunk;
+  out[3] = p.pairs;
+  out[4] = p.gram.kind;
+  out[5] = p.gram.parts;
+  out[6] = p.poly.kind;
+  out[7] = p.update.kind;
+  out[8] = p.last.kind;
+  return MA_OK;
+}
+
 int ma_orthogonalize(int64_t batch, int64_t rows, int64_t cols, const void *x, int x_type, int64_t x_row, int64_t x_batch,
                      uint16_t *out, int64_t out_row, int64_t out_batch, int steps, const float *coefficients, float eps,
                      void *workspace, size_t workspace_bytes, hipStream_t stream) {

@@ -145,3 +145,105 @@ def quantized(m):
 def values(codes, scales):
     at = torch.arange(codes.shape[-1]) // 256
     return codes.double() * scales.double()[..., at]
+
+
+def orthogonalized_large(u, steps=5, coefficients=COEFFICIENTS, eps=1e-7):
+    """(result, bound) as orthogonalized gives them for random roundings, where u
+    is: 64-bit products on the GPU for large matrices.  The singular values come
+    from the Gram matrix, near enough for a bound."""
+    u = u.detach().double()
+    x = (u.T if u.shape[0] > u.shape[1] else u).contiguous()
+    x = x / max(x.norm().item(), eps)
+    n, m = x.shape
+    ks = triples(coefficients, steps)
+    s = torch.linalg.eigvalsh((x @ x.T.contiguous()).cpu()).clamp(min=0).sqrt().clamp(min=1e-300).to(u.device)
+    err = _random(s, n, m, ks)
+    for a, b, c in ks:
+        gram = x @ x.T.contiguous()
+        ax = gram @ x
+        x = a * x + b * ax + c * (gram @ ax)
+    return (x.T if u.shape[0] > u.shape[1] else x), err
+
+
+def orthogonalized_worst(u, steps=5, coefficients=COEFFICIENTS, eps=1e-7):
+    """(result, bound) in the worst case, steps taken one by one or in twos (a
+    single one of an odd number in the middle), whichever bound is larger.
+
+    How far each entry can be off, to first order, every rounding being h of its
+    entry at most and none of them averaging out.  |M| holds the entries'
+    magnitudes; dX starts as h |X|:  dA = dX |X|' + |X| dX' + h |A|;
+    dP = |b| dA + |c| (|A| dA + dA |A|) + h |P|;  of a single step
+    dX <- |P| dX + dP |X| + h |P X|.  Of two:  dT = |P1| dA + dP1 |A| + h |T|;
+    dA' = |T| dP1 + dT |P1| + h |A'|;  dP2 as dP, of A';
+    dQ = |P2| dP1 + dP2 |P1| + h |Q|;  dX <- |Q| dX + dQ |X| + h |Q X|.  The last
+    product is not rounded."""
+    u = u.detach().cpu().double()
+    x0 = (u.T if u.shape[0] > u.shape[1] else u).contiguous()
+    x0 = x0 / max(x0.norm().item(), eps)
+    ks = triples(coefficients, steps)
+    eye = torch.eye(x0.shape[0], dtype=torch.float64)
+
+    def poly(k, gram, dgram):
+        p = k[0] * eye + k[1] * gram + k[2] * (gram @ gram)
+        size = gram.abs()
+        return p, abs(k[1]) * dgram + abs(k[2]) * (size @ dgram + dgram @ size) + H * p.abs()
+
+    def times(l, dl, r, dr):
+        d = l @ r
+        return d, l.abs() @ dr + dl @ r.abs() + H * d.abs()
+
+    def follow(pairs):
+        x, dx, t = x0, H * x0.abs(), 0
+        single = (steps // 2 + 1) // 2 * 2 if steps % 2 else -1
+        while t < steps:
+            gram, dgram = times(x, dx, x.T, dx.T)
+            f, df = poly(ks[t], gram, dgram)
+            if pairs and t != single:
+                second, dsecond = times(*times(f, df, gram, dgram), f, df)
+                p2, dp2 = poly(ks[t + 1], second, dsecond)
+                f, df = times(p2, dp2, f, df)
+                t += 1
+            x, dx = times(f, df, x, dx)
+            t += 1
+        return x, (dx - H * x.abs()).norm().item()
+
+    x, err = follow(False)
+    err = max(err, follow(True)[1])
+    return (x.T if u.shape[0] > u.shape[1] else x), err
+
+
+def flat_worst(n, steps=5, coefficients=COEFFICIENTS):
+    """For n equal singular values A, P and their products are multiples of I: all
+    entries of a diagonal are rounded alike, and X is off by one factor.  The
+    largest that factor can be (relative to the result), each rounding being h at
+    most; the recursion of orthogonalized_worst for numbers, but with the slope of
+    the polynomials.  Roundings of X are
+    not in it."""
+    ks = triples(coefficients, steps)
+
+    def follow(pairs):
+        s, err, t = n ** -0.5, 0.0, 0
+        single = (steps // 2 + 1) // 2 * 2 if steps % 2 else -1
+        while t < steps:
+            take = ks[t:t + 2] if pairs and t != single else ks[t:t + 1]
+            end, slope = _odd(torch.tensor(s, dtype=torch.float64), take)
+            a, b, c = take[0]
+            gram = s * s
+            p1 = a + b * gram + c * gram * gram
+            da = H * gram
+            moved = dp1 = abs(b + 2 * c * gram) * da + H * abs(p1)
+            if len(take) == 2:
+                a, b, c = take[1]
+                tt = p1 * gram
+                gram2 = tt * p1
+                dt = gram * dp1 + abs(p1) * da + H * abs(tt)
+                da2 = abs(p1) * dt + abs(tt) * dp1 + H * gram2
+                p2 = a + b * gram2 + c * gram2 * gram2
+                dp2 = abs(b + 2 * c * gram2) * da2 + H * abs(p2)
+                moved = abs(p1) * dp2 + abs(p2) * dp1 + H * abs(p1 * p2)
+            err = abs(slope.item()) * err + s * moved
+            s = abs(end.item())
+            t += len(take)
+        return err / s
+
+    return max(follow(False), follow(True))
