@@ -140,7 +140,7 @@ def _special(which, rows, cols):
 def test_orthogonalize_special_matrices(rows, cols, which, steps):
     """Singular vectors that are not spread over the entries, where roundings need
     not average out."""
-    u = _special(which, rows, cols)
+    u = _special(which, rows, cols) if rows <= cols else _special(which, cols, rows).T.contiguous()
     want, err = R.orthogonalized_worst(u, steps=steps)
     size = want.norm().item()
     off = (muon.orthogonalize(u.cuda(), steps=steps).cpu().double() - want).norm().item()
