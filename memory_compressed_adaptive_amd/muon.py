@@ -37,15 +37,17 @@ def _host_coefficients(coefficients, steps: int):
     """The C array of (a, b, c) for every step: `coefficients` is one triple or
     `steps` of them."""
     _L.require(steps >= 1, "steps must be at least 1")
-    rows = coefficients if hasattr(coefficients[0], "__len__") else (coefficients,) * steps
-    _L.require(len(rows) == steps and all(len(r) == 3 for r in rows),
+    rows = (coefficients,) * steps if not any(isinstance(v, tuple) for v in coefficients) else coefficients
+    _L.require(len(rows) == steps and all(isinstance(r, tuple) and len(r) == 3 for r in rows),
                "coefficients must be one triple (a, b, c) or one for each step")
-    return (C.c_float * (3 * steps))(*(float(v) for r in rows for v in r))
+    return (C.c_float * (3 * steps))(*(v for r in rows for v in r))
 
 
 def _coefficients(coefficients, steps: int):
-    if isinstance(coefficients, list):
-        coefficients = tuple(tuple(r) if isinstance(r, (list, tuple)) else r for r in coefficients)
+    if type(coefficients) is not tuple or not all(type(v) is float for v in coefficients):
+        # any sequences of numbers; as tuples of floats they are told apart by value
+        coefficients = tuple(tuple(map(float, r)) if hasattr(r, "__len__") and getattr(r, "ndim", 1) else float(r)
+                             for r in coefficients)
     return _host_coefficients(coefficients, int(steps))
 
 

@@ -214,3 +214,28 @@ def test_written_matrices_may_interleave_but_not_overlap(rows, cols, row, bat, b
     assert _step(L.lib().ma_muon_step, (None,), batch=batch, rows=rows, cols=cols, ps=(row, bat), gs=(0, 0), ws_bytes=1 << 60) == L.MA_EINVAL
     assert ("momentum" in L.last_error()[1]) == ok, L.last_error()[1]
     assert ok or "overlap" in L.last_error()[1]
+
+
+@pytest.mark.parametrize("given", [((1.5, -0.5, 0.0), (2.0, -1.0, 0.0)), [[1.5, -0.5, 0.0], [2.0, -1.0, 0.0]],
+                                   ([1.5, -0.5, 0.0], [2.0, -1.0, 0.0]), [(1.5, -0.5, 0.0), (2.0, -1.0, 0.0)],
+                                   torch.tensor([[1.5, -0.5, 0.0], [2.0, -1.0, 0.0]])])
+def test_coefficients_may_be_any_sequences(given):
+    assert list(muon._coefficients(given, 2)) == [1.5, -0.5, 0.0, 2.0, -1.0, 0.0]
+
+
+@pytest.mark.parametrize("given", [(1.5, -0.5, 0.0), [1.5, -0.5, 0.0], torch.tensor([1.5, -0.5, 0.0])])
+def test_one_triple_serves_every_step(given):
+    assert list(muon._coefficients(given, 2)) == [1.5, -0.5, 0.0] * 2
+
+
+@pytest.mark.parametrize("given", [(), [], ((),), (1.0, 2.0), ((1.0, 2.0),), ((1.0, 2.0, 3.0),), ((1.0, 2.0, 3.0), 1.0)])
+def test_other_coefficients_are_refused(given):
+    with pytest.raises(ValueError, match="coefficients"):
+        muon._coefficients(given, 2)
+
+
+def test_coefficients_that_change_are_read_again():
+    a = torch.tensor(1.5)
+    assert muon._coefficients((a, -0.5, 0.0), 1)[0] == 1.5
+    a += 0.25
+    assert muon._coefficients((a, -0.5, 0.0), 1)[0] == 1.75
