@@ -187,10 +187,16 @@ int ma_adamw8_step(int64_t n, int64_t t, float beta1, float beta2, float eps, fl
  * coefficients: host array of 3*steps floats.  With (3.4445, -4.7750, 2.0315)
  * five times, singular values from about 0.01 to 1 end between 0.68 and 1.2.
  * X, A and a I + b A + c A A are rounded to 11 bits (fp16 with a fixed power of
- * two) after every product, products are summed in fp32: the result is within
- * about 2e-3 of the formula's (2-norm over 2-norm) for matrices whose singular
- * values lie within two orders of magnitude; directions that are smaller by
- * 2^-11 and more are lost in the rounding of their larger neighbours.
+ * two) after every product, products are summed in fp32.  With five such steps
+ * the bf16 result is off the formula's by 2e-3 (2-norm over 2-norm; its own
+ * rounding is 1.7e-3 of it) for random matrices, by 2.8e-3 to 4.2e-3 where the
+ * singular values go evenly through two orders of magnitude.  Directions that
+ * are smaller by 2^-11 and more are lost in the rounding of their larger
+ * neighbours, and the steps raise what rounding leaves there as they raise any
+ * small singular value: a matrix of an eighth of the full rank is off by 2e-2
+ * to 4e-2.  Bits repeat for the same batch, rows and cols; how the products are
+ * made depends on all three, so a matrix's result can differ by roundings with
+ * the batch that it is in.
  * Coefficients for which a singular value could pass 1.95, an eigenvalue of the
  * polynomial 15, or all values shrink below 1e-3 are rejected (MA_EINVAL).
  * A zero matrix gives zeros, one with a NaN or an infinity gives NaN throughout.

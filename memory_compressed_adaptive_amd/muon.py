@@ -8,8 +8,16 @@ ma_momentum8_values of include/microadam.h; the formulas and their rounding
 stand there).  Calls are asynchronous on `stream` (default: the current stream
 of the tensors' device), allocate their workspace and new results through torch
 on that stream and can be captured into a graph.  A tensor that another stream
-made must be ordered before `stream` by the caller, as for any kernel, and so
-must what another stream does with a result.
+made must be ordered before `stream` by the caller, as for any kernel, and kept
+until its work there is done (Tensor.record_stream), and so must what another
+stream does with a result.
+
+Products are rounded to 11 bits: a result is off by about 2e-3 for random
+matrices, by more where singular values are far apart (the header gives
+figures).  The same call on the same sizes repeats its bits; a matrix alone and
+the same matrix in a larger batch can differ by roundings.  `coefficients`
+that could carry a singular value past 1.95 or an eigenvalue of a I + b A + c A A
+past 15 are refused (MicroAdamError): the products' number format ends there.
 """
 from __future__ import annotations
 

@@ -119,9 +119,12 @@ class Muon(torch.optim.Optimizer):
     the update, "rms" for 0.2 sqrt(max(rows, cols)) (one learning rate then
     serves this and MicroAdamW).  lr, weight_decay, momentum, nesterov and scale
     may be changed between steps.  A parameter without a gradient is left alone,
-    its momentum too.  Gradients are rounded to bfloat16, as MicroAdamW rounds
-    them.  The parameters are moved into one buffer for each shape and type here:
-    a model is moved or converted before this, not after (step refuses then).
+    its momentum too; its neighbours in a buffer then go in smaller batches, which
+    can change their results by roundings.  Gradients are rounded to bfloat16, as
+    MicroAdamW rounds them, into a buffer of 2 bytes per parameter that is kept
+    beside the momentum, with a copy for each parameter.  The parameters are moved
+    into one buffer for each shape and type here: a model is moved or converted
+    before this, not after (step refuses then).
     """
 
     def __init__(self, params, lr=1e-3, momentum=0.95, weight_decay=0.0, nesterov=True, scale="rms", steps=5,
