@@ -163,3 +163,22 @@ def test_a_kept_graph_is_not_used_with_new_parameters(bits):
         first.backward()
     still.grad = None
     (x @ w).sum().backward()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_captured_step_replays_as_eager_ones(bits):
+    ps, qs = _params(3), _params(3)
+    for p, q, g in zip(ps, qs, _grads(3)):
+        p.grad, q.grad = g, g.clone()
+    captured, eager = Muon(ps, weight_decay=0.1, momentum_bits=bits), Muon(qs, weight_decay=0.1, momentum_bits=bits)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured.step()
+    for t in range(4):
+        for p, q, g in zip(ps, qs, _grads(30 + t)):
+            p.grad.copy_(g)
+            q.grad.copy_(g)
+        graph.replay()
+        eager.step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(ps, qs)), t
