@@ -267,6 +267,94 @@ int ma_momentum8_values(int64_t rows, int64_t cols, const int8_t *codes, const f
  */
 int ma_debug_muon_plan(int64_t batch, int64_t rows, int64_t cols, int64_t *out);
 
+/*
+ * AdamW over a list of tensors, each where it lies: for a model's embeddings,
+ * head and vectors beside Muon, for adapters, or for all of a model.  Stateless,
+ * on caller-owned device arrays.
+ *
+ * A list is a host array, read during the call only; a captured launch holds its
+ * own.  State arrays (moments, copies) serve a whole list: element e of a tensor
+ * has its state at index at + e.  `at` is a multiple of 256 and lies behind the
+ * end of the tensor before it; the arrays have state_n elements, a multiple of
+ * 256, and begin at multiples of 16 bytes (scales: of 4).  What lies between a
+ * tensor's end and the next one's `at` is neither used nor changed.  Parameters
+ * and gradients may begin at any element.  Parameters must not overlap each other
+ * (MA_EINVAL) nor anything else of the call; gradients may be the same.  Types
+ * may differ from tensor to tensor.  Tensors with n = 0 are passed over.
+ *
+ * Calls only enqueue work on `stream` (at most one launch for every 112 tensors
+ * of one pair of types; ma_grad_norm one for every 184 and one more), allocate
+ * nothing on the device and can be captured into a HIP graph.  Nothing uses
+ * atomics: a call repeats its bits, and how tensors are put together in lists
+ * changes none of a step's.
+ *
+ * MA_EINVAL: null or misaligned pointers (parameters and gradients to their
+ * elements), negative sizes, unknown types, `at` out of order or past state_n,
+ * arguments out of range (below).  MA_EUNSUPPORTED: more than 2^40 elements.
+ */
+typedef struct ma_tensor {
+    void *param;            /* device; not read by ma_grad_norm, as `at` and p_type */
+    const void *grad;       /* device, read only */
+    int64_t n;              /* elements, one after the other in both */
+    int64_t at;
+    int32_t p_type, g_type; /* MA_TYPE_F32 or MA_TYPE_BF16 */
+} ma_tensor;
+
+/*
+ * The norm of all gradients of a list, N = sqrt(sum g^2), and the factor that
+ * clips them to max_norm: out (device f32[2]) = N, scale = min(1, max_norm /
+ * (N + 1e-6)).  If N is not finite, scale is NaN, which makes the steps below
+ * change nothing.  t (device, may be null): a count of steps, raised by one if N
+ * is finite.  Squares are summed in 64 bits.  max_norm > 0, may be infinite.
+ * workspace: device memory of at least ma_grad_norm_workspace(count) bytes,
+ * 256-byte aligned, the call's own until its work on `stream` is done.  An empty
+ * list has the norm 0.
+ */
+size_t ma_grad_norm_workspace(int64_t count);
+int ma_grad_norm(int64_t count, const ma_tensor *tensors, double max_norm, float *out, int64_t *t, void *workspace,
+                 size_t workspace_bytes, hipStream_t stream);
+
+typedef struct ma_adamw_args {
+    double lr, beta1, beta2, eps, wd;   /* lr finite, 0 <= beta < 1, eps > 0 (a normal fp32), wd >= 0 */
+    int64_t t;                          /* this step's number, from 1 */
+    /* device, each may be null; what a captured step reads anew at every replay */
+    const int64_t *t_dev;               /* instead of t; below 1 the step changes nothing */
+    const float *lr_dev;                /* instead of lr */
+    const float *scale;                 /* factor of the gradients; NaN: the step changes nothing */
+} ma_adamw_args;
+
+/*
+ * One AdamW step of all tensors: with x = scale*g
+ *   m <- beta1*m + (1-beta1)*x,  v <- beta2*v + (1-beta2)*x^2
+ *   p <- p - lr*(u + wd*p),  u = (m / (1-beta1^t)) / (sqrt(v / (1-beta2^t)) + eps)
+ * m, v: f32[state_n], zero before the first step.  In fp32; a bf16 parameter is
+ * widened and its new value rounded to nearest even once.  copy (may be null):
+ * f32[state_n], the 32-bit copies of the bf16 parameters, which are updated in
+ * their place and rounded into them (a list's fp32 parameters do not use theirs).
+ */
+int ma_adamw_many_step(int64_t count, const ma_tensor *tensors, const ma_adamw_args *args, float *copy, float *m, float *v,
+                       int64_t state_n, hipStream_t stream);
+
+/*
+ * The same step with the moments in 8 bits (2 + 8/256 bytes per parameter): for
+ * each 256 elements of a tensor (its last block may be short) two scales, sm =
+ * max |m| and sr = max sqrt(v) rounded to fp32, and for each element the codes
+ *   cm: int8 c,  m = sm*c*|c| / 127^2      cv: uint8 q,  sqrt(v) = sr*q^2 / 255^2
+ * of the nearest values (of two equally near ones the larger in magnitude; q >= 1
+ * where v > 0).  Unlike ma_adamw8_step's even steps these resolve m and sqrt(v)
+ * far below a block's largest value alike, so that their quotient keeps a meaning
+ * there.  Moments are formed and codes decided in 64 bits; the update takes the
+ * new moments before they are rounded.  All arrays zero before the first step; cm,
+ * cv have state_n elements, sm, sr state_n/256.  A block with a NaN or an infinity
+ * gets NaN scales and zero codes: it reads as NaN.
+ */
+int ma_adamw8_many_step(int64_t count, const ma_tensor *tensors, const ma_adamw_args *args, float *copy, int8_t *cm,
+                        uint8_t *cv, float *sm, float *sr, int64_t state_n, hipStream_t stream);
+
+/* Reads 8-bit moments: m, v (f32[state_n]), each rounded once. */
+int ma_adamw8_many_values(int64_t state_n, const int8_t *cm, const uint8_t *cv, const float *sm, const float *sr, float *m,
+                          float *v, hipStream_t stream);
+
 /* Optimizer-state bytes the second paragraph of the MicroAdam page counts:
  * ceil(d/2) + 4*m*k (0.9d at m = 10, k = d/100).  0 for NULL. */
 size_t ma_state_bytes(const ma_ctx *h);

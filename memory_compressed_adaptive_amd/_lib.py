@@ -40,9 +40,22 @@ EXPORTS = (
     "ma_kernel_times", "ma_set_pipeline", "ma_get_pipeline", "ma_set_count_touched", "ma_touched_count",
     "ma_orthogonalize_workspace", "ma_orthogonalize", "ma_muon_step", "ma_muon8_step", "ma_momentum8_values",
     "ma_debug_muon_plan",
+    "ma_grad_norm_workspace", "ma_grad_norm", "ma_adamw_many_step", "ma_adamw8_many_step", "ma_adamw8_many_values",
 )
 
 _lib = None
+
+
+class Tensor(C.Structure):
+    """ma_tensor"""
+    _fields_ = [("param", C.c_void_p), ("grad", C.c_void_p), ("n", C.c_int64), ("at", C.c_int64), ("p_type", C.c_int32),
+                ("g_type", C.c_int32)]
+
+
+class AdamwArgs(C.Structure):
+    """ma_adamw_args"""
+    _fields_ = [("lr", C.c_double), ("beta1", C.c_double), ("beta2", C.c_double), ("eps", C.c_double), ("wd", C.c_double),
+                ("t", C.c_int64), ("t_dev", C.c_void_p), ("lr_dev", C.c_void_p), ("scale", C.c_void_p)]
 
 
 class MicroAdamError(RuntimeError):
@@ -131,6 +144,16 @@ def lib():
     L.ma_momentum8_values.argtypes = [i64, i64, p, p, p, p]
     L.ma_debug_muon_plan.restype = C.c_int
     L.ma_debug_muon_plan.argtypes = [i64, i64, i64, C.POINTER(i64)]
+    L.ma_grad_norm_workspace.restype = size
+    L.ma_grad_norm_workspace.argtypes = [i64]
+    L.ma_grad_norm.restype = C.c_int
+    L.ma_grad_norm.argtypes = [i64, p, f64, p, p, p, size, p]
+    L.ma_adamw_many_step.restype = C.c_int
+    L.ma_adamw_many_step.argtypes = [i64, p, C.POINTER(AdamwArgs), p, p, p, i64, p]
+    L.ma_adamw8_many_step.restype = C.c_int
+    L.ma_adamw8_many_step.argtypes = [i64, p, C.POINTER(AdamwArgs), p, p, p, p, p, i64, p]
+    L.ma_adamw8_many_values.restype = C.c_int
+    L.ma_adamw8_many_values.argtypes = [i64, p, p, p, p, p, p, p]
     _lib = L
     return L
 

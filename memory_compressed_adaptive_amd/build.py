@@ -2,8 +2,8 @@
 
     python -m memory_compressed_adaptive_amd.build
 
-libmicroadam.so  -- the MicroAdam step and the Muon operators (C ABI in
-                    include/microadam.h)
+libmicroadam.so  -- the MicroAdam step, the Muon operators and AdamW over
+                    many tensors (C ABI in include/microadam.h)
 libmasynth.so    -- the seeded synthetic-input generator used by the benchmark
                     and the tests (no optimizer arithmetic in it)
 
@@ -37,7 +37,8 @@ COMMON = [
 ]
 
 TARGETS = {
-    "libmicroadam.so": [os.path.join(CSRC, "microadam.hip"), os.path.join(CSRC, "muon.hip")],
+    "libmicroadam.so": [os.path.join(CSRC, "microadam.hip"), os.path.join(CSRC, "muon.hip"),
+                        os.path.join(CSRC, "adamw_many.hip")],
     "libmasynth.so": [os.path.join(CSRC, "synth.hip")],
 }
 

@@ -1,0 +1,268 @@
+// Host side of the AdamW operators over many tensors (include/microadam.h):
+// argument checks, the tables that the launches carry, and the launches.
+#include <float.h>
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+#include <new>
+#include <utility>
+#include <vector>
+
+#include "adamw_many_kernels.hpp"
+#include "host.hpp"
+#include "microadam.h"
+
+using namespace adamw_many;
+using microadam::clear_error;
+using microadam::DeviceGuard;
+using microadam::fail;
+
+namespace {
+
+constexpr int64_t kMost = int64_t(1) << 40;   // elements of a tensor, and of a state
+constexpr unsigned kGroups = 256 * 8;         // workgroups of a launch, at most: eight to a CU
+
+bool type_ok(int t) { return t == MA_TYPE_F32 || t == MA_TYPE_BF16; }
+bool misaligned(const void *p, int type) { return ((uintptr_t)p & (type == MA_TYPE_F32 ? 3u : 1u)) != 0; }
+int64_t size_of(int type) { return type == MA_TYPE_F32 ? 4 : 2; }
+
+int check_list(const char *who, int64_t count, const ma_tensor *tensors) {
+  if (count < 0) return fail(MA_EINVAL, "%s: a negative count", who);
+  if (count && !tensors) return fail(MA_EINVAL, "%s: null list", who);
+  for (int64_t i = 0; i < count; ++i) {
+    const ma_tensor &t = tensors[i];
+    if (t.n < 0) return fail(MA_EINVAL, "%s: tensor %lld has a negative size", who, (long long)i);
+    if (t.n > kMost) return fail(MA_EUNSUPPORTED, "%s: tensor %lld has more than 2^40 elements", who, (long long)i);
+    if (!type_ok(t.g_type)) return fail(MA_EINVAL, "%s: tensor %lld: unknown type %d", who, (long long)i, (int)t.g_type);
+    if (t.n && (!t.grad || misaligned(t.grad, t.g_type)))
+      return fail(MA_EINVAL, "%s: tensor %lld: null or misaligned gradient", who, (long long)i);
+  }
+  return MA_OK;
+}
+
+// What a step needs besides: parameters that do not overlap, states in order.
+int check_step(const char *who, int64_t count, const ma_tensor *tensors, const ma_adamw_args *a, const float *copy, int64_t state_n) {
+  if (const int rc = check_list(who, count, tensors)) return rc;
+  if (!a) return fail(MA_EINVAL, "%s: null arguments", who);
+  if (!(a->beta1 >= 0.0 && a->beta1 < 1.0 && a->beta2 >= 0.0 && a->beta2 < 1.0))
+    return fail(MA_EINVAL, "%s: beta1 and beta2 must be in [0, 1)", who);
+  if (!(a->eps >= FLT_MIN && a->eps <= FLT_MAX)) return fail(MA_EINVAL, "%s: eps must be positive and finite (a normal fp32)", who);
+  if (!std::isfinite(a->lr) || !(a->wd >= 0.0) || !std::isfinite(a->wd))
+    return fail(MA_EINVAL, "%s: lr and wd must be finite, wd >= 0", who);
+  if (!a->t_dev && a->t < 1) return fail(MA_EINVAL, "%s: t must be >= 1", who);
+  if (((uintptr_t)a->t_dev & 7u) || ((uintptr_t)a->lr_dev & 3u) || ((uintptr_t)a->scale & 3u) || ((uintptr_t)copy & 15u))
+    return fail(MA_EINVAL, "%s: misaligned pointer", who);
+  if (state_n < 0 || state_n % kBlock) return fail(MA_EINVAL, "%s: the states' size must be a multiple of %d", who, kBlock);
+  if (state_n > kMost) return fail(MA_EUNSUPPORTED, "%s: states of more than 2^40 elements", who);
+  int64_t end = 0;
+  std::vector<std::pair<uintptr_t, uintptr_t>> spans;
+  spans.reserve((size_t)count);
+  bool sorted = true;
+  for (int64_t i = 0; i < count; ++i) {
+    const ma_tensor &t = tensors[i];
+    if (!type_ok(t.p_type)) return fail(MA_EINVAL, "%s: tensor %lld: unknown type %d", who, (long long)i, (int)t.p_type);
+    if (!t.n) continue;
+    if (!t.param || misaligned(t.param, t.p_type))
+      return fail(MA_EINVAL, "%s: tensor %lld: null or misaligned parameter", who, (long long)i);
+    if (t.at < end || t.at % kBlock || t.at > state_n || t.n > state_n - t.at)
+      return fail(MA_EINVAL, "%s: tensor %lld: its states must begin at a multiple of %d behind the last tensor's and end in the arrays",
+                  who, (long long)i, kBlock);
+    end = t.at + t.n;
+    const uintptr_t p = (uintptr_t)t.param, q = p + (uintptr_t)(t.n * size_of(t.p_type));
+    if (!spans.empty() && p < spans.back().second) sorted = false;
+    spans.emplace_back(p, q);
+  }
+  if (!sorted) std::sort(spans.begin(), spans.end());
+  for (size_t i = 1; i < spans.size(); ++i)
+    if (spans[i].first < spans[i - 1].second) return fail(MA_EINVAL, "%s: two parameters overlap", who);
+  return MA_OK;
+}
+
+int device_of(hipStream_t stream, int *dev) {
+  if (!stream || stream == hipStreamLegacy || stream == hipStreamPerThread) return hipGetDevice(dev) == hipSuccess ? MA_OK : MA_EHIP;
+  return hipStreamGetDevice(stream, dev) == hipSuccess ? MA_OK : MA_EHIP;
+}
+
+// Runs f(), which returns a hipError_t, with the stream's device current.
+template <class F> int on_device(const char *who, hipStream_t stream, F f) {
+  int dev = 0;
+  if (device_of(stream, &dev) != MA_OK) return fail(MA_EHIP, "%s: the stream has no device", who);
+  DeviceGuard guard(dev);
+  if (!guard.ok) return fail(MA_EHIP, "%s: device %d cannot be made current", who, dev);
+  const hipError_t e = f();
+  if (e != hipSuccess) return fail(MA_EHIP, "%s: launch failed: %s", who, hipGetErrorString(e));
+  return MA_OK;
+}
+
+// Nothing may be thrown through the C boundary.
+template <class F> int guarded(const char *who, F f) {
+  clear_error();
+  try {
+    return f();
+  } catch (const std::bad_alloc &) {
+    return fail(MA_ENOMEM, "%s: out of host memory", who);
+  }
+}
+
+// launch(table) for every kTable tensors of the list with these types.
+template <class F> hipError_t each_table(int64_t count, const ma_tensor *tensors, int p_type, int g_type, F launch) {
+  Table T;
+  int used = 0;
+  const auto flush = [&] {
+    std::fill(T.first + used, T.first + kTable, ~0u);
+    const hipError_t e = launch(T);
+    used = 0;
+    return e;
+  };
+  T.chunks = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const ma_tensor &t = tensors[i];
+    if (!t.n || t.p_type != p_type || t.g_type != g_type) continue;
+    if (!used) T.chunks = 0;
+    T.param[used] = t.param;
+    T.grad[used] = t.grad;
+    T.n[used] = t.n;
+    T.block[used] = (uint32_t)(t.at / kBlock);
+    T.first[used] = T.chunks;
+    T.chunks += (uint32_t)((t.n + kChunk - 1) / kChunk);   // at most 2^29 in all: the states have 2^40 elements
+    if (++used == kTable)
+      if (const hipError_t e = flush(); e != hipSuccess) return e;
+  }
+  return used ? flush() : hipSuccess;
+}
+
+// launch.template operator()<P, G, COPY>(table) over the whole list.
+template <class F> hipError_t each_type(int64_t count, const ma_tensor *tensors, bool copy, F launch) {
+  hipError_t e = each_table(count, tensors, MA_TYPE_F32, MA_TYPE_F32, [&](const Table &T) { return launch(T, (float *)0, (float *)0, std::false_type()); });
+  if (e == hipSuccess)
+    e = each_table(count, tensors, MA_TYPE_F32, MA_TYPE_BF16, [&](const Table &T) { return launch(T, (float *)0, (__bf16 *)0, std::false_type()); });
+  if (e == hipSuccess)
+    e = each_table(count, tensors, MA_TYPE_BF16, MA_TYPE_F32, [&](const Table &T) {
+      return copy ? launch(T, (__bf16 *)0, (float *)0, std::true_type()) : launch(T, (__bf16 *)0, (float *)0, std::false_type());
+    });
+  if (e == hipSuccess)
+    e = each_table(count, tensors, MA_TYPE_BF16, MA_TYPE_BF16, [&](const Table &T) {
+      return copy ? launch(T, (__bf16 *)0, (__bf16 *)0, std::true_type()) : launch(T, (__bf16 *)0, (__bf16 *)0, std::false_type());
+    });
+  return e;
+}
+
+StepArgs step_args(const ma_adamw_args &a) {
+  return {a.lr, a.beta1, a.beta2, a.eps, a.wd, a.t, a.t_dev, a.lr_dev, a.scale};
+}
+
+int64_t norm_launches(int64_t count) { return (count + kNormTable - 1) / kNormTable; }
+
+}  // namespace
+
+extern "C" {
+
+size_t ma_grad_norm_workspace(int64_t count) {
+  if (count <= 0 || count > (int64_t(1) << 40)) return 0;
+  return (size_t)norm_launches(count) * kNormGroups * sizeof(double);
+}
+
+int ma_grad_norm(int64_t count, const ma_tensor *tensors, double max_norm, float *out, int64_t *t, void *workspace,
+                 size_t workspace_bytes, hipStream_t stream) {
+  const char *who = "ma_grad_norm";
+  return guarded(who, [&] {
+    if (const int rc = check_list(who, count, tensors)) return rc;
+    if (!(max_norm > 0.0)) return fail(MA_EINVAL, "%s: max_norm must be positive", who);
+    if (!out || ((uintptr_t)out & 3u)) return fail(MA_EINVAL, "%s: null or misaligned out", who);
+    if ((uintptr_t)t & 7u) return fail(MA_EINVAL, "%s: misaligned count", who);
+    if (count && (!workspace || ((uintptr_t)workspace & 255u)))
+      return fail(MA_EINVAL, "%s: the workspace must be 256-byte aligned", who);
+    if (workspace_bytes < ma_grad_norm_workspace(count))
+      return fail(MA_EINVAL, "%s: a workspace of %zu bytes, %zu are needed", who, workspace_bytes, ma_grad_norm_workspace(count));
+    return on_device(who, stream, [&] {
+      double *partial = static_cast<double *>(workspace);
+      int64_t parts = 0;
+      NormTable T;
+      for (int64_t i = 0; i < count;) {
+        int used = 0;
+        T.chunks = 0;
+        for (; i < count && used < kNormTable; ++i) {
+          const ma_tensor &x = tensors[i];
+          if (!x.n) continue;
+          const int64_t chunks = (x.n + kNormChunk - 1) / kNormChunk;   // at most 2^27
+          T.grad[used] = x.grad;
+          T.n[used] = x.g_type == MA_TYPE_BF16 ? -x.n - 1 : x.n;
+          T.first[used++] = T.chunks;
+          T.chunks += (uint32_t)chunks;
+          if (T.chunks > (1u << 30)) { ++i; break; }
+        }
+        if (!used) break;
+        std::fill(T.first + used, T.first + kNormTable, ~0u);
+        const unsigned grid = std::min<unsigned>(T.chunks, kNormGroups);
+        hipLaunchKernelGGL(norm_kernel, dim3(grid), dim3(kThreads), 0, stream, T, partial + parts);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+        parts += grid;
+      }
+      hipLaunchKernelGGL(norm_finish_kernel, dim3(1), dim3(kThreads), 0, stream, partial, parts, max_norm, out, t);
+      return hipGetLastError();
+    });
+  });
+}
+
+int ma_adamw_many_step(int64_t count, const ma_tensor *tensors, const ma_adamw_args *args, float *copy, float *m, float *v,
+                       int64_t state_n, hipStream_t stream) {
+  const char *who = "ma_adamw_many_step";
+  return guarded(who, [&] {
+    if (const int rc = check_step(who, count, tensors, args, copy, state_n)) return rc;
+    if (!count || !state_n) return (int)MA_OK;
+    if (!m || !v || (((uintptr_t)m | (uintptr_t)v) & 15u)) return fail(MA_EINVAL, "%s: null or misaligned moments", who);
+    const StepArgs a = step_args(*args);
+    return on_device(who, stream, [&] {
+      return each_type(count, tensors, copy != nullptr, [&](const Table &T, auto *p, auto *g, auto c) {
+        using P = std::remove_pointer_t<decltype(p)>;
+        using G = std::remove_pointer_t<decltype(g)>;
+        hipLaunchKernelGGL((step_kernel<P, G, decltype(c)::value>), dim3(std::min(T.chunks, kGroups)), dim3(kThreads), 0, stream, T, a,
+                           copy, m, v);
+        return hipGetLastError();
+      });
+    });
+  });
+}
+
+int ma_adamw8_many_step(int64_t count, const ma_tensor *tensors, const ma_adamw_args *args, float *copy, int8_t *cm, uint8_t *cv,
+                        float *sm, float *sr, int64_t state_n, hipStream_t stream) {
+  const char *who = "ma_adamw8_many_step";
+  return guarded(who, [&] {
+    if (const int rc = check_step(who, count, tensors, args, copy, state_n)) return rc;
+    if (!count || !state_n) return (int)MA_OK;
+    if (!cm || !cv || !sm || !sr || (((uintptr_t)cm | (uintptr_t)cv) & 15u) || (((uintptr_t)sm | (uintptr_t)sr) & 3u))
+      return fail(MA_EINVAL, "%s: null or misaligned moments", who);
+    const StepArgs a = step_args(*args);
+    return on_device(who, stream, [&] {
+      return each_type(count, tensors, copy != nullptr, [&](const Table &T, auto *p, auto *g, auto c) {
+        using P = std::remove_pointer_t<decltype(p)>;
+        using G = std::remove_pointer_t<decltype(g)>;
+        hipLaunchKernelGGL((step8_kernel<P, G, decltype(c)::value>), dim3(std::min(T.chunks, kGroups)), dim3(kThreads), 0, stream, T, a,
+                           copy, cm, cv, sm, sr);
+        return hipGetLastError();
+      });
+    });
+  });
+}
+
+int ma_adamw8_many_values(int64_t state_n, const int8_t *cm, const uint8_t *cv, const float *sm, const float *sr, float *m, float *v,
+                          hipStream_t stream) {
+  const char *who = "ma_adamw8_many_values";
+  return guarded(who, [&] {
+    if (state_n < 0 || state_n % kBlock) return fail(MA_EINVAL, "%s: the states' size must be a multiple of %d", who, kBlock);
+    if (state_n > kMost) return fail(MA_EUNSUPPORTED, "%s: states of more than 2^40 elements", who);
+    if (!state_n) return (int)MA_OK;
+    if (!cm || !cv || !sm || !sr || !m || !v || (((uintptr_t)cm | (uintptr_t)cv | (uintptr_t)m | (uintptr_t)v) & 15u) ||
+        (((uintptr_t)sm | (uintptr_t)sr) & 3u))
+      return fail(MA_EINVAL, "%s: null or misaligned pointer", who);
+    return on_device(who, stream, [&] {
+      const unsigned grid = (unsigned)std::min<int64_t>((state_n + kChunk - 1) / kChunk, kGroups);
+      hipLaunchKernelGGL(values8_kernel, dim3(grid), dim3(kThreads), 0, stream, cm, cv, sm, sr, m, v, state_n / kBlock);
+      return hipGetLastError();
+    });
+  });
+}
+
+}  // extern "C"
