@@ -21,12 +21,15 @@ caller, as for any kernel, and kept until its work there is done
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
+import functools
 import math
 
 from . import _lib as _L
-from .muon import _place, _workspace, changed
+from .muon import _place, _workspace
 
+_HERE = contextlib.nullcontext()
 BLOCK = 256   # elements of a tensor that share the scales of their 8-bit moments
 
 
@@ -50,63 +53,31 @@ def views(state, params) -> list:
             for p, a in zip(params, starts(params))]
 
 
-def _dense(t) -> bool:
-    """Whether its elements fill a stretch of memory, in whatever order."""
-    if t.is_contiguous():
-        return True
-    step = 1
-    for s, n in sorted((s, n) for s, n in zip(t.stride(), t.shape) if n > 1):
-        if s != step:
-            return False
-        step *= n
-    return True
+@functools.lru_cache(maxsize=None)
+def _native():
+    """The module that reads lists of tensors (csrc/tensors.cpp)."""
+    import torch  # noqa: F401  its libraries come first
+    try:
+        from . import _tensors
+    except ImportError as e:
+        raise ImportError("_tensors.so is not built; run `python -m memory_compressed_adaptive_amd.build` "
+                          "(or __graft_entry__.build())") from e
+    return _tensors
 
 
-def _like(g, p) -> bool:
-    """Whether gradient and parameter have the same elements in the same places."""
-    if g.shape != p.shape:
-        return False
-    if g.is_contiguous() and p.is_contiguous():
-        return True
-    return g.numel() < 2 or (_dense(g) and all(a == b for a, b, n in zip(g.stride(), p.stride(), p.shape) if n > 1))
+def _sequence(x):
+    return x if isinstance(x, (list, tuple)) else list(x)
 
 
-def _type(t, what: str) -> int:
-    import torch
-    _L.require(t.dtype in (torch.float32, torch.bfloat16), f"{what} must be fp32 or bf16")
-    return _L.MA_TYPE_F32 if t.dtype == torch.float32 else _L.MA_TYPE_BF16
-
-
-def _list(params, grads):
-    """The ma_tensor array of a list, its length, its device and the states' size."""
-    _L.require(len(params) == len(grads), "there must be a gradient, or None, for every parameter")
-    rows = (_L.Tensor * len(params))()
-    device, count, at = None, 0, 0
-    for p, g in zip(params, grads):
-        n = p.numel()
-        if device is None:
-            device = p.device
-            _L.require(p.is_cuda, "parameters must be CUDA tensors")
-        if g is not None:
-            _L.require(p.device == device and g.device == device, "parameters and gradients must be on one device")
-            _L.require(_dense(p), "parameters must be dense")
-            _L.require(_like(g, p), "a gradient must have its parameter's shape and strides")
-            r = rows[count]
-            r.param, r.grad, r.n, r.at = p.data_ptr(), g.data_ptr(), n, at
-            r.p_type, r.g_type = _type(p, "parameters"), _type(g, "gradients")
-            count += 1
-        at += -(-n // BLOCK) * BLOCK
-    return rows, count, device, at
-
-
-def _state(t, what: str, dtypes, size: int, device):
-    _L.require(t.dtype in dtypes and t.is_contiguous() and t.numel() == size and t.device == device,
-               f"{what} must be contiguous {dtypes[0]} of {size} elements on the parameters' device")
+def _state(t, what: str, dtype, size: int, device):
+    if not (t.dtype == dtype and t.is_contiguous() and t.numel() == size and t.device == device):
+        raise ValueError(f"{what} must be contiguous {dtype} of {size} elements on the device of the tensors")
+    return t.data_ptr()
 
 
 def _one(t, what: str, dtype, device):
-    _L.require(t.dtype == dtype and t.numel() == 1 and t.device == device,
-               f"{what} must be one {dtype} on the parameters' device")
+    if not (t.dtype == dtype and t.numel() == 1 and t.device == device):
+        raise ValueError(f"{what} must be one {dtype} on the device of the tensors")
     return t.data_ptr()
 
 
@@ -126,6 +97,16 @@ def _arguments(t, lr, beta1, beta2, eps, wd, scale, device):
     return a
 
 
+def _stream(device, stream):
+    """The handle of the stream to use, and a context for allocations and the call."""
+    if stream is None:
+        handle = _native().stream(device.index)
+        if handle is not None:
+            return handle, _HERE
+    s, place = _place(device, stream)
+    return s.cuda_stream, place
+
+
 def grad_norm(grads, max_norm: float = math.inf, t=None, out=None, stream=None):
     """(norm, scale), two fp32 tensors of one element on the GPU: the norm of all
     gradients (None is passed over), and the factor min(1, max_norm / (norm + 1e-6))
@@ -134,26 +115,21 @@ def grad_norm(grads, max_norm: float = math.inf, t=None, out=None, stream=None):
     count of steps that is raised by one if the norm is finite.  out: fp32 of two
     elements for both."""
     import torch
-    grads = [g for g in grads if g is not None]
-    _L.require(len(grads) > 0 or out is not None, "there must be a gradient, or out")
-    device = out.device if out is not None else grads[0].device
-    _L.require(device.type == "cuda", "gradients must be CUDA tensors")
-    rows = (_L.Tensor * len(grads))()
-    for r, g in zip(rows, grads):
-        _L.require(g.device == device, "gradients must be on one device")
-        _L.require(_dense(g), "gradients must be dense")
-        r.grad, r.n, r.g_type = g.data_ptr(), g.numel(), _type(g, "gradients")
+    rows, count, index = _native().grads(grads)
+    _L.require(count > 0 or out is not None, "there must be a gradient, or out")
+    device = torch.device("cuda", index) if count else out.device
+    _L.require(device.type == "cuda", "out must be a CUDA tensor")
     L = _L.lib()
-    nbytes = L.ma_grad_norm_workspace(len(grads))
-    s, place = _place(device, stream)
+    nbytes = L.ma_grad_norm_workspace(count)
+    s, place = _stream(device, stream)
     with place:
         if out is None:
             out = torch.empty(2, dtype=torch.float32, device=device)
-        _state(out, "out", (torch.float32,), 2, device)
+        to = _state(out, "out", torch.float32, 2, device)
         ws = _workspace(nbytes, device)
-        _L.check(L.ma_grad_norm(len(grads), rows, max_norm, out.data_ptr(), None if t is None else _one(t, "t", torch.int64, device),
-                                ws.data_ptr(), nbytes, s.cuda_stream))
-    changed(out, *(() if t is None else (t,)))
+        _L.check(L.ma_grad_norm(count, rows, max_norm, to, None if t is None else _one(t, "t", torch.int64, device),
+                                ws.data_ptr(), nbytes, s))
+    _native().changed((out, t), (), ())
     return out.unbind()
 
 
@@ -169,29 +145,24 @@ def adamw_step(params, grads, m, v, t, lr=1e-3, beta1: float = 0.9, beta2: float
     copies of the bf16 parameters, which take the step in their place and are
     rounded into them."""
     import torch
-    rows, count, device, size = _list(params, grads)
+    params, grads = _sequence(params), _sequence(grads)
+    rows, count, index, size = _native().rows(params, grads)
     if not count:
         return
-    f32 = (torch.float32,)
-    _state(m, "m", f32, size, device)
-    _state(v, "v", f32, size, device)
-    if master is not None:
-        _state(master, "master", f32, size, device)
+    device = torch.device("cuda", index)
+    state = _state(m, "m", torch.float32, size, device), _state(v, "v", torch.float32, size, device)
+    copy = None if master is None else _state(master, "master", torch.float32, size, device)
     a = _arguments(t, lr, beta1, beta2, eps, wd, scale, device)
-    s, place = _place(device, stream)
+    s, place = _stream(device, stream)
     with place:
-        _L.check(_L.lib().ma_adamw_many_step(count, rows, C.byref(a), None if master is None else master.data_ptr(), m.data_ptr(),
-                                             v.data_ptr(), size, s.cuda_stream))
-    changed(m, v, *(() if master is None else (master,)), *(p for p, g in zip(params, grads) if g is not None))
+        _L.check(_L.lib().ma_adamw_many_step(count, rows, C.byref(a), copy, *state, size, s))
+    _native().changed((m, v, master), params, grads)
 
 
 def _moments8(cm, cv, sm, sr, size, device):
     import torch
-    _state(cm, "cm", (torch.int8,), size, device)
-    _state(cv, "cv", (torch.uint8,), size, device)
-    _state(sm, "sm", (torch.float32,), size // BLOCK, device)
-    _state(sr, "sr", (torch.float32,), size // BLOCK, device)
-    return cm.data_ptr(), cv.data_ptr(), sm.data_ptr(), sr.data_ptr()
+    return (_state(cm, "cm", torch.int8, size, device), _state(cv, "cv", torch.uint8, size, device),
+            _state(sm, "sm", torch.float32, size // BLOCK, device), _state(sr, "sr", torch.float32, size // BLOCK, device))
 
 
 def adamw8_step(params, grads, cm, cv, sm, sr, t, lr=1e-3, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
@@ -200,18 +171,18 @@ def adamw8_step(params, grads, cm, cv, sm, sr, t, lr=1e-3, beta1: float = 0.9, b
     state_size(params) elements, sm and sr fp32 scales of one for 256 of them,
     updated in place, all zeros before the first step."""
     import torch
-    rows, count, device, size = _list(params, grads)
+    params, grads = _sequence(params), _sequence(grads)
+    rows, count, index, size = _native().rows(params, grads)
     if not count:
         return
+    device = torch.device("cuda", index)
     state = _moments8(cm, cv, sm, sr, size, device)
-    if master is not None:
-        _state(master, "master", (torch.float32,), size, device)
+    copy = None if master is None else _state(master, "master", torch.float32, size, device)
     a = _arguments(t, lr, beta1, beta2, eps, wd, scale, device)
-    s, place = _place(device, stream)
+    s, place = _stream(device, stream)
     with place:
-        _L.check(_L.lib().ma_adamw8_many_step(count, rows, C.byref(a), None if master is None else master.data_ptr(), *state, size,
-                                              s.cuda_stream))
-    changed(cm, cv, sm, sr, *(() if master is None else (master,)), *(p for p, g in zip(params, grads) if g is not None))
+        _L.check(_L.lib().ma_adamw8_many_step(count, rows, C.byref(a), copy, *state, size, s))
+    _native().changed((cm, cv, sm, sr, master), params, grads)
 
 
 def adamw8_values(cm, cv, sm, sr, stream=None):
@@ -221,8 +192,8 @@ def adamw8_values(cm, cv, sm, sr, stream=None):
     _L.require(cm.is_cuda, "cm must be a CUDA tensor")
     _L.require(size % BLOCK == 0, f"cm must have a multiple of {BLOCK} elements")
     state = _moments8(cm, cv, sm, sr, size, device)
-    s, place = _place(device, stream)
+    s, place = _stream(device, stream)
     with place:
         m, v = (torch.empty(size, dtype=torch.float32, device=device) for _ in range(2))
-        _L.check(_L.lib().ma_adamw8_many_values(size, *state, m.data_ptr(), v.data_ptr(), s.cuda_stream))
+        _L.check(_L.lib().ma_adamw8_many_values(size, *state, m.data_ptr(), v.data_ptr(), s))
     return m, v

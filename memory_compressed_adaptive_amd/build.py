@@ -4,6 +4,8 @@
 
 libmicroadam.so  -- the MicroAdam step, the Muon operators and AdamW over
                     many tensors (C ABI in include/microadam.h)
+_tensors.so      -- reads lists of torch tensors into the arrays of the calls that
+                    take many (host code, built against torch's headers)
 libmasynth.so    -- the seeded synthetic-input generator used by the benchmark
                     and the tests (no optimizer arithmetic in it)
 
@@ -16,6 +18,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
@@ -43,13 +46,29 @@ TARGETS = {
 }
 
 
+EXTENSION = "_tensors.so"
+
+
+def _extension_command(dst: str) -> list[str]:
+    """Host code only."""
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    include = [sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(HIPCC)), "include"),
+               *cpp_extension.include_paths()]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+            "-D__HIP_PLATFORM_AMD__=1", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-I{INCLUDE}",
+            *(x for d in include for x in ("-isystem", d)), os.path.join(CSRC, "tensors.cpp"), "-o", dst,
+            f"-L{lib}", "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"]
+
+
 def _run(cmd: list[str], what: str, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError(f"hipcc failed for {what}")
+        raise RuntimeError(f"{os.path.basename(cmd[0])} failed for {what}")
     if verbose and r.stderr.strip():
         # hipcc's host pass does not know the packed-fp32 feature; harmless
         lines = [ln for ln in r.stderr.splitlines() if "packed-fp32-ops" not in ln]
@@ -64,6 +83,11 @@ def build(verbose: bool = False, only: str | None = None) -> list[str]:
     with tempfile.TemporaryDirectory() as tmpdir, ThreadPoolExecutor() as pool:
         obj = {src: os.path.join(tmpdir, os.path.basename(src) + ".o") for srcs in targets.values() for src in srcs}
         jobs = [pool.submit(_run, [HIPCC, *COMMON, "-c", src, "-o", o], src, verbose) for src, o in obj.items()]
+        if not only or only == EXTENSION:
+            dst = os.path.join(PKG, EXTENSION)
+            _run(_extension_command(dst + ".tmp"), EXTENSION, verbose)
+            os.replace(dst + ".tmp", dst)
+            out.append(dst)
         for job in jobs:
             job.result()
         for name, srcs in targets.items():

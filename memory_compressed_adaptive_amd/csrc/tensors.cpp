@@ -1,0 +1,172 @@
+// Reads lists of torch tensors into the ma_tensor array of a call (include/microadam.h),
+// with the checks of the Python front, and finds the current stream.  In Python the former
+// takes 1.5 us for a tensor and its gradient, here 0.02: a call on 120 vectors spent 180 us on
+// the host for 7 on the GPU.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <ATen/core/Tensor.h>
+#include <c10/hip/HIPFunctions.h>
+#include <c10/hip/HIPStream.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <exception>
+
+#include "microadam.h"
+
+namespace {
+
+constexpr int64_t kBlock = 256;   // elements of a tensor that share a block of the states
+
+struct Ref {   // owned
+  PyObject *o;
+  explicit Ref(PyObject *p) : o(p) {}
+  Ref(const Ref &) = delete;
+  Ref &operator=(const Ref &) = delete;
+  ~Ref() { Py_XDECREF(o); }
+};
+
+struct Refused {   // what becomes a ValueError
+  const char *what;
+};
+
+PyObject **items(const Ref &list) { return PySequence_Fast_ITEMS(list.o); }
+
+const at::Tensor &tensor(PyObject *o, const char *otherwise) {
+  if (!THPVariable_Check(o)) throw Refused{otherwise};
+  return THPVariable_Unpack(o);
+}
+
+int type_of(const at::Tensor &t, const char *otherwise) {
+  if (t.scalar_type() == at::kFloat) return MA_TYPE_F32;
+  if (t.scalar_type() == at::kBFloat16) return MA_TYPE_BF16;
+  throw Refused{otherwise};
+}
+
+// Whether its elements fill a stretch of memory, in whatever order, and mean what they are.
+bool dense(const at::Tensor &t) { return t.layout() == at::kStrided && !t.is_neg() && (t.is_contiguous() || t.is_non_overlapping_and_dense()); }
+
+// Whether gradient and parameter, both dense, have the same elements in the same places.
+bool like(const at::Tensor &g, const at::Tensor &p) {
+  if (g.sizes() != p.sizes()) return false;
+  if (g.numel() < 2 || (g.is_contiguous() && p.is_contiguous())) return true;
+  for (int64_t d = 0; d < p.dim(); ++d)
+    if (p.size(d) > 1 && g.stride(d) != p.stride(d)) return false;
+  return true;
+}
+
+template <class F> PyObject *guarded(F f) {
+  try {
+    return f();
+  } catch (const Refused &r) {
+    PyErr_SetString(PyExc_ValueError, r.what);
+  } catch (const std::exception &e) {
+    PyErr_SetString(PyExc_RuntimeError, e.what());
+  }
+  return nullptr;
+}
+
+ma_tensor *rows_of(PyObject *bytes) { return reinterpret_cast<ma_tensor *>(PyBytes_AS_STRING(bytes)); }
+
+// rows(params, grads) -> (ma_tensor array, how many, device, elements of the states)
+PyObject *rows(PyObject *, PyObject *args) {
+  PyObject *a, *b;
+  if (!PyArg_ParseTuple(args, "OO", &a, &b)) return nullptr;
+  const Ref ps(PySequence_Fast(a, "parameters must be a sequence of tensors"));
+  if (!ps.o) return nullptr;
+  const Ref gs(PySequence_Fast(b, "gradients must be a sequence of tensors"));
+  if (!gs.o) return nullptr;
+  return guarded([&]() -> PyObject * {
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(ps.o);
+    if (n != PySequence_Fast_GET_SIZE(gs.o)) throw Refused{"there must be a gradient, or None, for every parameter"};
+    const Ref out(PyBytes_FromStringAndSize(nullptr, n * (Py_ssize_t)sizeof(ma_tensor)));
+    if (!out.o) return nullptr;
+    ma_tensor *r = rows_of(out.o);
+    long long count = 0, at = 0;
+    int device = -1;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      const at::Tensor &p = tensor(items(ps)[i], "parameters must be tensors");
+      if (!p.is_cuda()) throw Refused{"parameters must be CUDA tensors"};
+      if (device < 0) device = p.get_device();
+      if (p.get_device() != device) throw Refused{"parameters and gradients must be on one device"};
+      if (items(gs)[i] != Py_None) {
+        const at::Tensor &g = tensor(items(gs)[i], "gradients must be tensors or None");
+        if (!g.is_cuda() || g.get_device() != device) throw Refused{"parameters and gradients must be on one device"};
+        if (!dense(p)) throw Refused{"parameters must be dense"};
+        if (!dense(g) || !like(g, p)) throw Refused{"a gradient must have its parameter's shape and strides"};
+        r[count++] = {p.mutable_data_ptr(), g.const_data_ptr(), p.numel(), at, type_of(p, "parameters must be fp32 or bf16"),
+                      type_of(g, "gradients must be fp32 or bf16")};
+      }
+      at += (p.numel() + kBlock - 1) / kBlock * kBlock;
+    }
+    return Py_BuildValue("OLiL", out.o, count, device, at);
+  });
+}
+
+// grads(list) -> (ma_tensor array, how many, device or -1); None is passed over
+PyObject *grads(PyObject *, PyObject *arg) {
+  const Ref gs(PySequence_Fast(arg, "gradients must be a sequence of tensors"));
+  if (!gs.o) return nullptr;
+  return guarded([&]() -> PyObject * {
+    const Py_ssize_t n = PySequence_Fast_GET_SIZE(gs.o);
+    const Ref out(PyBytes_FromStringAndSize(nullptr, n * (Py_ssize_t)sizeof(ma_tensor)));
+    if (!out.o) return nullptr;
+    ma_tensor *r = rows_of(out.o);
+    long long count = 0;
+    int device = -1;
+    for (Py_ssize_t i = 0; i < n; ++i) {
+      if (items(gs)[i] == Py_None) continue;
+      const at::Tensor &g = tensor(items(gs)[i], "gradients must be tensors or None");
+      if (!g.is_cuda()) throw Refused{"gradients must be CUDA tensors"};
+      if (device < 0) device = g.get_device();
+      if (g.get_device() != device) throw Refused{"gradients must be on one device"};
+      if (!dense(g)) throw Refused{"gradients must be dense"};
+      r[count++] = {nullptr, g.const_data_ptr(), g.numel(), 0, MA_TYPE_F32, type_of(g, "gradients must be fp32 or bf16")};
+    }
+    return Py_BuildValue("OLi", out.o, count, device);
+  });
+}
+
+// changed(states, params, grads): tells autograd that a call has written the states (None is
+// passed over) and the parameters with gradients
+PyObject *changed(PyObject *, PyObject *args) {
+  PyObject *c, *a, *b;
+  if (!PyArg_ParseTuple(args, "OOO", &c, &a, &b)) return nullptr;
+  const Ref ss(PySequence_Fast(c, "a sequence"));
+  if (!ss.o) return nullptr;
+  const Ref ps(PySequence_Fast(a, "a sequence"));
+  if (!ps.o) return nullptr;
+  const Ref gs(PySequence_Fast(b, "a sequence"));
+  if (!gs.o) return nullptr;
+  return guarded([&]() -> PyObject * {
+    const auto bump = [](const at::Tensor &t) {
+      if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+    };
+    for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(ss.o); ++i)
+      if (items(ss)[i] != Py_None) bump(tensor(items(ss)[i], "a tensor"));
+    for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(ps.o) && i < PySequence_Fast_GET_SIZE(gs.o); ++i)
+      if (items(gs)[i] != Py_None) bump(tensor(items(ps)[i], "a tensor"));
+    Py_RETURN_NONE;
+  });
+}
+
+// stream(device) -> the current stream's handle; None if another device is the current one
+PyObject *stream(PyObject *, PyObject *arg) {
+  const long device = PyLong_AsLong(arg);
+  if (device == -1 && PyErr_Occurred()) return nullptr;
+  return guarded([&]() -> PyObject * {
+    if (c10::hip::current_device() != device) Py_RETURN_NONE;
+    return PyLong_FromVoidPtr(c10::hip::getCurrentHIPStream((c10::DeviceIndex)device).stream());
+  });
+}
+
+PyMethodDef methods[] = {{"rows", rows, METH_VARARGS, nullptr},
+                         {"grads", grads, METH_O, nullptr},
+                         {"changed", changed, METH_VARARGS, nullptr},
+                         {"stream", stream, METH_O, nullptr},
+                         {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__tensors(void) { return PyModule_Create(&module); }

@@ -127,17 +127,6 @@ def test_layout_of_a_lists_states():
     assert float(adamw.views(flat, turned)[0][5, 3]) == 3 * 6 + 5
 
 
-def test_dense_tensors_are_told_from_others():
-    x = torch.zeros(4, 6, 5)
-    assert adamw._dense(x) and adamw._dense(x.permute(2, 0, 1)) and adamw._dense(x[1]) and adamw._dense(x[:, :, :1].squeeze(2)[:1, :1])
-    assert not adamw._dense(x[:, ::2]) and not adamw._dense(x[:, :, 1]) and not adamw._dense(torch.zeros(4, 1).expand(4, 6))
-    assert adamw._like(x.t() if x.dim() == 2 else x, x)
-    assert adamw._like(torch.zeros(6, 4).t(), torch.zeros(6, 4).t())
-    assert not adamw._like(torch.zeros(4, 6), torch.zeros(6, 4).t())
-    assert not adamw._like(torch.zeros(4, 6), torch.zeros(6, 4)) and not adamw._like(torch.zeros(24), torch.zeros(4, 6))
-    assert adamw._like(torch.zeros(1, 6).t(), torch.zeros(6, 1))
-
-
 def test_python_checks_need_no_device():
     p, g, s = [torch.zeros(4)], [torch.zeros(4)], torch.zeros(256)
     for call in (lambda: adamw.adamw_step(p, g, s, s, 1), lambda: adamw.adamw_step(p, [], s, s, 1), lambda: adamw.grad_norm(g),

@@ -224,6 +224,37 @@ def test_permuted_parameters(bits):
         fn([base[:, :, ::2]], [g[:, :, ::2]], *c.state, 2)
 
 
+def _moves(p, g):
+    """Whether a step takes this pair: with m = v = 0 each element moves by lr against its gradient's sign."""
+    q, size = p.clone(), adamw.state_size([p])
+    m, v = (torch.zeros(size, device="cuda") for _ in range(2))
+    try:
+        adamw.adamw_step([p], [g], m, v, 1, lr=1.0)
+    except ValueError:
+        return False
+    assert torch.allclose(p, q - g.sign(), atol=1e-5)
+    return True
+
+
+def test_layouts():
+    """Every dense layout is taken where the gradient has it too; others are refused."""
+    f = lambda *s: torch.randn(*s, device="cuda")  # noqa: E731
+    assert _moves(f(4, 6, 5).permute(2, 0, 1), f(4, 6, 5).permute(2, 0, 1))
+    assert _moves(f(2, 3, 4, 5).to(memory_format=torch.channels_last), f(2, 3, 4, 5).to(memory_format=torch.channels_last))
+    assert _moves(f(4, 6)[1], f(6)) and _moves(f(4, 6)[:1, :1], f(1, 1)) and _moves(f(6, 1), f(1, 6).t()) and _moves(f(3, 1, 4), f(3, 4)[:, None])
+    assert _moves(f(1, 6, 1).expand(1, 6, 1), f(1, 6, 1))
+    assert not _moves(f(4, 6), f(6, 4).t()) and not _moves(f(6, 4).t(), f(4, 6)) and not _moves(f(4, 6), f(6, 4)) and not _moves(f(24), f(4, 6))
+    assert not _moves(f(4, 6), f(4, 1).expand(4, 6)) and not _moves(f(4, 6)[:, ::2], f(4, 6)[:, ::2]) and not _moves(f(4, 1).expand(4, 6), f(4, 6))
+    assert not _moves(f(4, 6), f(4, 6).to_sparse()) and not _moves(f(4, 6), torch._neg_view(f(4, 6)))
+    with pytest.raises(ValueError):
+        adamw.grad_norm([f(4, 6)[:, 1]])
+    with pytest.raises(ValueError):
+        adamw.grad_norm([f(4, 1).expand(4, 6)])
+    want = f(3, 4, 5)
+    norm, _ = adamw.grad_norm(iter([want.permute(1, 2, 0), want[0, 0]]))
+    assert float(norm) == pytest.approx(float((want.double().square().sum() + want[0, 0].double().square().sum()).sqrt()), rel=1e-7)
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 def test_the_same_bits_in_other_lists_and_calls(bits):
     """How tensors are put together in lists changes no bit."""
