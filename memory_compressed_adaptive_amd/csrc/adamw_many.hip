@@ -22,7 +22,6 @@ using microadam::fail;
 namespace {
 
 constexpr int64_t kMost = int64_t(1) << 40;   // elements of a tensor, and of a state
-constexpr unsigned kGroups = 256 * 8;         // workgroups of a launch, at most: eight to a CU
 
 bool type_ok(int t) { return t == MA_TYPE_F32 || t == MA_TYPE_BF16; }
 bool misaligned(const void *p, int type) { return ((uintptr_t)p & (type == MA_TYPE_F32 ? 3u : 1u)) != 0; }
@@ -150,7 +149,9 @@ template <class F> hipError_t each_type(int64_t count, const ma_tensor *tensors,
 }
 
 StepArgs step_args(const ma_adamw_args &a) {
-  return {a.lr, a.beta1, a.beta2, a.eps, a.wd, a.t, a.t_dev, a.lr_dev, a.scale};
+  const int64_t n = a.t_dev ? 1 : a.t;
+  return {a.beta1, a.beta2, a.beta1 * (kUp / kM), a.beta2 * (kUp / (kR * kR)), (float)a.lr, (float)a.eps, (float)a.wd, correction1(a.beta1, n), correction2(a.beta2, n),
+          a.t_dev, a.lr_dev, a.scale};
 }
 
 int64_t norm_launches(int64_t count) { return (count + kNormTable - 1) / kNormTable; }
@@ -218,7 +219,7 @@ int ma_adamw_many_step(int64_t count, const ma_tensor *tensors, const ma_adamw_a
       return each_type(count, tensors, copy != nullptr, [&](const Table &T, auto *p, auto *g, auto c) {
         using P = std::remove_pointer_t<decltype(p)>;
         using G = std::remove_pointer_t<decltype(g)>;
-        hipLaunchKernelGGL((step_kernel<P, G, decltype(c)::value>), dim3(std::min(T.chunks, kGroups)), dim3(kThreads), 0, stream, T, a,
+        hipLaunchKernelGGL((step_kernel<P, G, decltype(c)::value>), dim3(T.chunks), dim3(kThreads), 0, stream, T, a,
                            copy, m, v);
         return hipGetLastError();
       });
@@ -239,7 +240,7 @@ int ma_adamw8_many_step(int64_t count, const ma_tensor *tensors, const ma_adamw_
       return each_type(count, tensors, copy != nullptr, [&](const Table &T, auto *p, auto *g, auto c) {
         using P = std::remove_pointer_t<decltype(p)>;
         using G = std::remove_pointer_t<decltype(g)>;
-        hipLaunchKernelGGL((step8_kernel<P, G, decltype(c)::value>), dim3(std::min(T.chunks, kGroups)), dim3(kThreads), 0, stream, T, a,
+        hipLaunchKernelGGL((step8_kernel<P, G, decltype(c)::value>), dim3(T.chunks), dim3(kThreads), 0, stream, T, a,
                            copy, cm, cv, sm, sr);
         return hipGetLastError();
       });
@@ -258,8 +259,7 @@ int ma_adamw8_many_values(int64_t state_n, const int8_t *cm, const uint8_t *cv, 
         (((uintptr_t)sm | (uintptr_t)sr) & 3u))
       return fail(MA_EINVAL, "%s: null or misaligned pointer", who);
     return on_device(who, stream, [&] {
-      const unsigned grid = (unsigned)std::min<int64_t>((state_n + kChunk - 1) / kChunk, kGroups);
-      hipLaunchKernelGGL(values8_kernel, dim3(grid), dim3(kThreads), 0, stream, cm, cv, sm, sr, m, v, state_n / kBlock);
+      hipLaunchKernelGGL(values8_kernel, dim3((unsigned)((state_n + kChunk - 1) / kChunk)), dim3(kThreads), 0, stream, cm, cv, sm, sr, m, v, state_n / kBlock);
       return hipGetLastError();
     });
   });
