@@ -282,8 +282,8 @@ int ma_debug_muon_plan(int64_t batch, int64_t rows, int64_t cols, int64_t *out);
  * (MA_EINVAL) nor anything else of the call; gradients may be the same.  Types
  * may differ from tensor to tensor.  Tensors with n = 0 are passed over.
  *
- * Calls only enqueue work on `stream` (at most one launch for every 112 tensors
- * of one pair of types; ma_grad_norm one for every 184 and one more), allocate
+ * Calls only enqueue work on `stream` (one launch for every 140 tensors of one
+ * pair of types; ma_grad_norm one for every 250 and one more), allocate
  * nothing on the device and can be captured into a HIP graph.  Nothing uses
  * atomics: a call repeats its bits, and how tensors are put together in lists
  * changes none of a step's.

@@ -105,29 +105,32 @@ template <class F> int guarded(const char *who, F f) {
   }
 }
 
-// launch(table) for every kTable tensors of the list with these types.
+// launch(table) for every kTable entries of the tensors with these types.
 template <class F> hipError_t each_table(int64_t count, const ma_tensor *tensors, int p_type, int g_type, F launch) {
   Table T;
   int used = 0;
+  T.chunks = 0;
   const auto flush = [&] {
     std::fill(T.first + used, T.first + kTable, ~0u);
     const hipError_t e = launch(T);
     used = 0;
+    T.chunks = 0;
     return e;
   };
-  T.chunks = 0;
   for (int64_t i = 0; i < count; ++i) {
     const ma_tensor &t = tensors[i];
-    if (!t.n || t.p_type != p_type || t.g_type != g_type) continue;
-    if (!used) T.chunks = 0;
-    T.param[used] = t.param;
-    T.grad[used] = t.grad;
-    T.n[used] = t.n;
-    T.block[used] = (uint32_t)(t.at / kBlock);
-    T.first[used] = T.chunks;
-    T.chunks += (uint32_t)((t.n + kChunk - 1) / kChunk);   // at most 2^29 in all: the states have 2^40 elements
-    if (++used == kTable)
-      if (const hipError_t e = flush(); e != hipSuccess) return e;
+    if (t.p_type != p_type || t.g_type != g_type) continue;
+    for (int64_t from = 0; from < t.n; from += kEntry) {
+      const int64_t n = std::min(t.n - from, kEntry);
+      T.param[used] = static_cast<char *>(t.param) + from * size_of(p_type);
+      T.grad[used] = static_cast<const char *>(t.grad) + from * size_of(g_type);
+      T.n[used] = (uint32_t)n;
+      T.block[used] = (uint32_t)((t.at + from) / kBlock);
+      T.first[used] = T.chunks;
+      T.chunks += (uint32_t)((n + kChunk - 1) / kChunk);   // at most 2^19 each
+      if (++used == kTable)
+        if (const hipError_t e = flush(); e != hipSuccess) return e;
+    }
   }
   return used ? flush() : hipSuccess;
 }
@@ -154,15 +157,39 @@ StepArgs step_args(const ma_adamw_args &a) {
           a.t_dev, a.lr_dev, a.scale};
 }
 
-int64_t norm_launches(int64_t count) { return (count + kNormTable - 1) / kNormTable; }
+// launch(table) for every kNormTable entries.
+template <class F> hipError_t each_norm_table(int64_t count, const ma_tensor *tensors, F launch) {
+  NormTable T;
+  int used = 0;
+  T.chunks = 0;
+  const auto flush = [&] {
+    std::fill(T.first + used, T.first + kNormTable, ~0u);
+    const hipError_t e = launch(T);
+    used = 0;
+    T.chunks = 0;
+    return e;
+  };
+  for (int64_t i = 0; i < count; ++i) {
+    const ma_tensor &t = tensors[i];
+    for (int64_t from = 0; from < t.n; from += kEntry) {
+      const int64_t n = std::min(t.n - from, kEntry);
+      T.grad[used] = static_cast<const char *>(t.grad) + from * size_of(t.g_type);
+      T.n[used] = (uint32_t)n | (t.g_type == MA_TYPE_BF16 ? kIsBf16 : 0u);
+      T.first[used] = T.chunks;
+      T.chunks += (uint32_t)((n + kNormChunk - 1) / kNormChunk);
+      if (++used == kNormTable)
+        if (const hipError_t e = flush(); e != hipSuccess) return e;
+    }
+  }
+  return used ? flush() : hipSuccess;
+}
 
 }  // namespace
 
 extern "C" {
 
 size_t ma_grad_norm_workspace(int64_t count) {
-  if (count <= 0 || count > (int64_t(1) << 40)) return 0;
-  return (size_t)norm_launches(count) * kNormGroups * sizeof(double);
+  return count > 0 ? kNormGroups * sizeof(double) : 0;
 }
 
 int ma_grad_norm(int64_t count, const ma_tensor *tensors, double max_norm, float *out, int64_t *t, void *workspace,
@@ -179,28 +206,14 @@ int ma_grad_norm(int64_t count, const ma_tensor *tensors, double max_norm, float
       return fail(MA_EINVAL, "%s: a workspace of %zu bytes, %zu are needed", who, workspace_bytes, ma_grad_norm_workspace(count));
     return on_device(who, stream, [&] {
       double *partial = static_cast<double *>(workspace);
-      int64_t parts = 0;
-      NormTable T;
-      for (int64_t i = 0; i < count;) {
-        int used = 0;
-        T.chunks = 0;
-        for (; i < count && used < kNormTable; ++i) {
-          const ma_tensor &x = tensors[i];
-          if (!x.n) continue;
-          const int64_t chunks = (x.n + kNormChunk - 1) / kNormChunk;   // at most 2^27
-          T.grad[used] = x.grad;
-          T.n[used] = x.g_type == MA_TYPE_BF16 ? -x.n - 1 : x.n;
-          T.first[used++] = T.chunks;
-          T.chunks += (uint32_t)chunks;
-          if (T.chunks > (1u << 30)) { ++i; break; }
-        }
-        if (!used) break;
-        std::fill(T.first + used, T.first + kNormTable, ~0u);
-        const unsigned grid = std::min<unsigned>(T.chunks, kNormGroups);
-        hipLaunchKernelGGL(norm_kernel, dim3(grid), dim3(kThreads), 0, stream, T, partial + parts);
-        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-        parts += grid;
-      }
+      int parts = 0;   // sums in `partial` so far: a launch adds to them, and may add more of them
+      const hipError_t e = each_norm_table(count, tensors, [&](const NormTable &T) {
+        const int grid = (int)std::min<uint32_t>(T.chunks, kNormGroups);
+        hipLaunchKernelGGL(norm_kernel, dim3(grid), dim3(kThreads), 0, stream, T, partial, parts);
+        parts = std::max(parts, grid);
+        return hipGetLastError();
+      });
+      if (e != hipSuccess) return e;
       hipLaunchKernelGGL(norm_finish_kernel, dim3(1), dim3(kThreads), 0, stream, partial, parts, max_norm, out, t);
       return hipGetLastError();
     });

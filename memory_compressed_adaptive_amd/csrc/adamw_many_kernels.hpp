@@ -18,23 +18,26 @@ constexpr int kThreads = 256;
 constexpr double kM = 127.0 * 127.0, kR = 255.0 * 255.0;   // what the largest 8-bit codes stand for, in units of the smallest
 constexpr int kRun = 8;          // consecutive elements of a thread
 constexpr int kChunk = kThreads * kRun;
-constexpr int kTable = 112;      // tensors of a launch: its arguments stay below 4 KiB
-constexpr int kNormTable = 184;
-constexpr int kNormChunk = 4 * kChunk;
-constexpr int kNormGroups = 1024;   // partial sums of a launch, at most
+constexpr int kTable = 140;      // tensors of a launch: as many as its 4 KiB of arguments hold
+constexpr int kNormTable = 250;
+constexpr int64_t kEntry = int64_t(1) << 30;   // elements of an entry: a longer tensor takes several
+constexpr int kNormRuns = 4, kNormChunk = kNormRuns * kChunk;
+constexpr int kNormGroups = 512;   // workgroups of a launch, at most: two to a CU
 
 struct Table {
   void *param[kTable];
   const void *grad[kTable];
-  int64_t n[kTable];
+  uint32_t n[kTable];
   uint32_t block[kTable];   // first block of its states
   uint32_t first[kTable];   // first chunk; 2^32 - 1 past the last tensor
   uint32_t chunks;
 };
 
+constexpr uint32_t kIsBf16 = 1u << 31;
+
 struct NormTable {
   const void *grad[kNormTable];
-  int64_t n[kNormTable];      // negative: bf16, -n - 1 elements
+  uint32_t n[kNormTable];   // with kIsBf16 where it is
   uint32_t first[kNormTable];
   uint32_t chunks;
 };
@@ -179,7 +182,7 @@ __global__ __launch_bounds__(kThreads) void step_kernel(Table T, StepArgs A, flo
   // where the chunk begins is the same in all lanes, what a lane adds the same in all chunks
   const int64_t from = (int64_t)(c - T.first[i]) * kChunk;
   const uint32_t o = threadIdx.x * kRun;
-  const int left = (int)min(T.n[i] - from, (int64_t)kChunk) - (int)o;
+  const int left = (int)min((int64_t)T.n[i] - from, (int64_t)kChunk) - (int)o;
   if (left <= 0) return;
   const int64_t state = (int64_t)T.block[i] * kBlock + from;
   float g[kRun], p[kRun], m[kRun], v[kRun];
@@ -323,7 +326,7 @@ __global__ __launch_bounds__(kThreads, 5) void step8_kernel(Table T, StepArgs A,
   const int i = Finder<kTable>(T.first)(c);
   const int64_t from = (int64_t)(c - T.first[i]) * kChunk, block = T.block[i] + from / kBlock, state = block * kBlock;
   const uint32_t o = threadIdx.x * kRun, b = threadIdx.x / kLanes;
-  const int rest = (int)min(T.n[i] - from, (int64_t)kChunk), left = rest - (int)o;
+  const int rest = (int)min((int64_t)T.n[i] - from, (int64_t)kChunk), left = rest - (int)o;
   if ((int)(b * kBlock) >= rest) return;   // a block's lanes together
   const void *const grad = T.grad[i];
   void *const param = T.param[i];
@@ -480,36 +483,55 @@ __device__ __forceinline__ double group_sum(double x, double *lds) {
   return s;
 }
 
-template <class G> __device__ __forceinline__ double squares(const void *grad, int64_t at, int64_t n) {
-  const auto g = (const Device<G> *)(const G *)grad;
-  double s = 0.0;
-  for (int64_t e = at + threadIdx.x * kRun; e < at + kNormChunk && e < n; e += kChunk) {
-    float x[kRun];
-    if (n - e >= kRun) load(g + e, x); else load(g + e, (int)(n - e), x);
+// A workgroup takes chunks of kNormChunk elements in turn, kNormRuns runs of a thread at once: it
+// only reads, so what counts is how many loads are on their way.  809 million bf16 gradients:
+// 346 us with one load of a thread at a time (1024 groups); with four, 253 (6.4 TB/s) with 512
+// groups, 278 with 384, 263 with 1024, 276 with 8192; with eight 260 with 512, with two 351.
+template <class G> __device__ __forceinline__ double squares(const void *grad, int64_t from, int64_t rest) {
+  const uint32_t o = threadIdx.x * kRun;
+  double s[kNormRuns] = {};
+  if (rest >= kNormChunk) {
+    float x[kNormRuns][kRun];
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) s = fma((double)x[i], (double)x[i], s);
+    for (int r = 0; r < kNormRuns; ++r) load(at<const G>(grad, from + r * kChunk, o), x[r]);
+#pragma unroll
+    for (int i = 0; i < kRun; ++i)
+#pragma unroll
+      for (int r = 0; r < kNormRuns; ++r) s[r] = fma((double)x[r][i], (double)x[r][i], s[r]);
+  } else {
+    for (int r = 0; r < kNormRuns; ++r) {
+      const int left = (int)rest - r * kChunk - (int)o;
+      float x[kRun];
+      if (left >= kRun) load(at<const G>(grad, from + r * kChunk, o), x);
+      else load(at<const G>(grad, from + r * kChunk, o), left, x);
+#pragma unroll
+      for (int i = 0; i < kRun; ++i) s[0] = fma((double)x[i], (double)x[i], s[0]);
+    }
   }
-  return s;
+  double sum = s[0];
+#pragma unroll
+  for (int r = 1; r < kNormRuns; ++r) sum += s[r];
+  return sum;
 }
 
-__global__ __launch_bounds__(kThreads) void norm_kernel(NormTable T, double *partial) {
+__global__ __launch_bounds__(kThreads) void norm_kernel(NormTable T, double *partial, int old) {
   __shared__ double lds[kThreads / 64];
   double s = 0.0;
   const Finder<kNormTable> find(T.first);
   for (uint32_t c = blockIdx.x; c < T.chunks; c += gridDim.x) {
     const int i = find(c);
-    const int64_t n = T.n[i], at = (int64_t)(c - T.first[i]) * kNormChunk;
-    s += n < 0 ? squares<__bf16>(T.grad[i], at, -n - 1) : squares<float>(T.grad[i], at, n);
+    const int64_t from = (int64_t)(c - T.first[i]) * kNormChunk, rest = (int64_t)(T.n[i] & ~kIsBf16) - from;
+    s += T.n[i] & kIsBf16 ? squares<__bf16>(T.grad[i], from, rest) : squares<float>(T.grad[i], from, rest);
   }
   s = group_sum(s, lds);
-  if (threadIdx.x == 0) partial[blockIdx.x] = s;
+  if (threadIdx.x == 0) partial[blockIdx.x] = (int)blockIdx.x < old ? partial[blockIdx.x] + s : s;
 }
 
-__global__ __launch_bounds__(kThreads) void norm_finish_kernel(const double *partial, int64_t parts, double max_norm, float *out,
+__global__ __launch_bounds__(kThreads) void norm_finish_kernel(const double *partial, int parts, double max_norm, float *out,
                                                                int64_t *t) {
   __shared__ double lds[kThreads / 64];
   double s = 0.0;
-  for (int64_t i = threadIdx.x; i < parts; i += kThreads) s += partial[i];
+  for (int i = threadIdx.x; i < parts; i += kThreads) s += partial[i];
   s = group_sum(s, lds);
   if (threadIdx.x == 0) {
     const double norm = sqrt(s);

@@ -102,7 +102,7 @@ def test_norm_refuses_arguments(kw):
 
 def test_norm_workspace():
     ws = L.lib().ma_grad_norm_workspace
-    assert ws(0) == ws(-1) == ws(1 << 50) == 0 and 0 < ws(1) <= 1 << 20 and ws(10000) > ws(1)
+    assert ws(0) == ws(-1) == 0 and 0 < ws(1) <= ws(10000) <= 1 << 20
 
 
 def test_values_refuse():
