@@ -65,6 +65,11 @@ def _native():
     return _tensors
 
 
+def require_dense(params) -> None:
+    """ValueError unless every parameter is one that the steps take."""
+    _native().rows(params, params)
+
+
 def _sequence(x):
     return x if isinstance(x, (list, tuple)) else list(x)
 

@@ -12,12 +12,16 @@ boundaries.  A parameter without a gradient contributes zeros.
 
 Muon, for the matrices of a model, stacks the equally shaped parameters of a
 group in one buffer in the same way, so that one call takes all of them; a
-model's other parameters go to MicroAdamW.
+model's other parameters go to MicroAdamW or AdamW.
+
+AdamW takes parameters of any shape where they lie, all of a group in one call, with
+dense moments in 32 or 8 bits, and can clip by the norm of all gradients.
 """
 from __future__ import annotations
 
 import torch
 
+from . import adamw as _adamw
 from . import muon as _muon
 from .optimizer import MicroAdam as _Handle
 
@@ -235,3 +239,148 @@ def _stacks(group):
             st["momentum"] = torch.zeros(flat.shape, dtype=torch.float32, device=flat.device)
         out.append(st)
     return out
+
+
+class AdamW(torch.optim.Optimizer):
+    """AdamW over parameters where they lie, each group in one call (ma_adamw_many_step,
+    ma_adamw8_many_step), optionally clipped by the norm of all gradients
+    (ma_grad_norm) without waiting for it.
+
+    params: float32 or bfloat16, dense, on one device.  state_bits: 32, or 8 for moments
+    of 2 + 8/256 bytes per parameter.  master_weights: 32-bit copies of the bfloat16
+    parameters, which take the steps in their place; they are made here, of the
+    weights that the parameters have now.  max_norm: clips the gradients of all groups
+    together to this norm; `grad_norm` is then the last step's, as a tensor on the
+    GPU, and a step whose norm is not finite changes nothing and is not counted.
+
+    lr, betas, eps and weight_decay may be changed between steps; lr may be a
+    float32 tensor of one element on the GPU, which a captured step reads at
+    every replay.  The count of steps is one for all groups and is kept on the GPU.
+    A parameter without a gradient is left alone, its moments too.  Gradients are
+    float32 or bfloat16 as they are; others, and ones that lie unlike their
+    parameter, are copied first.
+    """
+
+    def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, state_bits=32, master_weights=False,
+                 max_norm=None):
+        if max_norm is not None and not max_norm > 0:
+            raise ValueError("max_norm must be positive")
+        self.max_norm, self.grad_norm, self._count = max_norm, None, None
+        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits,
+                                      master_weights=master_weights))
+
+    def add_param_group(self, param_group):
+        super().add_param_group(param_group)
+        group = self.param_groups[-1]
+        try:
+            group["_moments"] = _moments(group, self.param_groups[0])
+            if self._count is None and group["params"]:
+                self._count = torch.zeros(1, dtype=torch.int64, device=group["params"][0].device)
+        except BaseException:   # memory that runs out too
+            self.param_groups.pop()
+            raise
+
+    @torch.no_grad()
+    def step(self, closure=None, scale=None):
+        """scale: a factor of all gradients instead of max_norm's, a float32 tensor of one
+        element on the GPU (adamw.grad_norm's of more gradients than these); where it is
+        NaN the step changes nothing and is not counted."""
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        if scale is not None and self.max_norm is not None:
+            raise ValueError("a step takes scale or max_norm, not both")
+        for group in self.param_groups:
+            if _layout(group["params"]) != group["_moments"]["layout"]:
+                raise RuntimeError("a parameter was converted or laid out anew after it was given to AdamW, whose moments "
+                                   "lie like it: make the optimizer afterwards")
+        grads = [[None if p.grad is None else _like(p.grad, p) for p in group["params"]] for group in self.param_groups]
+        if all(g is None for gs in grads for g in gs):
+            return loss
+        if self.max_norm is not None:
+            self.grad_norm, scale = _adamw.grad_norm([g for gs in grads for g in gs], self.max_norm, t=self._count)
+        elif scale is not None:
+            self._count.add_(scale == scale)
+        else:
+            self._count.add_(1)
+        for group, gs in zip(self.param_groups, grads):
+            st, (b1, b2) = group["_moments"], group["betas"]
+            kw = dict(lr=group["lr"], beta1=b1, beta2=b2, eps=group["eps"], wd=group["weight_decay"], scale=scale,
+                      master=st.get("master"))
+            if "cm" in st:
+                _adamw.adamw8_step(group["params"], gs, st["cm"], st["cv"], st["sm"], st["sr"], self._count, **kw)
+            else:
+                _adamw.adamw_step(group["params"], gs, st["m"], st["v"], self._count, **kw)
+        return loss
+
+    def state_dict(self):
+        """The usual dictionary, and under "adamw" the count and every group's moments as they are."""
+        sd = super().state_dict()
+        sd["adamw"] = dict(count=0 if self._count is None else int(self._count),
+                           groups=[{k: v.clone() if torch.is_tensor(v) else v for k, v in g["_moments"].items()}
+                                   for g in self.param_groups])
+        for g in sd["param_groups"]:
+            g.pop("_moments", None)
+        return sd
+
+    def load_state_dict(self, state_dict):
+        saved, mine = state_dict["adamw"], [g["_moments"] for g in self.param_groups]
+        same = len(saved["groups"]) == len(mine) and all(
+            a.keys() == b.keys() and [tuple(map(tuple, x[:2])) for x in a["layout"]] == [x[:2] for x in b["layout"]]
+            for a, b in zip(saved["groups"], mine))
+        if not same:
+            raise ValueError("the saved moments are those of other parameters, layouts, state_bits or master_weights")
+        super().load_state_dict({"state": state_dict["state"], "param_groups": [dict(g) for g in state_dict["param_groups"]]})
+        for g, st, new in zip(self.param_groups, mine, saved["groups"]):
+            g["_moments"] = st
+            for k, v in new.items():
+                if torch.is_tensor(v):
+                    st[k].copy_(v)
+        if self._count is not None:
+            self._count.fill_(saved["count"])
+
+
+def _layout(params):
+    return [(tuple(p.shape), p.stride(), p.dtype) for p in params]
+
+
+def _like(g, p):
+    """The gradient in a type and layout that the step takes."""
+    if g.is_sparse:
+        raise ValueError("AdamW does not take sparse gradients")
+    dtype = g.dtype if g.dtype in (torch.float32, torch.bfloat16) else torch.float32
+    if dtype == g.dtype and (g.stride() == p.stride() or g.numel() < 2 or (g.is_contiguous() and p.is_contiguous())):
+        return g
+    return torch.empty_like(p, dtype=dtype, memory_format=torch.preserve_format).copy_(g)
+
+
+def _moments(group, first):
+    """A group's moments, and the 32-bit copies of its bfloat16 parameters."""
+    ps = group["params"]
+    if group["state_bits"] not in (8, 32):
+        raise ValueError("state_bits must be 32 or 8")
+    if len(set(map(id, ps))) < len(ps):
+        raise ValueError("a parameter appears twice in a group")
+    for p in ps:
+        if p.device.type != "cuda":
+            raise ValueError("AdamW needs CUDA (HIP) parameters")
+        if p.dtype not in (torch.float32, torch.bfloat16):
+            raise ValueError("parameters must be float32 or bfloat16")
+        if p.device != (first["params"] or ps)[0].device:
+            raise ValueError("the parameters must share a device")
+    st = {"layout": _layout(ps)}
+    if not ps:
+        return st
+    size, device = _adamw.state_size(ps), ps[0].device
+    _adamw.require_dense(ps)
+    zeros = lambda n, dtype=torch.float32: torch.zeros(n, dtype=dtype, device=device)  # noqa: E731
+    if group["state_bits"] == 8:
+        st.update(cm=zeros(size, torch.int8), cv=zeros(size, torch.uint8), sm=zeros(size // _adamw.BLOCK), sr=zeros(size // _adamw.BLOCK))
+    else:
+        st.update(m=zeros(size), v=zeros(size))
+    if group["master_weights"] and any(p.dtype == torch.bfloat16 for p in ps):
+        st["master"] = zeros(size)
+        for view, p in zip(_adamw.views(st["master"], ps), ps):
+            view.copy_(p.detach())
+    return st

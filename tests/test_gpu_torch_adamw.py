@@ -1,0 +1,271 @@
+"""torch_optim.AdamW: its steps are those of the operators on the same lists, alone and
+beside Muon and MicroAdamW, clipped and not, captured and not, and its state round-trips."""
+import math
+
+import pytest
+import torch
+
+from gpu_harness import say
+from memory_compressed_adaptive_amd import adamw
+from memory_compressed_adaptive_amd.torch_optim import AdamW, MicroAdamW, Muon
+
+pytestmark = pytest.mark.gpu
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+SHAPES = [(40, 70), (1,), (300,), (3, 20, 90), (513,)]
+
+
+def _params(seed, dtypes=(F32,)):
+    g = torch.Generator().manual_seed(seed)
+    return [torch.nn.Parameter((0.02 * torch.randn(s, generator=g)).to(dtypes[i % len(dtypes)]).cuda()) for i, s in enumerate(SHAPES)]
+
+
+def _grads(seed):
+    g = torch.Generator().manual_seed(seed)
+    return [1e-3 * torch.randn(s, generator=g).cuda() for s in SHAPES]
+
+
+class Own:
+    """The operators on a list of their own."""
+
+    def __init__(self, ps, bits, copies):
+        self.ps, n = [p.detach().clone() for p in ps], adamw.state_size(ps)
+        self.master = None
+        if copies and any(p.dtype == BF16 for p in ps):
+            self.master = torch.zeros(n, device="cuda")
+            for v, p in zip(adamw.views(self.master, self.ps), self.ps):
+                v.copy_(p)
+        if bits == 32:
+            self.fn, self.state = adamw.adamw_step, [torch.zeros(n, device="cuda") for _ in range(2)]
+        else:
+            self.fn = adamw.adamw8_step
+            self.state = [torch.zeros(n, dtype=d, device="cuda") for d in (torch.int8, torch.uint8)]
+            self.state += [torch.zeros(n // 256, device="cuda") for _ in range(2)]
+
+    def step(self, gs, t, **kw):
+        self.fn(self.ps, gs, *self.state, t, master=self.master, **kw)
+
+    def same(self, ps):
+        return all(torch.equal(a, b) for a, b in zip(self.ps, ps))
+
+
+@pytest.mark.parametrize("dtypes,copies", [((F32,), False), ((BF16,), False), ((BF16, F32), True)])
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("max_norm", [None, 1e-2])
+def test_steps_are_the_operators(dtypes, copies, bits, max_norm):
+    ps = _params(1, dtypes)
+    own = [Own(ps[:2], bits, copies), Own(ps[2:], bits, copies)]
+    opt = AdamW([{"params": ps[:2]}, {"params": ps[2:], "weight_decay": 0.0}], lr=0.01, betas=(0.8, 0.99), weight_decay=0.1,
+                state_bits=bits, master_weights=copies, max_norm=max_norm)
+    lr = 0.01
+    for t in range(1, 6):
+        gs = [g.to(p.dtype) for g, p in zip(_grads(10 + t), ps)]
+        for i, (p, g) in enumerate(zip(ps, gs)):
+            p.grad = None if (t, i) in ((2, 0), (3, 3)) else g
+        if t == 4:
+            lr = 0.003
+            for group in opt.param_groups:
+                group["lr"] = lr
+        say(f"[torch adamw] step {t} {dtypes} bits={bits} max_norm={max_norm}")
+        opt.step()
+        scale = None
+        if max_norm is not None:
+            norm, scale = adamw.grad_norm([p.grad for p in ps], max_norm)
+            assert float(norm) == float(opt.grad_norm) and float(scale) < 1
+        count = torch.tensor([t], device="cuda")
+        own[0].step([p.grad for p in ps[:2]], count, lr=lr, beta1=0.8, beta2=0.99, wd=0.1, scale=scale)
+        own[1].step([p.grad for p in ps[2:]], count, lr=lr, beta1=0.8, beta2=0.99, wd=0.0, scale=scale)
+        assert own[0].same(ps[:2]) and own[1].same(ps[2:]), t
+
+
+def test_32_bits_are_torchs_adamw():
+    """Both differ from the formula by roundings: a few parts in 10^7 of lr a step, and of the parameter."""
+    ps, qs = _params(2), _params(2)
+    a, b = AdamW(ps, lr=1e-2, weight_decay=0.1), torch.optim.AdamW(qs, lr=1e-2, weight_decay=0.1)
+    for t in range(20):
+        for p, q, g in zip(ps, qs, _grads(40 + t)):
+            p.grad, q.grad = g, g.clone()
+        a.step(), b.step()
+        for p, q in zip(ps, qs):
+            assert bool(((p - q).abs() <= (t + 1) * (1e-2 * 40 * 2.0 ** -24 + 4 * 2.0 ** -24 * q.abs())).all()), t
+
+
+@pytest.mark.parametrize("value", [math.inf, math.nan])
+@pytest.mark.parametrize("how", ["max_norm", "scale"])
+def test_a_step_that_is_not_finite_is_not_taken(value, how):
+    ps, qs = _params(3), _params(3)
+    kw = dict(max_norm=1.0) if how == "max_norm" else {}
+    a, b = AdamW(ps, lr=1e-2, **kw), AdamW(qs, lr=1e-2, **kw)
+    for t in range(3):
+        for p, q, g in zip(ps, qs, _grads(50 + t)):
+            p.grad, q.grad = g, g.clone()
+        if t == 1:
+            ps[2].grad[7] = value
+            before = [p.detach().clone() for p in ps]
+        step = (lambda o, xs: o.step()) if how == "max_norm" else \
+            (lambda o, xs: o.step(scale=adamw.grad_norm([x.grad for x in xs], 1.0)[1]))
+        step(a, ps)
+        if t == 1:
+            assert all(torch.equal(p, x) for p, x in zip(ps, before))
+        else:
+            step(b, qs)
+    assert all(torch.equal(p, q) for p, q in zip(ps, qs)) and a.state_dict()["adamw"]["count"] == 2
+
+
+@pytest.mark.parametrize("bits,copies", [(32, False), (32, True), (8, True)])
+def test_state_dict_resume(bits, copies, tmp_path):
+    def run(split):
+        ps = _params(5, (BF16, F32))
+        opt = AdamW(ps, lr=0.01, state_bits=bits, master_weights=copies, max_norm=1e-2)
+        for t in range(6):
+            if t == split:
+                torch.save(opt.state_dict(), tmp_path / "state")
+                sd = torch.load(tmp_path / "state", weights_only=True)
+                ps2 = _params(6, (BF16, F32))
+                for a, b in zip(ps2, ps):
+                    a.data.copy_(b.data)
+                opt = AdamW(ps2, lr=0.5, state_bits=bits, master_weights=copies, max_norm=1e-2)
+                opt.load_state_dict(sd)
+                assert opt.param_groups[0]["lr"] == 0.01
+                ps = ps2
+            for p, g in zip(ps, _grads(20 + t)):
+                p.grad = g.to(p.dtype)
+            opt.step()
+        return ps
+
+    for a, b in zip(run(3), run(-1)):
+        assert torch.equal(a, b)
+
+
+def test_load_refuses_other_moments():
+    a = AdamW(_params(1, (BF16,)))
+    for kw, ps in ((dict(state_bits=8), _params(1, (BF16,))), (dict(master_weights=True), _params(1, (BF16,))), ({}, _params(1)[:2])):
+        with pytest.raises(ValueError, match="saved moments"):
+            AdamW(ps, **kw).load_state_dict(a.state_dict())
+    turned = [torch.nn.Parameter(p.detach().t().clone(memory_format=torch.contiguous_format).t()) if p.dim() == 2 else p for p in _params(1, (BF16,))]
+    with pytest.raises(ValueError, match="saved moments"):
+        AdamW(turned).load_state_dict(a.state_dict())
+
+
+def test_step_refuses_parameters_that_were_converted():
+    ps = _params(9)
+    opt = AdamW(ps)
+    for p, g in zip(ps, _grads(9)):
+        p.grad = g
+    before = ps[1].detach().clone()
+    ps[0].data = ps[0].data.t().contiguous().t()
+    with pytest.raises(RuntimeError, match="laid out anew"):
+        opt.step()
+    assert torch.equal(ps[1].detach(), before)
+    ps[0].data = ps[0].data.contiguous().clone()   # elsewhere, but lying the same: taken
+    opt.step()
+    assert not torch.equal(ps[1].detach(), before)
+
+
+def test_gradients_of_other_layouts():
+    w = torch.nn.Parameter(torch.randn(30, 20, device="cuda").t())
+    q = torch.nn.Parameter(w.detach().contiguous())
+    a, b = AdamW([w]), AdamW([q])
+    for g in (torch.randn(20, 30, device="cuda"), torch.randn(30, 20, device="cuda").t(), torch.ones(20, 1, device="cuda").expand(20, 30)):
+        w.grad, q.grad = g, g
+        a.step(), b.step()
+        assert torch.equal(w, q)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_captured_step_replays_as_eager_ones(bits):
+    ps, qs = _params(7, (BF16, F32)), _params(7, (BF16, F32))
+    lr = [torch.full((1,), 0.01, device="cuda") for _ in range(2)]
+    for p, q, g in zip(ps, qs, _grads(7)):
+        p.grad, q.grad = g.to(p.dtype), g.to(p.dtype)
+    kw = dict(weight_decay=0.1, state_bits=bits, master_weights=True, max_norm=1e-2)
+    captured, eager = AdamW(ps, lr=lr[0], **kw), AdamW(qs, lr=lr[1], **kw)
+    adamw.grad_norm([p.grad for p in ps])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured.step()
+    for t in range(5):
+        for p, q, g in zip(ps, qs, _grads(30 + t)):
+            p.grad.copy_(g)
+            q.grad.copy_(g)
+        for x in lr:
+            x.fill_(0.01 / (t + 1))
+        graph.replay()
+        eager.step()
+        torch.cuda.synchronize()
+        assert float(captured.grad_norm) == float(eager.grad_norm)
+        assert all(torch.equal(p, q) for p, q in zip(ps, qs)), t
+
+
+def test_a_model_trained_by_three_optimizers():
+    """Matrices to Muon, the embedding to AdamW in 8 bits, vectors to MicroAdamW, all clipped by
+    one norm, as a user sets them up; AdamW's update is checked against the operators."""
+    torch.manual_seed(0)
+    emb = torch.nn.Embedding(300, 48).cuda()
+    model = torch.nn.Sequential(torch.nn.Linear(48, 96), torch.nn.Tanh(), torch.nn.Linear(96, 8)).cuda()
+    matrices = [p for p in model.parameters() if p.dim() == 2]
+    vectors = [p for p in model.parameters() if p.dim() == 1]
+    every = [emb.weight, *matrices, *vectors]
+    ad = AdamW([emb.weight], lr=1e-2, state_bits=8)
+    opts = [Muon(matrices, lr=1e-2), MicroAdamW(vectors, lr=1e-3, density=0.05, m=4, block=64)]
+    own = Own([emb.weight], 8, False)
+    x, y = torch.randint(0, 150, (64,), device="cuda"), torch.randn(64, 8, device="cuda")
+    unseen = emb.weight[150:].detach().clone()
+    for t in range(1, 5):
+        for p in every:
+            p.grad = None
+        torch.nn.functional.mse_loss(model(emb(x)), y).backward()
+        norm, scale = adamw.grad_norm([p.grad for p in every], 0.05)
+        assert float(scale) < 1
+        own.step([emb.weight.grad], torch.tensor([t], device="cuda"), lr=1e-2, scale=scale)
+        ad.step(scale=scale)
+        for p in matrices + vectors:
+            p.grad.mul_(scale)
+        for o in opts:
+            o.step()
+        assert own.same([emb.weight]) and all(bool(p.isfinite().all()) for p in every)
+    assert torch.equal(emb.weight[150:].detach(), unseen)
+
+
+def test_added_group_and_refusals():
+    ps = _params(1)
+    opt = AdamW(ps[:2])
+    opt.add_param_group({"params": ps[2:], "lr": 0.02, "state_bits": 8})
+    for p, g in zip(ps, _grads(1)):
+        p.grad = g
+    before = [p.detach().clone() for p in ps]
+    opt.step()
+    assert all(not torch.equal(p, q) for p, q in zip(ps, before))
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        opt.add_param_group({"params": [torch.nn.Parameter(torch.zeros(4, 4, dtype=torch.float16, device="cuda"))]})
+    with pytest.raises(ValueError, match="dense"):
+        opt.add_param_group({"params": [torch.nn.Parameter(torch.zeros(4, 4, device="cuda")[:, ::2])]})
+    assert len(opt.param_groups) == 2
+    with pytest.raises(ValueError, match="not both"):
+        AdamW(_params(1), max_norm=1.0).step(scale=torch.ones(1, device="cuda"))
+    opt.step()
+    loss = opt.step(lambda: torch.tensor(3.0))
+    assert float(loss) == 3.0
+
+
+def test_a_kept_graph_is_not_used_with_new_parameters():
+    torch.manual_seed(0)
+    w, still = (torch.nn.Parameter(torch.randn(40, 40, device="cuda")) for _ in range(2))
+    x = torch.randn(8, 40, device="cuda", requires_grad=True)
+    opt = AdamW([w, still])
+    first, second = (x @ w).sum(), (x @ still).sum()
+    first.backward(retain_graph=True)
+    opt.step()
+    second.backward(retain_graph=True)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        first.backward()
+    still.grad = None
+    (x @ w).sum().backward()
