@@ -157,8 +157,8 @@ StepArgs step_args(const ma_adamw_args &a) {
           a.t_dev, a.lr_dev, a.scale};
 }
 
-// launch(table) for every kNormTable entries.
-template <class F> hipError_t each_norm_table(int64_t count, const ma_tensor *tensors, F launch) {
+// launch(table) for every kNormTable entries, in chunks of CHUNK elements.
+template <int CHUNK, class F> hipError_t each_norm_table(int64_t count, const ma_tensor *tensors, F launch) {
   NormTable T;
   int used = 0;
   T.chunks = 0;
@@ -176,12 +176,22 @@ template <class F> hipError_t each_norm_table(int64_t count, const ma_tensor *te
       T.grad[used] = static_cast<const char *>(t.grad) + from * size_of(t.g_type);
       T.n[used] = (uint32_t)n | (t.g_type == MA_TYPE_BF16 ? kIsBf16 : 0u);
       T.first[used] = T.chunks;
-      T.chunks += (uint32_t)((n + kNormChunk - 1) / kNormChunk);
+      T.chunks += (uint32_t)((n + CHUNK - 1) / CHUNK);
       if (++used == kNormTable)
         if (const hipError_t e = flush(); e != hipSuccess) return e;
     }
   }
   return used ? flush() : hipSuccess;
+}
+
+// Whether one workgroup takes a whole list.
+bool is_small(int64_t count, const ma_tensor *tensors) {
+  int64_t chunks = 0, used = 0;
+  for (int64_t i = 0; i < count && chunks <= kSmallChunks; ++i) {
+    chunks += (tensors[i].n + kSmallChunk - 1) / kSmallChunk;
+    used += tensors[i].n > 0;
+  }
+  return chunks > 0 && chunks <= kSmallChunks && used <= kNormTable;
 }
 
 }  // namespace
@@ -207,7 +217,12 @@ int ma_grad_norm(int64_t count, const ma_tensor *tensors, double max_norm, float
     return on_device(who, stream, [&] {
       double *partial = static_cast<double *>(workspace);
       int parts = 0;   // sums in `partial` so far: a launch adds to them, and may add more of them
-      const hipError_t e = each_norm_table(count, tensors, [&](const NormTable &T) {
+      if (is_small(count, tensors))
+        return each_norm_table<kSmallChunk>(count, tensors, [&](const NormTable &T) {
+          hipLaunchKernelGGL(norm_small_kernel, dim3(1), dim3(kSmallThreads), 0, stream, T, max_norm, out, t);
+          return hipGetLastError();
+        });
+      const hipError_t e = each_norm_table<kNormChunk>(count, tensors, [&](const NormTable &T) {
         const int grid = (int)std::min<uint32_t>(T.chunks, kNormGroups);
         hipLaunchKernelGGL(norm_kernel, dim3(grid), dim3(kThreads), 0, stream, T, partial, parts);
         parts = std::max(parts, grid);
