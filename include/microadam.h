@@ -278,9 +278,10 @@ int ma_debug_muon_plan(int64_t batch, int64_t rows, int64_t cols, int64_t *out);
  * end of the tensor before it; the arrays have state_n elements, a multiple of
  * 256, and begin at multiples of 16 bytes (scales: of 4).  What lies between a
  * tensor's end and the next one's `at` is neither used nor changed.  Parameters
- * and gradients may begin at any element.  Parameters must not overlap each other
- * (MA_EINVAL) nor anything else of the call; gradients may be the same.  Types
- * may differ from tensor to tensor.  Tensors with n = 0 are passed over.
+ * and gradients may begin at any element.  What is written (parameters, states)
+ * must not overlap (MA_EINVAL), nor what is only read overlap it; gradients may be
+ * the same.  Types may differ from tensor to tensor.  Tensors with n = 0 are
+ * passed over.
  *
  * Calls only enqueue work on `stream` (one launch for every 140 tensors of one
  * pair of types; ma_grad_norm one for every 250 and one more, or one alone
@@ -352,7 +353,7 @@ int ma_adamw_many_step(int64_t count, const ma_tensor *tensors, const ma_adamw_a
 int ma_adamw8_many_step(int64_t count, const ma_tensor *tensors, const ma_adamw_args *args, float *copy, int8_t *cm,
                         uint8_t *cv, float *sm, float *sr, int64_t state_n, hipStream_t stream);
 
-/* Reads 8-bit moments: m, v (f32[state_n]), each rounded once. */
+/* Reads 8-bit moments: m, v (f32[state_n], apart from them and each other), each rounded once. */
 int ma_adamw8_many_values(int64_t state_n, const int8_t *cm, const uint8_t *cv, const float *sm, const float *sr, float *m,
                           float *v, hipStream_t stream);
 

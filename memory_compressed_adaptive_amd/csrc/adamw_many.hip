@@ -6,8 +6,9 @@
 
 #include <algorithm>
 #include <cmath>
-#include <new>
-#include <utility>
+#include <exception>
+#include <initializer_list>
+#include <type_traits>
 #include <vector>
 
 #include "adamw_many_kernels.hpp"
@@ -41,8 +42,16 @@ int check_list(const char *who, int64_t count, const ma_tensor *tensors) {
   return MA_OK;
 }
 
-// What a step needs besides: parameters that do not overlap, states in order.
-int check_step(const char *who, int64_t count, const ma_tensor *tensors, const ma_adamw_args *a, const float *copy, int64_t state_n) {
+struct Span {   // of memory that a call writes
+  uintptr_t begin, end;
+  Span(const void *p, uint64_t bytes) : begin((uintptr_t)p), end((uintptr_t)p + bytes) {}
+  bool operator<(const Span &o) const { return begin < o.begin; }
+  bool meets(const Span &o) const { return begin < o.end && o.begin < end; }
+};
+
+// What a step needs besides: states in order, and nothing that is written twice.
+int check_step(const char *who, int64_t count, const ma_tensor *tensors, const ma_adamw_args *a, const float *copy, int64_t state_n,
+               std::initializer_list<Span> states) {
   if (const int rc = check_list(who, count, tensors)) return rc;
   if (!a) return fail(MA_EINVAL, "%s: null arguments", who);
   if (!(a->beta1 >= 0.0 && a->beta1 < 1.0 && a->beta2 >= 0.0 && a->beta2 < 1.0))
@@ -56,7 +65,7 @@ int check_step(const char *who, int64_t count, const ma_tensor *tensors, const m
   if (state_n < 0 || state_n % kBlock) return fail(MA_EINVAL, "%s: the states' size must be a multiple of %d", who, kBlock);
   if (state_n > kMost) return fail(MA_EUNSUPPORTED, "%s: states of more than 2^40 elements", who);
   int64_t end = 0;
-  std::vector<std::pair<uintptr_t, uintptr_t>> spans;
+  std::vector<Span> spans;
   spans.reserve((size_t)count);
   bool sorted = true;
   for (int64_t i = 0; i < count; ++i) {
@@ -69,13 +78,19 @@ int check_step(const char *who, int64_t count, const ma_tensor *tensors, const m
       return fail(MA_EINVAL, "%s: tensor %lld: its states must begin at a multiple of %d behind the last tensor's and end in the arrays",
                   who, (long long)i, kBlock);
     end = t.at + t.n;
-    const uintptr_t p = (uintptr_t)t.param, q = p + (uintptr_t)(t.n * size_of(t.p_type));
-    if (!spans.empty() && p < spans.back().second) sorted = false;
-    spans.emplace_back(p, q);
+    const Span s(t.param, (uint64_t)(t.n * size_of(t.p_type)));
+    if (!spans.empty() && s.begin < spans.back().end) sorted = false;
+    spans.push_back(s);
   }
   if (!sorted) std::sort(spans.begin(), spans.end());
   for (size_t i = 1; i < spans.size(); ++i)
-    if (spans[i].first < spans[i - 1].second) return fail(MA_EINVAL, "%s: two parameters overlap", who);
+    if (spans[i].meets(spans[i - 1])) return fail(MA_EINVAL, "%s: two parameters overlap", who);
+  for (const Span *x = states.begin(); x != states.end(); ++x) {
+    for (const Span *y = states.begin(); y != x; ++y)
+      if (x->meets(*y)) return fail(MA_EINVAL, "%s: two of the states overlap", who);
+    for (const Span &s : spans)
+      if (x->meets(s)) return fail(MA_EINVAL, "%s: a state and a parameter overlap", who);
+  }
   return MA_OK;
 }
 
@@ -100,7 +115,7 @@ template <class F> int guarded(const char *who, F f) {
   clear_error();
   try {
     return f();
-  } catch (const std::bad_alloc &) {
+  } catch (const std::exception &) {   // of the list of parameters
     return fail(MA_ENOMEM, "%s: out of host memory", who);
   }
 }
@@ -239,9 +254,12 @@ int ma_adamw_many_step(int64_t count, const ma_tensor *tensors, const ma_adamw_a
                        int64_t state_n, hipStream_t stream) {
   const char *who = "ma_adamw_many_step";
   return guarded(who, [&] {
-    if (const int rc = check_step(who, count, tensors, args, copy, state_n)) return rc;
+    if (count > 0 && state_n > 0 && (!m || !v || (((uintptr_t)m | (uintptr_t)v) & 15u)))
+      return fail(MA_EINVAL, "%s: null or misaligned moments", who);
+    const uint64_t bytes = 4 * (uint64_t)state_n;
+    if (const int rc = check_step(who, count, tensors, args, copy, state_n, {{copy, copy ? bytes : 0}, {m, bytes}, {v, bytes}}))
+      return rc;
     if (!count || !state_n) return (int)MA_OK;
-    if (!m || !v || (((uintptr_t)m | (uintptr_t)v) & 15u)) return fail(MA_EINVAL, "%s: null or misaligned moments", who);
     const StepArgs a = step_args(*args);
     return on_device(who, stream, [&] {
       return each_type(count, tensors, copy != nullptr, [&](const Table &T, auto *p, auto *g, auto c) {
@@ -259,10 +277,14 @@ int ma_adamw8_many_step(int64_t count, const ma_tensor *tensors, const ma_adamw_
                         float *sm, float *sr, int64_t state_n, hipStream_t stream) {
   const char *who = "ma_adamw8_many_step";
   return guarded(who, [&] {
-    if (const int rc = check_step(who, count, tensors, args, copy, state_n)) return rc;
-    if (!count || !state_n) return (int)MA_OK;
-    if (!cm || !cv || !sm || !sr || (((uintptr_t)cm | (uintptr_t)cv) & 15u) || (((uintptr_t)sm | (uintptr_t)sr) & 3u))
+    if (count > 0 && state_n > 0 &&
+        (!cm || !cv || !sm || !sr || (((uintptr_t)cm | (uintptr_t)cv) & 15u) || (((uintptr_t)sm | (uintptr_t)sr) & 3u)))
       return fail(MA_EINVAL, "%s: null or misaligned moments", who);
+    const uint64_t codes = (uint64_t)state_n, scales = codes / kBlock * 4;
+    if (const int rc = check_step(who, count, tensors, args, copy, state_n,
+                                  {{copy, copy ? 4 * codes : 0}, {cm, codes}, {cv, codes}, {sm, scales}, {sr, scales}}))
+      return rc;
+    if (!count || !state_n) return (int)MA_OK;
     const StepArgs a = step_args(*args);
     return on_device(who, stream, [&] {
       return each_type(count, tensors, copy != nullptr, [&](const Table &T, auto *p, auto *g, auto c) {

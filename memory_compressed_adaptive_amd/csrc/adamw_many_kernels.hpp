@@ -2,10 +2,19 @@
 // with its moments in 32 bits, and the step with its moments in 8 bits.
 //
 // The list travels in the kernel's arguments (no copy to the device, nothing to
-// keep alive, and a captured launch holds its own), cut into chunks that the
-// workgroups take in turn.  State arrays are laid out in blocks of 256 elements,
-// each tensor starting a block, so that they are aligned whatever the
-// parameters are; parameters and gradients may begin at any element.
+// keep alive, and a captured launch holds its own), cut into chunks.  State arrays
+// are laid out in blocks of 256 elements, each tensor starting a block, so that
+// they are aligned whatever the parameters are; parameters and gradients may
+// begin at any element.
+//
+// All of it is bound by memory (14 to 28 bytes an element and some 30 to 60
+// operations), short lists by the launch.  The steps give each workgroup one chunk:
+// in a loop, a wave's next loads would wait for its last stores, which retire in
+// order with them (51.8 million fp32 parameters: 279 us with 2048 workgroups in a
+// loop, 251 with one chunk each, 5.4 TB/s; 405 million bf16 ones with copies 2290
+// and 2130, 5.3 TB/s; a copy of 1 GiB runs at 5.1).  Loads that bypass the caches
+// made the steps 4% slower, such stores 0.5% faster but reading 8-bit moments twice
+// as slow: neither is used.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -173,6 +182,9 @@ template <class T> __device__ __forceinline__ void store(T *p, int left, const f
 __device__ __forceinline__ float moved(const Step &k, float p, float u) { return fmaf(-k.lr, fmaf(k.wd, p, u), p); }
 
 // ------------------------------------------------------------ moments in 32 bits
+// In fp32 throughout, each operation rounded once; 48 registers, eight waves a SIMD.  (Runs
+// of four elements, so that an access covers whole lines, were 8% faster where the list fits
+// the last cache and 2% slower where it does not.)
 
 template <class P, class G, bool COPY>
 __global__ __launch_bounds__(kThreads) void step_kernel(Table T, StepArgs A, float *copies, float *ms, float *vs) {
@@ -229,8 +241,8 @@ __global__ __launch_bounds__(kThreads) void step_kernel(Table T, StepArgs A, flo
 
 // Half of a wave holds a block, a lane eight elements.  (16 lanes with 16 elements each would
 // share the work on maxima and scales better, but took 186 registers, two waves a SIMD:
-// 262 million bf16 parameters in 772 us instead of 651.)  The lanes' neighbours are read
-// without going through LDS.
+// 772 us instead of 651 for 262 million bf16 parameters at that state of the kernel.)  The
+// lanes' neighbours are read without going through LDS.
 constexpr int kLanes = kBlock / kRun;
 constexpr double kUp = 0x1p64, kDown = 0x1p-32;   // factor of m and v, and the inverse of its root
 
@@ -309,12 +321,14 @@ __device__ __forceinline__ uint32_t kept(uint32_t w, int left) {
   return left >= 4 ? w : left <= 0 ? 0u : w & ((1u << (8 * left)) - 1u);
 }
 
-// Bound by instructions, not by memory, if written down plainly: 144 of them an element took
-// 960 us for 262 million bf16 parameters, whose bytes take 510.  So moments are formed in 64
-// bits, which cost the same as 32, but what follows goes by 32-bit estimates of the codes'
-// roots, good to a few parts in 10^7; the one lane in 600 with an element nearer to a border
-// than that decides its codes again in 64 bits.  1/x and roots are the hardware's estimates:
-// the update is off by a few parts in 10^7 of itself.
+// Written down plainly, this is bound by instructions: 960 us for 262 million bf16 parameters,
+// whose bytes take 510 at a copy's rate.  64-bit operations cost what 32-bit ones do (4 cycles a
+// wave; additions and products in 32 bits less), so moments are formed in 64 bits; what follows
+// goes by 32-bit estimates of the codes' roots, good to a few parts in 10^7, and a lane with
+// an element nearer to a border than that (one in 700) decides its codes again in 64 bits.
+// 1/x and roots are the hardware's estimates: the update is off by a few parts in 10^7 of
+// itself.  443 instructions a wave and 8 elements, 89 registers, five waves a SIMD (with four
+// the same time, with six, and registers in memory, 545 us): 502 to 520 us, 5.1 to 5.3 TB/s.
 template <class P, class G, bool COPY>
 __global__ __launch_bounds__(kThreads, 5) void step8_kernel(Table T, StepArgs A, float *copies, int8_t *cm, uint8_t *cv, float *sm,
                                                             float *sr) {
@@ -448,7 +462,8 @@ __global__ __launch_bounds__(kThreads, 5) void step8_kernel(Table T, StepArgs A,
   }
 }
 
-// The moments that an 8-bit state stands for; blocks of 256, one half wave each.
+// The moments that an 8-bit state stands for; blocks of 256, one half wave each.  10 bytes an
+// element, 8 of them written: 262 million in 450 us (5.8 TB/s; 714 with 2048 workgroups in a loop).
 __global__ __launch_bounds__(kThreads) void values8_kernel(const int8_t *cm, const uint8_t *cv, const float *sm, const float *sr,
                                                            float *m, float *v, int64_t blocks) {
   const int64_t b = (int64_t)blockIdx.x * (kChunk / kBlock) + threadIdx.x / kLanes;

@@ -24,7 +24,7 @@ def _args(**kw):
 
 def _step(bits, tensors=({},), args=None, copy=None, state=None, state_n=256, count=None, **kw):
     a = _args(**kw) if args is None else args
-    state = ((4096,) * (2 if bits == 32 else 4)) if state is None else state
+    state = tuple(4096 * (i + 1) for i in range(2 if bits == 32 else 4)) if state is None else state
     fn = L.lib().ma_adamw_many_step if bits == 32 else L.lib().ma_adamw8_many_step
     rows = None if tensors is None else _list(*tensors)
     return fn(len(tensors) if count is None else count, rows, None if a == 0 else C.byref(a), copy, *state, state_n, None)
@@ -66,9 +66,26 @@ def test_steps_refuse_moments(bits):
     count = 2 if bits == 32 else 4
     for i in range(count):
         for bad in (None, 4098):
-            state = [4096] * count
+            state = [4096 * (k + 1) for k in range(count)]
             state[i] = bad
             assert _step(bits, state=state) == L.MA_EINVAL
+            assert "moments" in L.last_error()[1]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_steps_refuse_memory_that_is_written_twice(bits):
+    count = 2 if bits == 32 else 4
+    apart = [1 << 16, 1 << 17, 1 << 18, 1 << 19][:count]
+    for i in range(count):
+        for j in range(i):
+            state = list(apart)
+            state[i] = state[j]
+            assert _step(bits, state=state) == L.MA_EINVAL and "overlap" in L.last_error()[1]
+        state = list(apart)
+        state[i] = 256 + 384       # the parameter's last elements
+        assert _step(bits, state=state) == L.MA_EINVAL and "overlap" in L.last_error()[1]
+        assert _step(bits, state=apart, copy=apart[i]) == L.MA_EINVAL and "overlap" in L.last_error()[1]
+    assert _step(bits, state=apart, copy=256) == L.MA_EINVAL and "overlap" in L.last_error()[1]
 
 
 @pytest.mark.parametrize("bits", [32, 8])

@@ -390,6 +390,20 @@ def test_norm_of_long_lists_and_none():
     assert float(norm) == 0.0 and float(scale) == 1.0
 
 
+@pytest.mark.parametrize("shapes", [
+    [(2048,)] * 64, [(2048,)] * 65, [(2049,)] * 32, [(2049,)] * 33, [(64 * 2048,)], [(64 * 2048 + 1,)],   # one launch, or two
+    [(3,)] * 60 + [(0,)] * 200, [(1,)] * 250, [(1,)] * 251, [(5,)] * 501,                                 # one table, two, three
+    [(8192 * 3,), (8191,), (8193,)], [(8192 * 513,)], [(511,), (512,), (513,), (1536,), (2047,)]])
+@pytest.mark.parametrize("gtypes", [(F32,), (BF16, F32)])
+def test_norms_of_all_lengths(shapes, gtypes):
+    c = Case(32, shapes=shapes, gtypes=gtypes, offset=3)
+    g = c.grads(zeros=0.0)
+    say(f"[norm] {len(shapes)} tensors of {shapes[0]}")
+    norm, _ = adamw.grad_norm(g)
+    want = _want(g)
+    assert abs(float(norm) - want) <= 1.001 * R.U * want
+
+
 def test_norm_of_one_long_tensor():
     g = torch.randn(40_000_003, device="cuda", generator=torch.Generator("cuda").manual_seed(2)).bfloat16()
     norm, _ = adamw.grad_norm([g])
@@ -524,6 +538,29 @@ def test_autograd_is_told():
     adamw.adamw_step([w], [torch.ones(4, device="cuda")], m, v, 1)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.backward()
+
+
+def test_inference_tensors_and_generators():
+    with torch.inference_mode():
+        p, g = torch.zeros(10, device="cuda"), torch.ones(10, device="cuda")
+        m, v = torch.zeros(256, device="cuda"), torch.zeros(256, device="cuda")
+        adamw.adamw_step((x for x in [p]), (x for x in [g]), m, v, 1)
+        assert bool((p < 0).all())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_tensor_given_twice_and_gradients_shared(bits):
+    c = Case(43, shapes=[(300,), (300,)], bits=bits)
+    g = c.grads()[0]
+    before = c.snapshot()
+    c.run([g, g], 1, lr=1e-3)
+    c.check(before, [g, g], 1, 1e-3, 0.0)
+    c.params[1] = c.params[0]
+    with pytest.raises(L.MicroAdamError, match="overlap"):
+        c.run([g, g], 2)
+    c.params[0], c.params[1] = c.params[0][:299], c.params[0][1:]
+    with pytest.raises(L.MicroAdamError, match="overlap"):
+        c.run([g[:299], g[1:]], 2)
 
 
 def test_refusals_with_tensors():
