@@ -70,6 +70,16 @@ def require_dense(params) -> None:
     _native().rows(params, params)
 
 
+def layout(params) -> bytes:
+    """The types, shapes and strides of all parameters, which say how their moments lie."""
+    return _native().layout(params)
+
+
+def fits(params, grads) -> bool:
+    """Whether the steps take every gradient (or None) as it is: fp32 or bf16, lying like its parameter."""
+    return _native().fits(params, grads)
+
+
 def _sequence(x):
     return x if isinstance(x, (list, tuple)) else list(x)
 

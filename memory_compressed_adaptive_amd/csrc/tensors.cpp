@@ -11,6 +11,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
+#include <vector>
 
 #include "microadam.h"
 
@@ -127,6 +128,41 @@ PyObject *grads(PyObject *, PyObject *arg) {
   });
 }
 
+// fits(params, grads) -> whether every gradient can be taken as it is
+PyObject *fits(PyObject *, PyObject *args) {
+  PyObject *a, *b;
+  if (!PyArg_ParseTuple(args, "OO", &a, &b)) return nullptr;
+  const Ref ps(PySequence_Fast(a, "a sequence"));
+  if (!ps.o) return nullptr;
+  const Ref gs(PySequence_Fast(b, "a sequence"));
+  if (!gs.o) return nullptr;
+  return guarded([&]() -> PyObject * {
+    for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(ps.o) && i < PySequence_Fast_GET_SIZE(gs.o); ++i) {
+      if (items(gs)[i] == Py_None) continue;
+      const at::Tensor &p = tensor(items(ps)[i], "a tensor"), &g = tensor(items(gs)[i], "a tensor");
+      if ((g.scalar_type() != at::kFloat && g.scalar_type() != at::kBFloat16) || !dense(g) || !like(g, p)) Py_RETURN_FALSE;
+    }
+    Py_RETURN_TRUE;
+  });
+}
+
+// layout(params) -> types, sizes and strides of all as bytes, to be compared
+PyObject *layout(PyObject *, PyObject *arg) {
+  const Ref ps(PySequence_Fast(arg, "a sequence"));
+  if (!ps.o) return nullptr;
+  return guarded([&]() -> PyObject * {
+    std::vector<int64_t> out;
+    for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(ps.o); ++i) {
+      const at::Tensor &p = tensor(items(ps)[i], "a tensor");
+      out.push_back((int64_t)p.scalar_type());
+      out.push_back(p.dim());
+      out.insert(out.end(), p.sizes().begin(), p.sizes().end());
+      out.insert(out.end(), p.strides().begin(), p.strides().end());
+    }
+    return PyBytes_FromStringAndSize(reinterpret_cast<const char *>(out.data()), (Py_ssize_t)(out.size() * sizeof(int64_t)));
+  });
+}
+
 // changed(states, params, grads): tells autograd that a call has written the states (None is
 // passed over) and the parameters with gradients
 PyObject *changed(PyObject *, PyObject *args) {
@@ -162,6 +198,8 @@ PyObject *stream(PyObject *, PyObject *arg) {
 
 PyMethodDef methods[] = {{"rows", rows, METH_VARARGS, nullptr},
                          {"grads", grads, METH_O, nullptr},
+                         {"fits", fits, METH_VARARGS, nullptr},
+                         {"layout", layout, METH_O, nullptr},
                          {"changed", changed, METH_VARARGS, nullptr},
                          {"stream", stream, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};

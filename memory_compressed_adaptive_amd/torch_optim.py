@@ -274,6 +274,7 @@ class AdamW(torch.optim.Optimizer):
         group = self.param_groups[-1]
         try:
             group["_moments"] = _moments(group, self.param_groups[0])
+            group["_layout"] = _adamw.layout(group["params"])
             if self._count is None and group["params"]:
                 self._count = torch.zeros(1, dtype=torch.int64, device=group["params"][0].device)
         except BaseException:   # memory that runs out too
@@ -292,12 +293,15 @@ class AdamW(torch.optim.Optimizer):
         if scale is not None and self.max_norm is not None:
             raise ValueError("a step takes scale or max_norm, not both")
         for group in self.param_groups:
-            if _layout(group["params"]) != group["_moments"]["layout"]:
+            if _adamw.layout(group["params"]) != group["_layout"]:
                 raise RuntimeError("a parameter was converted or laid out anew after it was given to AdamW, whose moments "
                                    "lie like it: make the optimizer afterwards")
-        grads = [[None if p.grad is None else _like(p.grad, p) for p in group["params"]] for group in self.param_groups]
+        grads = [[p.grad for p in group["params"]] for group in self.param_groups]
         if all(g is None for gs in grads for g in gs):
             return loss
+        for group, gs in zip(self.param_groups, grads):
+            if not _adamw.fits(group["params"], gs):
+                gs[:] = [None if g is None else _like(g, p) for g, p in zip(gs, group["params"])]
         if self.max_norm is not None:
             self.grad_norm, scale = _adamw.grad_norm([g for gs in grads for g in gs], self.max_norm, t=self._count)
         elif scale is not None:
@@ -322,27 +326,24 @@ class AdamW(torch.optim.Optimizer):
                                    for g in self.param_groups])
         for g in sd["param_groups"]:
             g.pop("_moments", None)
+            g.pop("_layout", None)
         return sd
 
     def load_state_dict(self, state_dict):
-        saved, mine = state_dict["adamw"], [g["_moments"] for g in self.param_groups]
+        saved, mine = state_dict["adamw"], [(g["_moments"], g["_layout"]) for g in self.param_groups]
         same = len(saved["groups"]) == len(mine) and all(
-            a.keys() == b.keys() and [tuple(map(tuple, x[:2])) for x in a["layout"]] == [x[:2] for x in b["layout"]]
-            for a, b in zip(saved["groups"], mine))
+            a.keys() == b.keys() and [tuple(map(tuple, x)) for x in a["layout"]] == b["layout"]
+            for a, (b, _) in zip(saved["groups"], mine))
         if not same:
             raise ValueError("the saved moments are those of other parameters, layouts, state_bits or master_weights")
         super().load_state_dict({"state": state_dict["state"], "param_groups": [dict(g) for g in state_dict["param_groups"]]})
-        for g, st, new in zip(self.param_groups, mine, saved["groups"]):
-            g["_moments"] = st
+        for g, (st, layout), new in zip(self.param_groups, mine, saved["groups"]):
+            g["_moments"], g["_layout"] = st, layout
             for k, v in new.items():
                 if torch.is_tensor(v):
                     st[k].copy_(v)
         if self._count is not None:
             self._count.fill_(saved["count"])
-
-
-def _layout(params):
-    return [(tuple(p.shape), p.stride(), p.dtype) for p in params]
 
 
 def _like(g, p):
@@ -369,7 +370,7 @@ def _moments(group, first):
             raise ValueError("parameters must be float32 or bfloat16")
         if p.device != (first["params"] or ps)[0].device:
             raise ValueError("the parameters must share a device")
-    st = {"layout": _layout(ps)}
+    st = {"layout": [(tuple(p.shape), p.stride()) for p in ps]}
     if not ps:
         return st
     size, device = _adamw.state_size(ps), ps[0].device
