@@ -325,7 +325,7 @@ __device__ __forceinline__ uint32_t kept(uint32_t w, int left) {
 // whose bytes take 510 at a copy's rate.  64-bit operations cost what 32-bit ones do (4 cycles a
 // wave; additions and products in 32 bits less), so moments are formed in 64 bits; what follows
 // goes by 32-bit estimates of the codes' roots, good to a few parts in 10^7, and a lane with
-// an element nearer to a border than that (one in 700) decides its codes again in 64 bits.
+// an element nearer to a border than that (one in 600) decides its codes again in 64 bits.
 // 1/x and roots are the hardware's estimates: the update is off by a few parts in 10^7 of
 // itself.  443 instructions a wave and 8 elements, 89 registers, five waves a SIMD (with four
 // the same time, with six, and registers in memory, 545 us): 502 to 520 us, 5.1 to 5.3 TB/s.
@@ -486,8 +486,8 @@ __global__ __launch_bounds__(kThreads) void values8_kernel(const int8_t *cm, con
 }
 
 // ------------------------------------------------------ the norm of all gradients
-// Squares and sums in 64 bits: no gradient's square overflows or vanishes, and the
-// order of the sums, fixed by the list, shows in no bit of a 32-bit result.
+// Squares and sums in 64 bits, which cost what 32 do: no gradient's square overflows or
+// vanishes, and the order of the sums, fixed by the list, next to never shows in a 32-bit result.
 
 template <int THREADS> __device__ __forceinline__ double group_sum(double x) {
   __shared__ double lds[THREADS / 64];
