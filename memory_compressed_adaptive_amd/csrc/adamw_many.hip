@@ -137,12 +137,15 @@ template <class F> hipError_t each_table(int64_t count, const ma_tensor *tensors
     if (t.p_type != p_type || t.g_type != g_type) continue;
     for (int64_t from = 0; from < t.n; from += kEntry) {
       const int64_t n = std::min(t.n - from, kEntry);
+      const uint32_t chunks = (uint32_t)((n + kChunk - 1) / kChunk);   // at most 2^19
+      if (T.chunks + chunks > kMostChunks)
+        if (const hipError_t e = flush(); e != hipSuccess) return e;
       T.param[used] = static_cast<char *>(t.param) + from * size_of(p_type);
       T.grad[used] = static_cast<const char *>(t.grad) + from * size_of(g_type);
       T.n[used] = (uint32_t)n;
       T.block[used] = (uint32_t)((t.at + from) / kBlock);
       T.first[used] = T.chunks;
-      T.chunks += (uint32_t)((n + kChunk - 1) / kChunk);   // at most 2^19 each
+      T.chunks += chunks;
       if (++used == kTable)
         if (const hipError_t e = flush(); e != hipSuccess) return e;
     }
@@ -309,8 +312,14 @@ int ma_adamw8_many_values(int64_t state_n, const int8_t *cm, const uint8_t *cv, 
         (((uintptr_t)sm | (uintptr_t)sr) & 3u))
       return fail(MA_EINVAL, "%s: null or misaligned pointer", who);
     return on_device(who, stream, [&] {
-      hipLaunchKernelGGL(values8_kernel, dim3((unsigned)((state_n + kChunk - 1) / kChunk)), dim3(kThreads), 0, stream, cm, cv, sm, sr, m, v, state_n / kBlock);
-      return hipGetLastError();
+      constexpr int64_t most = int64_t(kMostChunks) * kChunk;
+      for (int64_t at = 0; at < state_n; at += most) {
+        const int64_t n = std::min(state_n - at, most), b = at / kBlock;
+        hipLaunchKernelGGL(values8_kernel, dim3((unsigned)((n + kChunk - 1) / kChunk)), dim3(kThreads), 0, stream, cm + at, cv + at,
+                           sm + b, sr + b, m + at, v + at, n / kBlock);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+      }
+      return hipSuccess;
     });
   });
 }

@@ -30,6 +30,7 @@ constexpr int kChunk = kThreads * kRun;
 constexpr int kTable = 140;      // tensors of a launch: as many as its 4 KiB of arguments hold
 constexpr int kNormTable = 250;
 constexpr int64_t kEntry = int64_t(1) << 30;   // elements of an entry: a longer tensor takes several
+constexpr uint32_t kMostChunks = 1u << 23;     // of a launch: a grid may have 2^32 - 1 threads
 constexpr int kNormRuns = 4, kNormChunk = kNormRuns * kChunk;
 constexpr int kSmallThreads = 1024, kSmallSpan = 64 * kRun, kSmallChunk = kNormRuns * kSmallSpan;
 constexpr int kSmallChunks = 64;   // of a list that one workgroup takes, at most

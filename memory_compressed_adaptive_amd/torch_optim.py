@@ -292,6 +292,8 @@ class AdamW(torch.optim.Optimizer):
                 loss = closure()
         if scale is not None and self.max_norm is not None:
             raise ValueError("a step takes scale or max_norm, not both")
+        if scale is not None and not (torch.is_tensor(scale) and scale.dtype == torch.float32 and scale.numel() == 1 and scale.is_cuda):
+            raise ValueError("scale must be a float32 tensor of one element on the GPU")
         for group in self.param_groups:
             if _adamw.layout(group["params"]) != group["_layout"]:
                 raise RuntimeError("a parameter was converted or laid out anew after it was given to AdamW, whose moments "

@@ -191,3 +191,23 @@ def test_the_references_scales():
     s = torch.tensor([1.0, 1.0 + 2.0 ** -23, 1.0, 1.0 + 2.0 ** -23, 1.0 + 2.0 ** -22, float("nan"), 1.0])
     top = torch.tensor([1.0, 1.0, 1.0 + 2.0 ** -24, 1.0 + 2.0 ** -24, 1.0 + 2.0 ** -24, float("nan"), float("nan")], dtype=torch.float64)
     assert R.is_rounded(s, top).tolist() == [True, False, True, True, False, True, False]
+
+
+@pytest.mark.parametrize("handle,given,switched", [(7, None, False), (None, None, True), (7, "stream", True), (None, "stream", True)])
+def test_the_tensors_device_is_current_during_a_call(monkeypatch, handle, given, switched):
+    """With the tensors' device current, the current stream's handle will do; otherwise, and for
+    a stream that is given, the call is made as the Muon operators make theirs."""
+    class Native:
+        @staticmethod
+        def stream(index):
+            assert index == 3
+            return handle
+
+    class Stream:
+        cuda_stream = 11
+
+    monkeypatch.setattr(adamw, "_native", lambda: Native)
+    monkeypatch.setattr(adamw, "_place", lambda device, stream: (Stream, ("placed", device, stream)))
+    device = torch.device("cuda", 3)
+    got = adamw._stream(device, given)
+    assert got == ((11, ("placed", device, given)) if switched else (7, adamw._HERE))

@@ -625,6 +625,34 @@ def test_offsets_past_32_bits(bits):
     assert abs(float(norm) - want) <= 1.001 * R.U * want
 
 
+def test_more_chunks_than_a_grid_takes():
+    """17 parameters of 2^30 elements and some (35 GB of bf16, 36 GB of moments) with one gradient:
+    past 2^32 threads of a launch.  The ends are as if they were lists of their own."""
+    if torch.cuda.mem_get_info()[0] < 100e9:
+        pytest.skip("too little memory")
+    gen = torch.Generator("cuda").manual_seed(10)
+    n, tail = 2 ** 30 + 1000, 5096
+    g = torch.zeros(n, dtype=BF16, device="cuda")
+    g[-tail:] = (1e-3 * torch.randn(tail, device="cuda", generator=gen)).bfloat16()
+    ps = [torch.zeros(n, dtype=BF16, device="cuda") for _ in range(17)]
+    for p in ps:
+        p[-tail:] = (0.02 * torch.randn(tail, device="cuda", generator=gen)).bfloat16()
+    qs = [p[-tail:].clone() for p in ps]
+    state, small = ([torch.zeros(adamw.state_size(x) // k, dtype=d, device="cuda")
+                     for d, k in ((torch.int8, 1), (torch.uint8, 1), (torch.float32, 256), (torch.float32, 256))] for x in (ps, qs))
+    assert (n - tail) % 256 == 0 and state[0].numel() > 2 ** 34
+    say("[adamw many] 17 of 2^30 elements")
+    adamw.adamw8_step(ps, [g] * 17, *state, 1, lr=1e-3)
+    adamw.adamw8_step(qs, [g[-tail:]] * 17, *small, 1, lr=1e-3)
+    for i, (p, q, a, b) in enumerate(zip(ps, qs, adamw.starts(ps), adamw.starts(qs))):
+        assert torch.equal(p[-tail:], q), i
+        a += n - tail
+        e = -(-tail // 256) * 256
+        for x, y, k in zip(state, small, (1, 1, 256, 256)):
+            assert torch.equal(x[a // k:(a + e) // k], y[b // k:(b + e) // k]), i
+    assert not any(bool(p[:-tail].any()) for p in (ps[0], ps[15], ps[16]))
+
+
 def test_the_c_call_takes_the_null_stream():
     p, g = torch.zeros(10, device="cuda"), torch.ones(10, device="cuda")
     m, v = torch.zeros(256, device="cuda"), torch.zeros(256, device="cuda")

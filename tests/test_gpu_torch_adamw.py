@@ -251,6 +251,10 @@ def test_added_group_and_refusals():
     assert len(opt.param_groups) == 2
     with pytest.raises(ValueError, match="not both"):
         AdamW(_params(1), max_norm=1.0).step(scale=torch.ones(1, device="cuda"))
+    for scale in (0.5, torch.ones(1), torch.ones(2, device="cuda"), torch.ones(1, device="cuda", dtype=torch.float64)):
+        with pytest.raises(ValueError, match="scale"):
+            opt.step(scale=scale)
+    assert opt.state_dict()["adamw"]["count"] == 1
     opt.step()
     loss = opt.step(lambda: torch.tensor(3.0))
     assert float(loss) == 3.0
