@@ -284,11 +284,11 @@ int ma_debug_muon_plan(int64_t batch, int64_t rows, int64_t cols, int64_t *out);
  * passed over.
  *
  * Calls only enqueue work on `stream` (one launch for every 140 tensors of one
- * pair of types; ma_grad_norm one for every 250 and one more, or one alone
- * for a short list), allocate
- * nothing on the device and can be captured into a HIP graph.  Nothing uses
- * atomics: a call repeats its bits, and how tensors are put together in lists
- * changes none of a step's.
+ * pair of types, as a rule; ma_grad_norm one for every 250 and one more, or one
+ * alone for a short list), allocate nothing on the device and can be captured
+ * into a HIP graph.  After MA_EHIP some of a call's launches may have been made.
+ * Nothing uses atomics: a call repeats its bits, and how tensors are put together
+ * in lists changes none of a step's.
  *
  * MA_EINVAL: null or misaligned pointers (parameters and gradients to their
  * elements), negative sizes, unknown types, `at` out of order or past state_n,

@@ -531,6 +531,30 @@ def test_another_stream(bits):
     assert all(torch.equal(x, y) for x, y in zip(a.params + a.state, b.params + b.state))
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_two_lists_at_once(bits):
+    """Steps and norms of two lists on two streams, under way together, are those one after the other."""
+    shapes = [(300_000,), (7,), (65_537,)] + [(100,)] * 150
+    a, b = ([Case(44 + k, shapes=shapes, ptypes=(BF16, F32), gtypes=(F32,), bits=bits, copy=True) for k in range(2)] for _ in range(2))
+    gs = [[c.grads() for _ in range(4)] for c in a]
+    streams, ts = [torch.cuda.Stream() for _ in a], [torch.zeros(1, dtype=torch.int64, device="cuda") for _ in a + b]
+    torch.cuda.synchronize()
+    norms = [[], []]
+    for i in range(4):
+        for k, (c, s) in enumerate(zip(a, streams)):
+            norm, scale = adamw.grad_norm(gs[k][i], 0.1, t=ts[k], stream=s)
+            c.run(gs[k][i], ts[k], lr=1e-3, wd=0.1, scale=scale, stream=s)
+            norms[k].append((norm, scale))
+    torch.cuda.synchronize()
+    for k, c in enumerate(b):
+        for i in range(4):
+            norm, scale = adamw.grad_norm(gs[k][i], 0.1, t=ts[2 + k])
+            c.run(gs[k][i], ts[2 + k], lr=1e-3, wd=0.1, scale=scale)
+            assert float(norm) == float(norms[k][i][0]) and float(scale) == float(norms[k][i][1])
+        for x, y in zip(a[k].params + a[k].state + [a[k].master], c.params + c.state + [c.master]):
+            assert torch.equal(x, y)
+
+
 def test_autograd_is_told():
     w = torch.nn.Parameter(torch.ones(4, device="cuda"))
     y = (w * w).sum()
