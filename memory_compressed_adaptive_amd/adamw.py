@@ -75,9 +75,10 @@ def layout(params) -> bytes:
     return _native().layout(params)
 
 
-def fits(params, grads) -> bool:
-    """Whether the steps take every gradient (or None) as it is: fp32 or bf16, lying like its parameter."""
-    return _native().fits(params, grads)
+def missing(params, grads) -> int:
+    """How many parameters have None for a gradient; -1 if the steps do not take some gradient
+    as it is (fp32 or bf16, lying like its parameter)."""
+    return _native().missing(params, grads)
 
 
 def _sequence(x):

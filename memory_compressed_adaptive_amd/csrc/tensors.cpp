@@ -128,8 +128,8 @@ PyObject *grads(PyObject *, PyObject *arg) {
   });
 }
 
-// fits(params, grads) -> whether every gradient can be taken as it is
-PyObject *fits(PyObject *, PyObject *args) {
+// missing(params, grads) -> how many parameters have no gradient; -1 if a gradient cannot be taken as it is
+PyObject *missing(PyObject *, PyObject *args) {
   PyObject *a, *b;
   if (!PyArg_ParseTuple(args, "OO", &a, &b)) return nullptr;
   const Ref ps(PySequence_Fast(a, "a sequence"));
@@ -137,12 +137,16 @@ PyObject *fits(PyObject *, PyObject *args) {
   const Ref gs(PySequence_Fast(b, "a sequence"));
   if (!gs.o) return nullptr;
   return guarded([&]() -> PyObject * {
+    long none = 0;
     for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(ps.o) && i < PySequence_Fast_GET_SIZE(gs.o); ++i) {
-      if (items(gs)[i] == Py_None) continue;
+      if (items(gs)[i] == Py_None) {
+        ++none;
+        continue;
+      }
       const at::Tensor &p = tensor(items(ps)[i], "a tensor"), &g = tensor(items(gs)[i], "a tensor");
-      if ((g.scalar_type() != at::kFloat && g.scalar_type() != at::kBFloat16) || !dense(g) || !like(g, p)) Py_RETURN_FALSE;
+      if ((g.scalar_type() != at::kFloat && g.scalar_type() != at::kBFloat16) || !dense(g) || !like(g, p)) return PyLong_FromLong(-1);
     }
-    Py_RETURN_TRUE;
+    return PyLong_FromLong(none);
   });
 }
 
@@ -198,7 +202,7 @@ PyObject *stream(PyObject *, PyObject *arg) {
 
 PyMethodDef methods[] = {{"rows", rows, METH_VARARGS, nullptr},
                          {"grads", grads, METH_O, nullptr},
-                         {"fits", fits, METH_VARARGS, nullptr},
+                         {"missing", missing, METH_VARARGS, nullptr},
                          {"layout", layout, METH_O, nullptr},
                          {"changed", changed, METH_VARARGS, nullptr},
                          {"stream", stream, METH_O, nullptr},

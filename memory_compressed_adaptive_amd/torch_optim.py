@@ -19,6 +19,8 @@ dense moments in 32 or 8 bits, and can clip by the norm of all gradients.
 """
 from __future__ import annotations
 
+from itertools import zip_longest
+
 import torch
 
 from . import adamw as _adamw
@@ -255,17 +257,23 @@ class AdamW(torch.optim.Optimizer):
 
     lr, betas, eps and weight_decay may be changed between steps; lr may be a
     float32 tensor of one element on the GPU, which a captured step reads at
-    every replay.  The count of steps is one for all groups and is kept on the GPU.
-    A parameter without a gradient is left alone, its moments too.  Gradients are
-    float32 or bfloat16 as they are; others, and ones that lie unlike their
-    parameter, are copied first.
+    every replay.  A parameter without a gradient is left alone, its moments and its
+    count of steps too.  Counts are kept on the GPU, one for all parameters that
+    have had gradients at the same steps; these go in one call for each group.  A
+    captured step goes on with the parameters and counts it was captured with.
+    Gradients are float32 or bfloat16 as they are; others, and ones that lie unlike
+    their parameter, are copied first.
     """
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.0, state_bits=32, master_weights=False,
                  max_norm=None):
         if max_norm is not None and not max_norm > 0:
             raise ValueError("max_norm must be positive")
-        self.max_norm, self.grad_norm, self._count = max_norm, None, None
+        self.max_norm, self.grad_norm = max_norm, None
+        # A count for each history of gradients, the first _histories of _counts; a group's _slots say
+        # which one a parameter goes by.  A history is at least one parameter's, so that there is room
+        # for all of them from the start: a captured step holds their addresses.
+        self._counts, self._histories, self._begun = [], 0, False
         super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits,
                                       master_weights=master_weights))
 
@@ -275,8 +283,10 @@ class AdamW(torch.optim.Optimizer):
         try:
             group["_moments"] = _moments(group, self.param_groups[0])
             group["_layout"] = _adamw.layout(group["params"])
-            if self._count is None and group["params"]:
-                self._count = torch.zeros(1, dtype=torch.int64, device=group["params"][0].device)
+            group["_slots"] = [self._histories if self._begun else 0] * len(group["params"])
+            if group["params"]:
+                self._counts += torch.zeros(len(group["params"]), dtype=torch.int64, device=group["params"][0].device).split(1)
+                self._histories = group["_slots"][0] + 1
         except BaseException:   # memory that runs out too
             self.param_groups.pop()
             raise
@@ -299,36 +309,69 @@ class AdamW(torch.optim.Optimizer):
                 raise RuntimeError("a parameter was converted or laid out anew after it was given to AdamW, whose moments "
                                    "lie like it: make the optimizer afterwards")
         grads = [[p.grad for p in group["params"]] for group in self.param_groups]
-        if all(g is None for gs in grads for g in gs):
-            return loss
-        for group, gs in zip(self.param_groups, grads):
-            if not _adamw.fits(group["params"], gs):
+        none = [_adamw.missing(group["params"], gs) for group, gs in zip(self.param_groups, grads)]
+        for i, (group, gs) in enumerate(zip(self.param_groups, grads)):
+            if none[i] < 0:
                 gs[:] = [None if g is None else _like(g, p) for g, p in zip(gs, group["params"])]
+                none[i] = sum(g is None for g in gs)
+        if sum(none) == sum(map(len, grads)):
+            return loss
+        slots = [0] if self._histories == 1 and not any(none) else self._part(grads)
+        self._begun = True
+        counts = [self._counts[s] for s in slots]
         if self.max_norm is not None:
-            self.grad_norm, scale = _adamw.grad_norm([g for gs in grads for g in gs], self.max_norm, t=self._count)
-        elif scale is not None:
-            self._count.add_(scale == scale)
-        else:
-            self._count.add_(1)
+            # the norm's call counts the step where there is one count to raise
+            self.grad_norm, scale = _adamw.grad_norm([g for gs in grads for g in gs], self.max_norm,
+                                                     t=counts[0] if len(slots) == 1 else None)
+        if self.max_norm is None or len(slots) > 1:
+            taken = 1 if scale is None else (scale == scale).reshape(1)
+            for count in counts:
+                count.add_(taken)
         for group, gs in zip(self.param_groups, grads):
             st, (b1, b2) = group["_moments"], group["betas"]
             kw = dict(lr=group["lr"], beta1=b1, beta2=b2, eps=group["eps"], wd=group["weight_decay"], scale=scale,
                       master=st.get("master"))
-            if "cm" in st:
-                _adamw.adamw8_step(group["params"], gs, st["cm"], st["cv"], st["sm"], st["sr"], self._count, **kw)
-            else:
-                _adamw.adamw_step(group["params"], gs, st["m"], st["v"], self._count, **kw)
+            for slot, count in zip(slots, counts):
+                some = gs if len(slots) == 1 else [g if s == slot else None for s, g in zip(group["_slots"], gs)]
+                if all(g is None for g in some):
+                    continue
+                if "cm" in st:
+                    _adamw.adamw8_step(group["params"], some, st["cm"], st["cv"], st["sm"], st["sr"], count, **kw)
+                else:
+                    _adamw.adamw_step(group["params"], some, st["m"], st["v"], count, **kw)
         return loss
 
+    def _part(self, grads):
+        """The histories of the parameters with gradients; those without one that shared such a history
+        part from it here."""
+        has, new = set(), {}
+        for group, gs in zip(self.param_groups, grads):
+            has.update(s for s, g in zip(group["_slots"], gs) if g is not None)
+        parting = [(group["_slots"], i) for group, gs in zip(self.param_groups, grads)
+                   for i, (s, g) in enumerate(zip(group["_slots"], gs)) if g is None and s in has]
+        if parting and self._begun and torch.cuda.is_current_stream_capturing():
+            # every replay would copy the count anew
+            raise RuntimeError("other parameters have gradients than in the steps before: take a step with these before capturing one")
+        for slots, i in parting:
+            s = slots[i]
+            if s not in new:
+                new[s], self._histories = self._histories, self._histories + 1
+                if self._begun:
+                    self._counts[new[s]].copy_(self._counts[s])
+            slots[i] = new[s]
+        return sorted(has)
+
     def state_dict(self):
-        """The usual dictionary, and under "adamw" the count and every group's moments as they are."""
+        """The usual dictionary, and under "adamw" the counts and every group's moments as they are."""
         sd = super().state_dict()
-        sd["adamw"] = dict(count=0 if self._count is None else int(self._count),
+        sd["adamw"] = dict(counts=[int(c) for c in self._counts[:self._histories]],
+                           slots=[list(g["_slots"]) for g in self.param_groups],
                            groups=[{k: v.clone() if torch.is_tensor(v) else v for k, v in g["_moments"].items()}
                                    for g in self.param_groups])
         for g in sd["param_groups"]:
             g.pop("_moments", None)
             g.pop("_layout", None)
+            g.pop("_slots", None)
         return sd
 
     def load_state_dict(self, state_dict):
@@ -339,22 +382,24 @@ class AdamW(torch.optim.Optimizer):
         if not same:
             raise ValueError("the saved moments are those of other parameters, layouts, state_bits or master_weights")
         super().load_state_dict({"state": state_dict["state"], "param_groups": [dict(g) for g in state_dict["param_groups"]]})
-        for g, (st, layout), new in zip(self.param_groups, mine, saved["groups"]):
-            g["_moments"], g["_layout"] = st, layout
+        for g, (st, layout), new, slots in zip(self.param_groups, mine, saved["groups"], saved["slots"]):
+            g["_moments"], g["_layout"], g["_slots"] = st, layout, list(slots)
             for k, v in new.items():
                 if torch.is_tensor(v):
                     st[k].copy_(v)
-        if self._count is not None:
-            self._count.fill_(saved["count"])
+        self._histories = len(saved["counts"])
+        self._begun = self._histories > 1 or any(saved["counts"])
+        for count, n in zip_longest(self._counts, saved["counts"], fillvalue=0):
+            count.fill_(n)
 
 
 def _like(g, p):
     """The gradient in a type and layout that the step takes."""
     if g.is_sparse:
         raise ValueError("AdamW does not take sparse gradients")
-    dtype = g.dtype if g.dtype in (torch.float32, torch.bfloat16) else torch.float32
-    if dtype == g.dtype and (g.stride() == p.stride() or g.numel() < 2 or (g.is_contiguous() and p.is_contiguous())):
+    if _adamw.missing([p], [g]) == 0:
         return g
+    dtype = g.dtype if g.dtype in (torch.float32, torch.bfloat16) else torch.float32
     return torch.empty_like(p, dtype=dtype, memory_format=torch.preserve_format).copy_(g)
 
 

@@ -64,7 +64,7 @@ def test_steps_are_the_operators(dtypes, copies, bits, max_norm):
     own = [Own(ps[:2], bits, copies), Own(ps[2:], bits, copies)]
     opt = AdamW([{"params": ps[:2]}, {"params": ps[2:], "weight_decay": 0.0}], lr=0.01, betas=(0.8, 0.99), weight_decay=0.1,
                 state_bits=bits, master_weights=copies, max_norm=max_norm)
-    lr = 0.01
+    lr, counts = 0.01, [0] * len(ps)
     for t in range(1, 6):
         gs = [g.to(p.dtype) for g, p in zip(_grads(10 + t), ps)]
         for i, (p, g) in enumerate(zip(ps, gs)):
@@ -79,9 +79,12 @@ def test_steps_are_the_operators(dtypes, copies, bits, max_norm):
         if max_norm is not None:
             norm, scale = adamw.grad_norm([p.grad for p in ps], max_norm)
             assert float(norm) == float(opt.grad_norm) and float(scale) < 1
-        count = torch.tensor([t], device="cuda")
-        own[0].step([p.grad for p in ps[:2]], count, lr=lr, beta1=0.8, beta2=0.99, wd=0.1, scale=scale)
-        own[1].step([p.grad for p in ps[2:]], count, lr=lr, beta1=0.8, beta2=0.99, wd=0.0, scale=scale)
+        counts = [k + (p.grad is not None) for k, p in zip(counts, ps)]
+        for k in sorted(set(counts)):
+            some = [p.grad if c == k else None for c, p in zip(counts, ps)]
+            count = torch.tensor([k], device="cuda")
+            own[0].step(some[:2], count, lr=lr, beta1=0.8, beta2=0.99, wd=0.1, scale=scale)
+            own[1].step(some[2:], count, lr=lr, beta1=0.8, beta2=0.99, wd=0.0, scale=scale)
         assert own[0].same(ps[:2]) and own[1].same(ps[2:]), t
 
 
@@ -95,6 +98,50 @@ def test_32_bits_are_torchs_adamw():
         a.step(), b.step()
         for p, q in zip(ps, qs):
             assert bool(((p - q).abs() <= (t + 1) * (1e-2 * 40 * 2.0 ** -24 + 4 * 2.0 ** -24 * q.abs())).all()), t
+
+
+def test_parameters_that_join_later_are_torchs_adamw():
+    """The first step of a parameter is corrected as a first step, whenever it comes."""
+    ps, qs = _params(12), _params(12)
+    a, b = AdamW([{"params": ps[:2]}, {"params": ps[2:]}], lr=1e-2), torch.optim.AdamW(qs, lr=1e-2, weight_decay=0.0)
+    for t in range(12):
+        for i, (p, q, g) in enumerate(zip(ps, qs, _grads(60 + t))):
+            p.grad, q.grad = (None, None) if t < 3 * i or (i == 0 and t % 5 == 4) else (g, g.clone())
+        a.step(), b.step()
+        for p, q in zip(ps, qs):
+            assert bool(((p - q).abs() <= (t + 1) * (1e-2 * 40 * 2.0 ** -24 + 4 * 2.0 ** -24 * q.abs())).all()), t
+    assert sorted(a.state_dict()["adamw"]["counts"]) == sorted({int(b.state[q].get("step", 0)) for q in qs})
+
+
+def test_a_captured_step_of_some_parameters():
+    ps, qs = _params(13), _params(13)
+    a, b = AdamW(ps, lr=1e-2, max_norm=1.0), AdamW(qs, lr=1e-2, max_norm=1.0)
+
+    def grads(t, but=None):
+        for i, (p, q, g) in enumerate(zip(ps, qs, _grads(70 + t))):
+            if i == but:
+                p.grad = q.grad = None
+            elif p.grad is None:
+                p.grad, q.grad = g, g.clone()
+            else:
+                p.grad.copy_(g), q.grad.copy_(g)
+
+    grads(0), a.step(), b.step()
+    grads(1, but=1)
+    a.step(), b.step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.step()
+    for t in range(2, 5):
+        grads(t, but=1)
+        graph.replay()
+        b.step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(ps, qs)), t
+    grads(5), a.step(), b.step()
+    assert all(torch.equal(p, q) for p, q in zip(ps, qs))
+    assert a.state_dict()["adamw"]["counts"] == b.state_dict()["adamw"]["counts"] == [6, 2]
 
 
 @pytest.mark.parametrize("value", [math.inf, math.nan])
@@ -116,7 +163,7 @@ def test_a_step_that_is_not_finite_is_not_taken(value, how):
             assert all(torch.equal(p, x) for p, x in zip(ps, before))
         else:
             step(b, qs)
-    assert all(torch.equal(p, q) for p, q in zip(ps, qs)) and a.state_dict()["adamw"]["count"] == 2
+    assert all(torch.equal(p, q) for p, q in zip(ps, qs)) and a.state_dict()["adamw"]["counts"] == [2]
 
 
 @pytest.mark.parametrize("bits,copies", [(32, False), (32, True), (8, True)])
@@ -254,7 +301,7 @@ def test_added_group_and_refusals():
     for scale in (0.5, torch.ones(1), torch.ones(2, device="cuda"), torch.ones(1, device="cuda", dtype=torch.float64)):
         with pytest.raises(ValueError, match="scale"):
             opt.step(scale=scale)
-    assert opt.state_dict()["adamw"]["count"] == 1
+    assert opt.state_dict()["adamw"]["counts"] == [1]
     opt.step()
     loss = opt.step(lambda: torch.tensor(3.0))
     assert float(loss) == 3.0
