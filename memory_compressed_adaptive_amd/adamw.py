@@ -82,6 +82,8 @@ def missing(params, grads) -> int:
 
 
 def _sequence(x):
+    """A list as it is; what an iterator yields, kept until the call is made: the rows that are read
+    from it hold addresses only."""
     return x if isinstance(x, (list, tuple)) else list(x)
 
 
@@ -131,6 +133,7 @@ def grad_norm(grads, max_norm: float = math.inf, t=None, out=None, stream=None):
     count of steps that is raised by one if the norm is finite.  out: fp32 of two
     elements for both."""
     import torch
+    grads = _sequence(grads)
     rows, count, index = _native().grads(grads)
     _L.require(count > 0 or out is not None, "there must be a gradient, or out")
     device = torch.device("cuda", index) if count else out.device

@@ -3,6 +3,7 @@ the tests' own reference that need no GPU: every call here is refused, or empty,
 before a device is touched."""
 import ctypes as C
 import math
+import weakref
 
 import pytest
 import torch
@@ -211,3 +212,52 @@ def test_the_tensors_device_is_current_during_a_call(monkeypatch, handle, given,
     device = torch.device("cuda", 3)
     got = adamw._stream(device, given)
     assert got == ((11, ("placed", device, given)) if switched else (7, adamw._HERE))
+
+
+@pytest.mark.parametrize("call", ["norm", "step", "step8"])
+@pytest.mark.parametrize("of", [list, iter], ids=["list", "iterator"])
+def test_what_an_iterator_yields_is_kept_until_the_call_is_made(monkeypatch, call, of):
+    """The list that is read holds addresses only: whoever reads it keeps the tensors."""
+    alive, seen = [], []
+
+    class Native:
+        @staticmethod
+        def grads(gs):
+            alive.extend(map(weakref.ref, gs))
+            return b"", 2, 0
+
+        @staticmethod
+        def rows(ps, gs):
+            alive.extend([weakref.ref(x) for xs in (ps, gs) for x in xs])
+            return b"", 2, 0, 512
+
+        @staticmethod
+        def stream(index):
+            return 7
+
+        @staticmethod
+        def changed(*lists):
+            pass
+
+    class Lib:
+        ma_grad_norm_workspace = staticmethod(lambda count: 256)
+
+        def __getattr__(self, name):
+            def enqueue(*args):
+                seen.extend(r() is not None for r in alive)
+                return L.MA_OK
+            return enqueue
+
+    monkeypatch.setattr(adamw, "_native", lambda: Native)
+    monkeypatch.setattr(adamw, "_state", lambda t, *rest: 0)
+    monkeypatch.setattr(adamw, "_workspace", lambda nbytes, device: torch.zeros(nbytes, dtype=torch.uint8))
+    monkeypatch.setattr(adamw._L, "lib", Lib)
+    tensors = lambda: of([torch.zeros(4), torch.zeros(4)])  # noqa: E731
+    s = torch.zeros(512)
+    if call == "norm":
+        adamw.grad_norm(tensors(), out=torch.zeros(2))
+    elif call == "step":
+        adamw.adamw_step(tensors(), tensors(), s, s, 1)
+    else:
+        adamw.adamw8_step(tensors(), tensors(), s, s, s, s, 1)
+    assert seen == [True] * (2 if call == "norm" else 4)

@@ -686,3 +686,15 @@ def test_the_c_call_takes_the_null_stream():
     L.check(L.lib().ma_adamw_many_step(1, rows, C.byref(a), None, m.data_ptr(), v.data_ptr(), 256, None))
     torch.cuda.synchronize()
     assert torch.allclose(p, torch.full_like(p, -1e-3), rtol=1e-5) and not bool(m[10:].any())
+
+
+@pytest.mark.parametrize("n", [1000, 1024, 2048])
+def test_norm_of_gradients_that_an_iterator_makes(n):
+    """Nobody else holds the 32-bit copies, which are as large as the call's workspace."""
+    torch.manual_seed(5)
+    g = [torch.randn(n, device="cuda").to(BF16) for _ in range(300)]
+    want = math.sqrt(sum(float(x.double().square().sum()) for x in g))
+    for _ in range(3):
+        norm, scale = adamw.grad_norm((x.float() for x in g), 1.0)
+        assert float(norm) == pytest.approx(want, rel=2.0 ** -23)
+        assert float(scale) == pytest.approx(1 / (want + 1e-6), rel=2.0 ** -23)
