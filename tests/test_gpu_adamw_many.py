@@ -696,5 +696,6 @@ def test_norm_of_gradients_that_an_iterator_makes(n):
     want = math.sqrt(sum(float(x.double().square().sum()) for x in g))
     for _ in range(3):
         norm, scale = adamw.grad_norm((x.float() for x in g), 1.0)
-        assert float(norm) == pytest.approx(want, rel=2.0 ** -23)
-        assert float(scale) == pytest.approx(1 / (want + 1e-6), rel=2.0 ** -23)
+        # one rounding each, beside those in 64 bits
+        assert float(norm) == pytest.approx(want, rel=1.01 * 2.0 ** -24)
+        assert float(scale) == pytest.approx(1 / (want + 1e-6), rel=1.01 * 2.0 ** -24)
