@@ -49,6 +49,7 @@ def state_size(params) -> int:
 
 def views(state, params) -> list:
     """The part of a state array that belongs to each tensor, in the tensor's shape."""
+    params = _sequence(params)
     return [state[a:a + p.numel()].as_strided(p.shape, p.stride(), state.storage_offset() + a)
             for p, a in zip(params, starts(params))]
 
@@ -67,6 +68,7 @@ def _native():
 
 def require_dense(params) -> None:
     """ValueError unless every parameter is one that the steps take."""
+    params = _sequence(params)
     _native().rows(params, params)
 
 

@@ -261,3 +261,14 @@ def test_what_an_iterator_yields_is_kept_until_the_call_is_made(monkeypatch, cal
     else:
         adamw.adamw8_step(tensors(), tensors(), s, s, s, s, 1)
     assert seen == [True] * (2 if call == "norm" else 4)
+
+
+def test_the_layout_of_what_an_iterator_yields():
+    ps = [torch.zeros(3, 100), torch.zeros(7)]
+    flat = torch.arange(1024.0)
+    assert [v.shape for v in adamw.views(flat[:768], iter(ps))] == [p.shape for p in ps]
+    assert adamw.starts(iter(ps)) == [0, 512] and adamw.state_size(iter(ps)) == 768
+    assert adamw.layout(iter(ps)) == adamw.layout(ps) and adamw.missing(iter(ps), iter([None, ps[1]])) == 1
+    for given in (ps, iter(ps)):
+        with pytest.raises(ValueError, match="CUDA"):
+            adamw.require_dense(given)
