@@ -90,13 +90,13 @@ def _sequence(x):
 
 
 def _state(t, what: str, dtype, size: int, device):
-    if not (t.dtype == dtype and t.is_contiguous() and t.numel() == size and t.device == device):
+    if not (t.dtype == dtype and t.is_contiguous() and t.numel() == size and t.device == device and not t.is_neg()):
         raise ValueError(f"{what} must be contiguous {dtype} of {size} elements on the device of the tensors")
     return t.data_ptr()
 
 
 def _one(t, what: str, dtype, device):
-    if not (t.dtype == dtype and t.numel() == 1 and t.device == device):
+    if not (t.dtype == dtype and t.numel() == 1 and t.device == device and not t.is_neg()):
         raise ValueError(f"{what} must be one {dtype} on the device of the tensors")
     return t.data_ptr()
 

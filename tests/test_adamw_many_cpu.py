@@ -272,3 +272,16 @@ def test_the_layout_of_what_an_iterator_yields():
     for given in (ps, iter(ps)):
         with pytest.raises(ValueError, match="CUDA"):
             adamw.require_dense(given)
+
+
+def test_negated_views_are_refused():
+    """Such a view's memory holds the values with the other sign (the imaginary part of a conjugate)."""
+    x = torch.complex(torch.zeros(256), torch.ones(256)).conj().imag
+    x = x.as_strided((128,), (1,))
+    assert x.is_neg() and x.is_contiguous()
+    with pytest.raises(ValueError, match="m must be"):
+        adamw._state(x, "m", torch.float32, 128, x.device)
+    with pytest.raises(ValueError, match="scale must be"):
+        adamw._one(x[:1], "scale", torch.float32, x.device)
+    y = torch.ones(128)
+    assert adamw._state(y, "m", torch.float32, 128, y.device) == adamw._one(y[:1], "scale", torch.float32, y.device) == y.data_ptr()
