@@ -31,6 +31,7 @@ from .muon import _place, _workspace
 
 _HERE = contextlib.nullcontext()
 BLOCK = 256   # elements of a tensor that share the scales of their 8-bit moments
+_FLT_MIN, _FLT_MAX = 2.0 ** -126, 2.0 ** 128 - 2.0 ** 104
 
 
 def starts(params) -> list[int]:
@@ -73,7 +74,8 @@ def require_dense(params) -> None:
 
 
 def layout(params) -> bytes:
-    """The types, shapes and strides of all parameters, which say how their moments lie."""
+    """The types, devices, shapes and strides of all parameters, which say how their moments lie and
+    whether the steps take them."""
     return _native().layout(params)
 
 
@@ -81,6 +83,13 @@ def missing(params, grads) -> int:
     """How many parameters have None for a gradient; -1 if the steps do not take some gradient
     as it is (fp32 or bf16, lying like its parameter)."""
     return _native().missing(params, grads)
+
+
+def check_numbers(lr, beta1, beta2, eps, wd) -> None:
+    """ValueError for numbers that the steps refuse."""
+    _L.require(0.0 <= beta1 < 1.0 and 0.0 <= beta2 < 1.0, "beta1 and beta2 must be in [0, 1)")
+    _L.require(_FLT_MIN <= eps <= _FLT_MAX, "eps must be positive and finite (a normal fp32)")
+    _L.require(math.isfinite(lr) and 0.0 <= wd < math.inf, "lr and weight decay must be finite, weight decay not negative")
 
 
 def _sequence(x):
@@ -165,19 +174,9 @@ def adamw_step(params, grads, m, v, t, lr=1e-3, beta1: float = 0.9, beta2: float
     factor (grad_norm's); NaN: nothing changes.  master: fp32 like m, the 32-bit
     copies of the bf16 parameters, which take the step in their place and are
     rounded into them."""
-    import torch
-    params, grads = _sequence(params), _sequence(grads)
-    rows, count, index, size = _native().rows(params, grads)
-    if not count:
-        return
-    device = torch.device("cuda", index)
-    state = _state(m, "m", torch.float32, size, device), _state(v, "v", torch.float32, size, device)
-    copy = None if master is None else _state(master, "master", torch.float32, size, device)
-    a = _arguments(t, lr, beta1, beta2, eps, wd, scale, device)
-    s, place = _stream(device, stream)
-    with place:
-        _L.check(_L.lib().ma_adamw_many_step(count, rows, C.byref(a), copy, *state, size, s))
-    _native().changed((m, v, master), params, grads)
+    call = step_call(params, grads, (m, v), t, lr, beta1, beta2, eps, wd, scale, master, stream)
+    if call:
+        call()
 
 
 def _moments8(cm, cv, sm, sr, size, device):
@@ -186,24 +185,46 @@ def _moments8(cm, cv, sm, sr, size, device):
             _state(sm, "sm", torch.float32, size // BLOCK, device), _state(sr, "sr", torch.float32, size // BLOCK, device))
 
 
+def step_call(params, grads, state, t, lr, beta1, beta2, eps, wd, scale=None, master=None, stream=None, apart=False):
+    """A function that makes the call of adamw_step (state: m, v) or adamw8_step (state: cm,
+    cv, sm, sr), after all that is looked at here has been: what a caller who makes several
+    of them needs in order to make all or none.  The library itself looks at the
+    numbers (check_numbers) and, here with `apart`, at whether parameters
+    overlap.  None if there is no gradient."""
+    import torch
+    params, grads = _sequence(params), _sequence(grads)
+    rows, count, index, size = _native().rows(params, grads)
+    if not count:
+        return None
+    device = torch.device("cuda", index)
+    if len(state) == 2:
+        fn = _L.lib().ma_adamw_many_step
+        at = _state(state[0], "m", torch.float32, size, device), _state(state[1], "v", torch.float32, size, device)
+    else:
+        fn = _L.lib().ma_adamw8_many_step
+        at = _moments8(*state, size, device)
+    copy = None if master is None else _state(master, "master", torch.float32, size, device)
+    a = _arguments(t, lr, beta1, beta2, eps, wd, scale, device)
+    if apart:
+        _L.require(not _native().overlap(params, grads), "two parameters overlap")
+    s, place = _stream(device, stream)
+
+    def call():
+        with place:
+            _L.check(fn(count, rows, C.byref(a), copy, *at, size, s))
+        _native().changed((*state, master), params, grads)
+
+    return call
+
+
 def adamw8_step(params, grads, cm, cv, sm, sr, t, lr=1e-3, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
                 wd: float = 0.0, scale=None, master=None, stream=None):
     """adamw_step with the moments in 8 bits: cm int8 and cv uint8 codes of
     state_size(params) elements, sm and sr fp32 scales of one for 256 of them,
     updated in place, all zeros before the first step."""
-    import torch
-    params, grads = _sequence(params), _sequence(grads)
-    rows, count, index, size = _native().rows(params, grads)
-    if not count:
-        return
-    device = torch.device("cuda", index)
-    state = _moments8(cm, cv, sm, sr, size, device)
-    copy = None if master is None else _state(master, "master", torch.float32, size, device)
-    a = _arguments(t, lr, beta1, beta2, eps, wd, scale, device)
-    s, place = _stream(device, stream)
-    with place:
-        _L.check(_L.lib().ma_adamw8_many_step(count, rows, C.byref(a), copy, *state, size, s))
-    _native().changed((cm, cv, sm, sr, master), params, grads)
+    call = step_call(params, grads, (cm, cv, sm, sr), t, lr, beta1, beta2, eps, wd, scale, master, stream)
+    if call:
+        call()
 
 
 def adamw8_values(cm, cv, sm, sr, stream=None):

@@ -10,7 +10,9 @@
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <exception>
+#include <utility>
 #include <vector>
 
 #include "microadam.h"
@@ -150,7 +152,33 @@ PyObject *missing(PyObject *, PyObject *args) {
   });
 }
 
-// layout(params) -> types, sizes and strides of all as bytes, to be compared
+// overlap(params, grads) -> whether two of the parameters with gradients, all dense, share memory
+PyObject *overlap(PyObject *, PyObject *args) {
+  PyObject *a, *b;
+  if (!PyArg_ParseTuple(args, "OO", &a, &b)) return nullptr;
+  const Ref ps(PySequence_Fast(a, "a sequence"));
+  if (!ps.o) return nullptr;
+  const Ref gs(PySequence_Fast(b, "a sequence"));
+  if (!gs.o) return nullptr;
+  return guarded([&]() -> PyObject * {
+    std::vector<std::pair<const char *, const char *>> spans;
+    bool sorted = true;
+    for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(ps.o) && i < PySequence_Fast_GET_SIZE(gs.o); ++i) {
+      if (items(gs)[i] == Py_None) continue;
+      const at::Tensor &p = tensor(items(ps)[i], "a tensor");
+      if (!p.numel()) continue;
+      const char *from = static_cast<const char *>(p.const_data_ptr());
+      if (!spans.empty() && from < spans.back().second) sorted = false;
+      spans.emplace_back(from, from + p.nbytes());
+    }
+    if (!sorted) std::sort(spans.begin(), spans.end());
+    for (size_t i = 1; i < spans.size(); ++i)
+      if (spans[i].first < spans[i - 1].second) Py_RETURN_TRUE;
+    Py_RETURN_FALSE;
+  });
+}
+
+// layout(params) -> types, devices, sizes and strides of all as bytes, to be compared
 PyObject *layout(PyObject *, PyObject *arg) {
   const Ref ps(PySequence_Fast(arg, "a sequence"));
   if (!ps.o) return nullptr;
@@ -159,6 +187,7 @@ PyObject *layout(PyObject *, PyObject *arg) {
     for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(ps.o); ++i) {
       const at::Tensor &p = tensor(items(ps)[i], "a tensor");
       out.push_back((int64_t)p.scalar_type());
+      out.push_back((int64_t)p.device().type() << 32 | (int64_t)(uint8_t)p.device().index() << 1 | (int64_t)p.is_neg());
       out.push_back(p.dim());
       out.insert(out.end(), p.sizes().begin(), p.sizes().end());
       out.insert(out.end(), p.strides().begin(), p.strides().end());
@@ -203,6 +232,7 @@ PyObject *stream(PyObject *, PyObject *arg) {
 PyMethodDef methods[] = {{"rows", rows, METH_VARARGS, nullptr},
                          {"grads", grads, METH_O, nullptr},
                          {"missing", missing, METH_VARARGS, nullptr},
+                         {"overlap", overlap, METH_VARARGS, nullptr},
                          {"layout", layout, METH_O, nullptr},
                          {"changed", changed, METH_VARARGS, nullptr},
                          {"stream", stream, METH_O, nullptr},

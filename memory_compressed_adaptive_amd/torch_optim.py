@@ -260,7 +260,8 @@ class AdamW(torch.optim.Optimizer):
     every replay.  A parameter without a gradient is left alone, its moments and its
     count of steps too.  Counts are kept on the GPU, one for all parameters that
     have had gradients at the same steps; these go in one call for each group.  A
-    captured step goes on with the parameters and counts it was captured with.
+    captured step goes on with the parameters and counts it was captured with.  A
+    step that is refused changes nothing in any group and is not counted.
     Gradients are float32 or bfloat16 as they are; others, and ones that lie unlike
     their parameter, are copied first.
     """
@@ -281,6 +282,7 @@ class AdamW(torch.optim.Optimizer):
         super().add_param_group(param_group)
         group = self.param_groups[-1]
         try:
+            _numbers(group)
             group["_moments"] = _moments(group, self.param_groups[0])
             group["_layout"] = _adamw.layout(group["params"])
             group["_slots"] = [self._histories if self._begun else 0] * len(group["params"])
@@ -306,8 +308,9 @@ class AdamW(torch.optim.Optimizer):
             raise ValueError("scale must be a float32 tensor of one element on the GPU")
         for group in self.param_groups:
             if _adamw.layout(group["params"]) != group["_layout"]:
-                raise RuntimeError("a parameter was converted or laid out anew after it was given to AdamW, whose moments "
+                raise RuntimeError("a parameter was moved, converted or laid out anew after it was given to AdamW, whose moments "
                                    "lie like it: make the optimizer afterwards")
+            _numbers(group)
         grads = [[p.grad for p in group["params"]] for group in self.param_groups]
         none = [_adamw.missing(group["params"], gs) for group, gs in zip(self.param_groups, grads)]
         for i, (group, gs) in enumerate(zip(self.param_groups, grads)):
@@ -319,26 +322,32 @@ class AdamW(torch.optim.Optimizer):
         slots = [0] if self._histories == 1 and not any(none) else self._part(grads)
         self._begun = True
         counts = [self._counts[s] for s in slots]
+        norm = None
         if self.max_norm is not None:
-            # the norm's call counts the step where there is one count to raise
-            self.grad_norm, scale = _adamw.grad_norm([g for gs in grads for g in gs], self.max_norm,
-                                                     t=counts[0] if len(slots) == 1 else None)
-        if self.max_norm is None or len(slots) > 1:
-            taken = 1 if scale is None else (scale == scale).reshape(1)
-            for count in counts:
-                count.add_(taken)
+            out = torch.empty(2, dtype=torch.float32, device=counts[0].device)
+            norm, scale = out.unbind()
+        # All calls are looked at before the first one is made and the step is counted: a step is
+        # taken by all groups or refused.
+        calls = []
         for group, gs in zip(self.param_groups, grads):
             st, (b1, b2) = group["_moments"], group["betas"]
-            kw = dict(lr=group["lr"], beta1=b1, beta2=b2, eps=group["eps"], wd=group["weight_decay"], scale=scale,
-                      master=st.get("master"))
+            state = [st[k] for k in (("cm", "cv", "sm", "sr") if "cm" in st else ("m", "v")) if k in st]
             for slot, count in zip(slots, counts):
                 some = gs if len(slots) == 1 else [g if s == slot else None for s, g in zip(group["_slots"], gs)]
                 if all(g is None for g in some):
                     continue
-                if "cm" in st:
-                    _adamw.adamw8_step(group["params"], some, st["cm"], st["cv"], st["sm"], st["sr"], count, **kw)
-                else:
-                    _adamw.adamw_step(group["params"], some, st["m"], st["v"], count, **kw)
+                calls.append(_adamw.step_call(group["params"], some, state, count, group["lr"], b1, b2, group["eps"], group["weight_decay"],
+                                              scale=scale, master=st.get("master"), apart=True))
+        if norm is not None:
+            # the norm's call counts the step where there is one count to raise
+            _adamw.grad_norm([g for gs in grads for g in gs], self.max_norm, t=counts[0] if len(slots) == 1 else None, out=out)
+            self.grad_norm = norm
+        if norm is None or len(slots) > 1:
+            taken = 1 if scale is None else (scale == scale).reshape(1)
+            for count in counts:
+                count.add_(taken)
+        for call in calls:
+            call()
         return loss
 
     def _part(self, grads):
@@ -391,6 +400,12 @@ class AdamW(torch.optim.Optimizer):
         self._begun = self._histories > 1 or any(saved["counts"])
         for count, n in zip_longest(self._counts, saved["counts"], fillvalue=0):
             count.fill_(n)
+
+
+def _numbers(group):
+    """ValueError for a group's numbers that the steps refuse."""
+    (b1, b2), lr = group["betas"], group["lr"]
+    _adamw.check_numbers(0.0 if torch.is_tensor(lr) else lr, b1, b2, group["eps"], group["weight_decay"])
 
 
 def _like(g, p):

@@ -320,3 +320,43 @@ def test_a_kept_graph_is_not_used_with_new_parameters():
         first.backward()
     still.grad = None
     (x @ w).sum().backward()
+
+
+@pytest.mark.parametrize("bits,max_norm", [(32, None), (32, 1e-2), (8, None), (8, 1e-2)])
+def test_a_refused_step_changes_nothing(bits, max_norm):
+    """Put right and taken again it is the step that it would have been."""
+    ps, qs = _params(15), _params(15)
+    kw = dict(lr=1e-2, state_bits=bits, max_norm=max_norm)
+    a, b = (AdamW([{"params": x[:2]}, {"params": x[2:]}], **kw) for x in (ps, qs))
+    bad = [dict(eps=0.0), dict(betas=(0.9, 1.0)), dict(weight_decay=-0.1), dict(lr=torch.ones(1)), dict(lr=math.nan),
+           dict(lr=torch.ones(1, dtype=torch.float64, device="cuda")), dict(lr=torch.ones(2, device="cuda"))]
+
+    def everything():
+        return [x.clone() for x in ps] + [v.clone() for g in a.param_groups for v in g["_moments"].values() if torch.is_tensor(v)]
+
+    for t, wrong in enumerate(bad):
+        for p, q, g in zip(ps, qs, _grads(80 + t)):
+            p.grad, q.grad = g, g.clone()
+        before, counts = everything(), a.state_dict()["adamw"]["counts"]
+        group = a.param_groups[1]
+        kept = {k: group[k] for k in wrong}
+        group.update(wrong)
+        with pytest.raises(ValueError):
+            a.step()
+        assert all(torch.equal(x, y) for x, y in zip(before, everything())) and a.state_dict()["adamw"]["counts"] == counts
+        group.update(kept)
+        own, ps[4].data = ps[4].data, ps[3].data.view(-1)[7:520]
+        with pytest.raises(ValueError, match="overlap"):
+            a.step()
+        ps[4].data = own
+        with pytest.raises(ValueError):
+            a.step(scale=torch.ones(1)) if max_norm is None else a.step(scale=torch.ones(1, device="cuda"))
+        assert all(torch.equal(x, y) for x, y in zip(before, everything())) and a.state_dict()["adamw"]["counts"] == counts
+        a.step(), b.step()
+        assert all(torch.equal(p, q) for p, q in zip(ps, qs)), t
+    where = ps[0].data
+    ps[0].data = where.cpu()
+    with pytest.raises(RuntimeError, match="moved"):
+        a.step()
+    ps[0].data = where
+    assert a.state_dict()["adamw"]["counts"] == [len(bad)]

@@ -1,8 +1,11 @@
 """Argument checks of torch_optim.AdamW that need no GPU."""
+import ctypes as C
+import math
+
 import pytest
 import torch
 
-from memory_compressed_adaptive_amd import torch_optim
+from memory_compressed_adaptive_amd import _lib, torch_optim
 from memory_compressed_adaptive_amd.torch_optim import AdamW
 
 
@@ -119,3 +122,180 @@ def test_gradients_are_copied_only_where_they_must_be():
     assert torch_optim._like(torch.ones(4, 6), turned).stride() == turned.stride()
     with pytest.raises(ValueError, match="sparse"):
         torch_optim._like(torch.ones(4, 6).to_sparse(), p)
+
+
+class _Library:
+    """Refuses numbers as the library does, counts what it is asked to do and launches nothing."""
+
+    def __init__(self):
+        self.real, self.calls = _lib.lib(), []
+
+    def ma_grad_norm_workspace(self, count):
+        return 0
+
+    def ma_grad_norm(self, count, rows, max_norm, out, t, *rest):
+        if not max_norm > 0:
+            return self.real.ma_grad_norm(0, None, max_norm, None, None, None, 0, None)
+        if t:
+            C.cast(t, C.POINTER(C.c_int64))[0] += 1
+        self.calls.append("norm")
+        return 0
+
+    def ma_adamw_many_step(self, count, rows, args, *rest):
+        code = self.real.ma_adamw_many_step(0, None, args, None, None, None, 0, None)
+        if code == 0:
+            self.calls.append("step")
+        return code
+
+    def __getattr__(self, name):
+        return getattr(self.real, name)
+
+
+def _without_a_gpu(monkeypatch):
+    """The optimizer over CPU parameters, with the library's calls made to a stand-in."""
+    from memory_compressed_adaptive_amd import adamw
+    native, library = adamw._native(), _Library()
+
+    class Native:
+        def rows(self, params, grads):
+            return b"", sum(g is not None for g in grads), 0, adamw.state_size(params)
+
+        def grads(self, grads):
+            return b"", len(grads), 0
+
+        def stream(self, index):
+            return 7
+
+        def changed(self, *lists):
+            pass
+
+        def __getattr__(self, name):
+            return getattr(native, name)
+
+    def moments(group, first):
+        n = adamw.state_size(group["params"])
+        return {"layout": [], "m": torch.zeros(n), "v": torch.zeros(n)}
+
+    def one(t, what, dtype, device):
+        if t.dtype != dtype or t.numel() != 1:
+            raise ValueError(what)
+        return t.data_ptr()
+
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **kw: empty(*a, **kw))
+    monkeypatch.setattr(adamw, "_native", lambda: Native())
+    monkeypatch.setattr(adamw, "_state", lambda t, *rest: t.data_ptr())
+    monkeypatch.setattr(adamw, "_one", one)
+    monkeypatch.setattr(adamw, "_workspace", lambda nbytes, device: empty(nbytes, dtype=torch.uint8))
+    monkeypatch.setattr(_lib, "lib", lambda: library)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch_optim, "_moments", moments)
+    return library.calls
+
+
+BAD_NUMBERS = [dict(eps=0.0), dict(eps=math.nan), dict(betas=(1.0, 0.999)), dict(betas=(0.9, -0.1)), dict(betas=(0.9, math.nan)),
+               dict(weight_decay=-0.1), dict(weight_decay=math.inf), dict(lr=math.inf), dict(lr=math.nan), dict(eps=1e-40), dict(eps=1e39)]
+
+
+@pytest.mark.parametrize("bad", BAD_NUMBERS + [dict(lr=torch.ones(1, dtype=torch.float64)), dict(lr=torch.ones(2)), dict(betas=(0.9,)),
+                                               dict(eps=None), dict(weight_decay="0.1")])
+@pytest.mark.parametrize("max_norm", [None, 1.0])
+@pytest.mark.parametrize("histories", [1, 2])
+def test_a_refused_step_is_not_counted(monkeypatch, bad, max_norm, histories):
+    calls = _without_a_gpu(monkeypatch)
+    ps = [_p(4), _p(4), _p(4)]
+    opt = AdamW([{"params": ps[:2]}, {"params": ps[2:]}], max_norm=max_norm)
+    for p in ps[:1] if histories == 2 else ps:
+        p.grad = torch.ones(4)
+    opt.step()
+    for p in ps:
+        p.grad = torch.ones(4)
+    calls.clear()
+    before = opt.state_dict()["adamw"]["counts"]
+    group = opt.param_groups[1]
+    kept = {k: group[k] for k in bad}
+    group.update(bad)
+    for _ in range(2):
+        with pytest.raises((ValueError, TypeError)):
+            opt.step()
+    assert opt.state_dict()["adamw"]["counts"] == before and calls == []
+    group.update(kept)
+    opt.step()
+    assert opt.state_dict()["adamw"]["counts"] == [n + 1 for n in before] and calls.count("step") == 2 + (histories == 2)
+
+
+def test_a_step_whose_norm_is_refused_is_not_counted(monkeypatch):
+    calls = _without_a_gpu(monkeypatch)
+    p = _p(4)
+    p.grad = torch.ones(4)
+    opt = AdamW([p], max_norm=1.0)
+    opt.max_norm = -1.0
+    with pytest.raises(_lib.MicroAdamError, match="max_norm"):
+        opt.step()
+    assert opt.state_dict()["adamw"]["counts"] == [0] and calls == []
+
+
+@pytest.mark.parametrize("max_norm", [None, 1.0])
+def test_a_step_of_overlapping_parameters_is_not_counted(monkeypatch, max_norm):
+    """Tied after the optimizer was made, as a model's head and embedding may be."""
+    calls = _without_a_gpu(monkeypatch)
+    ps = [_p(4), _p(4), _p(4)]
+    opt = AdamW([{"params": ps[:1]}, {"params": ps[1:]}], max_norm=max_norm)
+    for p in ps:
+        p.grad = torch.ones(4)
+    opt.step()
+    calls.clear()
+    ps[2].data = ps[1].data
+    with pytest.raises(ValueError, match="overlap"):
+        opt.step()
+    assert opt.state_dict()["adamw"]["counts"] == [1] and calls == []
+    ps[2].grad = None            # not written: no overlap
+    opt.step()
+    ps[2].data, ps[2].grad = torch.zeros(4), torch.ones(4)
+    opt.step()
+    assert sorted(opt.state_dict()["adamw"]["counts"]) == [2, 3]
+
+
+@pytest.mark.parametrize("bad", BAD_NUMBERS)
+def test_a_group_with_bad_numbers_is_not_kept(monkeypatch, bad):
+    monkeypatch.setattr(torch_optim, "_moments", lambda group, first: {"layout": []})
+    with pytest.raises(ValueError):
+        AdamW([_p(4)], **bad)
+    opt = AdamW([_p(4)])
+    with pytest.raises(ValueError):
+        opt.add_param_group({"params": [_p(4)], **bad})
+    assert len(opt.param_groups) == 1
+
+
+@pytest.mark.parametrize("what", ["lr", "beta1", "beta2", "eps", "wd"])
+def test_the_numbers_refused_are_the_librarys(what):
+    """The step's look at its numbers and the library's, at both sides of each border."""
+    from memory_compressed_adaptive_amd import adamw
+    tiny, huge = 2.0 ** -126, float(torch.finfo(torch.float32).max)
+    for x in (0.0, -0.0, 1.0, math.nextafter(1.0, 0.0) if hasattr(math, "nextafter") else 1.0 - 2.0 ** -53, tiny, tiny * (1 - 2.0 ** -53), huge,
+              huge * (1 + 2.0 ** -52), 1e300, -1e-300, -1.0, math.inf, -math.inf, math.nan, 5e-324, 1, 0):
+        kw = {**dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, wd=0.0), what: x}
+        code = _lib.lib().ma_adamw_many_step(0, None, C.byref(_lib.AdamwArgs(**kw, t=1)), None, None, None, 0, None)
+        try:
+            adamw.check_numbers(**kw)
+            taken = True
+        except ValueError:
+            taken = False
+        assert taken == (code == 0), (what, x)
+
+
+def test_a_moved_parameter_is_found():
+    from memory_compressed_adaptive_amd import adamw
+    p = torch.zeros(3, 4)
+    kinds = [p, p.to("meta"), p.bfloat16(), p.t(), p.view(12), torch._neg_view(p)]
+    assert len({adamw.layout([x]) for x in kinds}) == len(kinds)
+    assert adamw.layout([p]) == adamw.layout([p.clone()])
+
+
+def test_overlap():
+    from memory_compressed_adaptive_amd import adamw
+    x, y = torch.zeros(10), torch.zeros(10, dtype=torch.bfloat16)
+    overlap = lambda ps, gs=None: adamw._native().overlap(ps, gs or ps)  # noqa: E731
+    assert not overlap([]) and not overlap([x]) and not overlap([x[5:], y, x[:5]]) and not overlap([x[3:3], x[:5], x[5:5], x[5:]])
+    assert overlap([x, x]) and overlap([x[:5], x[4:]]) and overlap([x[4:], y, x[:5]]) and overlap([x, x[2:3]]) and overlap([y[:6], y[5:]])
+    assert not overlap([x, x], [x, None]) and not overlap([x, y, x], [None, y, x])
