@@ -283,7 +283,7 @@ class AdamW(torch.optim.Optimizer):
         group = self.param_groups[-1]
         try:
             _numbers(group)
-            group["_moments"] = _moments(group, self.param_groups[0])
+            group["_moments"] = _moments(group, next((g for g in self.param_groups if g["params"]), group))
             group["_layout"] = _adamw.layout(group["params"])
             group["_slots"] = [self._histories if self._begun else 0] * len(group["params"])
             if group["params"]:

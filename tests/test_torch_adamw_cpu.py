@@ -299,3 +299,18 @@ def test_overlap():
     assert not overlap([]) and not overlap([x]) and not overlap([x[5:], y, x[:5]]) and not overlap([x[3:3], x[:5], x[5:5], x[5:]])
     assert overlap([x, x]) and overlap([x[:5], x[4:]]) and overlap([x[4:], y, x[:5]]) and overlap([x, x[2:3]]) and overlap([y[:6], y[5:]])
     assert not overlap([x, x], [x, None]) and not overlap([x, y, x], [None, y, x])
+
+
+def test_the_device_is_that_of_the_first_parameter(monkeypatch):
+    """Also where the first group is an empty one: counts and norm are on one device."""
+    asked = []
+
+    def moments(group, first):
+        asked.append(first["params"])
+        return {"layout": []}
+
+    monkeypatch.setattr(torch_optim, "_moments", moments)
+    p, q = _p(1), _p(2)
+    opt = AdamW([{"params": []}, {"params": [p]}, {"params": [q]}])
+    opt.add_param_group({"params": [_p(3)]})
+    assert [[x is p for x in ps] for ps in asked] == [[], [True], [True], [True]]
