@@ -370,6 +370,21 @@ class AdamW(torch.optim.Optimizer):
             slots[i] = new[s]
         return sorted(has)
 
+    def __getstate__(self):
+        """What copy.deepcopy and pickle take: the counts too, as one tensor."""
+        return {**super().__getstate__(), "max_norm": self.max_norm, "grad_norm": self.grad_norm, "_histories": self._histories,
+                "_begun": self._begun, "_counts": torch.cat(self._counts) if self._counts else None}
+
+    def __setstate__(self, state):
+        if "_counts" in state:   # (not where torch loads a state dictionary)
+            counts = state["_counts"]
+            state = {**state, "_counts": [] if counts is None else list(counts.split(1))}
+        super().__setstate__(state)
+        for g in self.param_groups:
+            # unpickled onto another device, moments and all
+            if "_moments" in g and g["_moments"]["layout"] == [(tuple(p.shape), p.stride()) for p in g["params"]]:
+                g["_layout"] = _adamw.layout(g["params"])
+
     def state_dict(self):
         """The usual dictionary, and under "adamw" the counts and every group's moments as they are."""
         sd = super().state_dict()

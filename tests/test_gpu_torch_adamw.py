@@ -1,6 +1,8 @@
 """torch_optim.AdamW: its steps are those of the operators on the same lists, alone and
 beside Muon and MicroAdamW, clipped and not, captured and not, and its state round-trips."""
+import copy
 import math
+import pickle
 
 import pytest
 import torch
@@ -360,3 +362,31 @@ def test_a_refused_step_changes_nothing(bits, max_norm):
         a.step()
     ps[0].data = where
     assert a.state_dict()["adamw"]["counts"] == [len(bad)]
+
+
+@pytest.mark.parametrize("how", ["deepcopy", "pickle"])
+@pytest.mark.parametrize("bits,copies", [(32, False), (8, True)])
+def test_a_copy_goes_on_as_the_original(how, bits, copies):
+    ps = _params(16, (BF16, F32))
+    ps[0] = torch.nn.Parameter(ps[0].detach().t().contiguous().t())      # a dense layout of its own
+    a = AdamW([{"params": ps[:2]}, {"params": ps[2:]}], lr=1e-2, state_bits=bits, master_weights=copies, max_norm=1e-2)
+
+    def step(opt, t, but=None):
+        flat = [p for g in opt.param_groups for p in g["params"]]
+        for i, (p, g) in enumerate(zip(flat, _grads(90 + t))):
+            p.grad = None if i == but else g.to(p.dtype)
+        opt.step()
+        return flat
+
+    step(a, 0), step(a, 1, but=3)
+    b = copy.deepcopy(a) if how == "deepcopy" else pickle.loads(pickle.dumps(a))
+    norm = float(a.grad_norm)
+    assert float(b.grad_norm) == norm
+    for t in range(2, 5):
+        xs, ys = step(a, t), step(b, t)
+        assert all(torch.equal(x, y) and x.data_ptr() != y.data_ptr() for x, y in zip(xs, ys)), t
+        assert float(a.grad_norm) == float(b.grad_norm) != norm
+    before = [x.clone() for x in ys]
+    step(a, 5)
+    assert all(torch.equal(x, y) for x, y in zip(before, ys))
+    assert a.state_dict()["adamw"]["counts"] == [6, 5] and b.state_dict()["adamw"]["counts"] == [5, 4]

@@ -1,6 +1,9 @@
 """Argument checks of torch_optim.AdamW that need no GPU."""
+import copy
 import ctypes as C
+import io
 import math
+import pickle
 
 import pytest
 import torch
@@ -314,3 +317,44 @@ def test_the_device_is_that_of_the_first_parameter(monkeypatch):
     opt = AdamW([{"params": []}, {"params": [p]}, {"params": [q]}])
     opt.add_param_group({"params": [_p(3)]})
     assert [[x is p for x in ps] for ps in asked] == [[], [True], [True], [True]]
+
+
+def _duplicates():
+    def through(dump, load):
+        def f(opt):
+            buffer = io.BytesIO()
+            dump(opt, buffer)
+            buffer.seek(0)
+            return load(buffer)
+        return f
+    return [copy.deepcopy, through(pickle.dump, pickle.load), through(torch.save, lambda f: torch.load(f, weights_only=False))]
+
+
+@pytest.mark.parametrize("duplicate", _duplicates(), ids=["deepcopy", "pickle", "torch.save"])
+@pytest.mark.parametrize("max_norm", [None, 1.0])
+def test_a_copy_goes_on_by_itself(monkeypatch, duplicate, max_norm):
+    calls = _without_a_gpu(monkeypatch)
+    opt = AdamW([{"params": [_p(4), _p(4)]}, {"params": [_p(4)]}], max_norm=max_norm)
+    opt.param_groups[0]["params"][0].grad = torch.ones(4)
+    opt.step()
+    other = duplicate(opt)
+    assert other.max_norm == max_norm and (other.grad_norm is None) == (max_norm is None)
+    assert other.state_dict()["adamw"]["counts"] == opt.state_dict()["adamw"]["counts"] == [1, 0]
+    for g in other.param_groups:
+        for p in g["params"]:
+            p.grad = torch.ones(4)
+    calls.clear()
+    other.step()
+    assert calls.count("step") == 3 and calls.count("norm") == (max_norm is not None)
+    assert other.state_dict()["adamw"]["counts"] == [2, 1] and opt.state_dict()["adamw"]["counts"] == [1, 0]
+    other.add_param_group({"params": [_p(5)]})
+    again = AdamW([{"params": [_p(4), _p(4)]}, {"params": [_p(4)]}, {"params": [_p(5)]}])
+    again.load_state_dict(other.state_dict())
+    assert again.state_dict()["adamw"]["counts"] == [2, 1, 0]
+
+
+def test_a_copy_of_an_optimizer_without_parameters(monkeypatch):
+    monkeypatch.setattr(torch_optim, "_moments", lambda group, first: {"layout": []})
+    opt = copy.deepcopy(AdamW([{"params": []}]))
+    opt.add_param_group({"params": [_p(3)]})
+    assert opt.state_dict()["adamw"]["counts"] == [0]
