@@ -382,7 +382,7 @@ class AdamW(torch.optim.Optimizer):
         super().__setstate__(state)
         for g in self.param_groups:
             # unpickled onto another device, moments and all
-            if "_moments" in g and g["_moments"]["layout"] == [(tuple(p.shape), p.stride()) for p in g["params"]]:
+            if "_moments" in g and all(g["_moments"].get(k) == v for k, v in _kinds(g["params"]).items()):
                 g["_layout"] = _adamw.layout(g["params"])
 
     def state_dict(self):
@@ -399,12 +399,19 @@ class AdamW(torch.optim.Optimizer):
         return sd
 
     def load_state_dict(self, state_dict):
+        """Moments, copies and counts are written where this optimizer's lie."""
         saved, mine = state_dict["adamw"], [(g["_moments"], g["_layout"]) for g in self.param_groups]
         same = len(saved["groups"]) == len(mine) and all(
-            a.keys() == b.keys() and [tuple(map(tuple, x)) for x in a["layout"]] == b["layout"]
+            a.keys() | {"types"} == b.keys() | {"types"} and [tuple(map(tuple, x)) for x in a["layout"]] == b["layout"]
             for a, (b, _) in zip(saved["groups"], mine))
         if not same:
             raise ValueError("the saved moments are those of other parameters, layouts, state_bits or master_weights")
+        # Moments are the same in either type, but a copy is kept of bfloat16 parameters only.  (States were
+        # saved without types at first; then they are taken to be those of the parameters now.)
+        for a, (b, _) in zip(saved["groups"], mine):
+            if "master" in b and any(y == "bfloat16" != x for x, y in zip(a.get("types", b["types"]), b["types"])):
+                raise ValueError("a bfloat16 parameter was float32 when its state was saved, without a 32-bit copy: load into "
+                                 "parameters of the types that were saved")
         super().load_state_dict({"state": state_dict["state"], "param_groups": [dict(g) for g in state_dict["param_groups"]]})
         for g, (st, layout), new, slots in zip(self.param_groups, mine, saved["groups"], saved["slots"]):
             g["_moments"], g["_layout"], g["_slots"] = st, layout, list(slots)
@@ -433,6 +440,11 @@ def _like(g, p):
     return torch.empty_like(p, dtype=dtype, memory_format=torch.preserve_format).copy_(g)
 
 
+def _kinds(ps):
+    """What a group's state says of its parameters."""
+    return {"layout": [(tuple(p.shape), p.stride()) for p in ps], "types": [str(p.dtype).replace("torch.", "") for p in ps]}
+
+
 def _moments(group, first):
     """A group's moments, and the 32-bit copies of its bfloat16 parameters."""
     ps = group["params"]
@@ -447,7 +459,7 @@ def _moments(group, first):
             raise ValueError("parameters must be float32 or bfloat16")
         if p.device != (first["params"] or ps)[0].device:
             raise ValueError("the parameters must share a device")
-    st = {"layout": [(tuple(p.shape), p.stride()) for p in ps]}
+    st = _kinds(ps)
     if not ps:
         return st
     size, device = _adamw.state_size(ps), ps[0].device
@@ -460,5 +472,6 @@ def _moments(group, first):
     if group["master_weights"] and any(p.dtype == torch.bfloat16 for p in ps):
         st["master"] = zeros(size)
         for view, p in zip(_adamw.views(st["master"], ps), ps):
-            view.copy_(p.detach())
+            if p.dtype == torch.bfloat16:
+                view.copy_(p.detach())
     return st

@@ -390,3 +390,24 @@ def test_a_copy_goes_on_as_the_original(how, bits, copies):
     step(a, 5)
     assert all(torch.equal(x, y) for x, y in zip(before, ys))
     assert a.state_dict()["adamw"]["counts"] == [6, 5] and b.state_dict()["adamw"]["counts"] == [5, 4]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_load_with_copies_goes_by_the_types_saved(bits):
+    """A parameter of 32 bits has no copy that a 16-bit one could go on from."""
+    def make(seed, dtypes):
+        return AdamW(_params(seed, dtypes), lr=1e-2, state_bits=bits, master_weights=True)
+
+    a = make(17, (BF16, F32))
+    for p, g in zip(a.param_groups[0]["params"], _grads(17)):
+        p.grad = g
+    a.step()
+    with pytest.raises(ValueError, match="32-bit copy"):
+        make(18, (BF16,)).load_state_dict(a.state_dict())
+    b = make(18, (BF16, F32))
+    b.load_state_dict(a.state_dict())
+    for x, y in zip(a.param_groups[0]["params"], b.param_groups[0]["params"]):
+        y.data.copy_(x.data)
+        y.grad = x.grad.clone()
+    a.step(), b.step()
+    assert all(torch.equal(x, y) for x, y in zip(a.param_groups[0]["params"], b.param_groups[0]["params"]))

@@ -358,3 +358,82 @@ def test_a_copy_of_an_optimizer_without_parameters(monkeypatch):
     opt = copy.deepcopy(AdamW([{"params": []}]))
     opt.add_param_group({"params": [_p(3)]})
     assert opt.state_dict()["adamw"]["counts"] == [0]
+
+
+def _moments_on_the_cpu(monkeypatch):
+    """The real moments, for CPU parameters that say they are CUDA ones where they are looked at."""
+    real = torch_optim._moments
+
+    class On:
+        """A parameter whose device is of type cuda, and which makes its tensors on the CPU."""
+
+        class device:
+            type = "cuda"
+
+        def __init__(self, p):
+            self._p = p
+
+        def __getattr__(self, name):
+            return getattr(self._p, name)
+
+    zeros = torch.zeros
+    monkeypatch.setattr(torch, "zeros", lambda *a, device=None, **kw: zeros(*a, **kw))
+    monkeypatch.setattr(torch_optim._adamw, "require_dense", lambda ps: None)
+    monkeypatch.setattr(torch_optim, "_moments", lambda group, first: real({**group, "params": [On(p) for p in group["params"]]},
+                                                                           {"params": [On(p) for p in first["params"]][:0]}))
+    return zeros
+
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def _filled(dtypes, value, **kw):
+    return AdamW([torch.nn.Parameter(torch.full((4, 3), value).to(d)) for d in dtypes], master_weights=True, **kw)
+
+
+def test_copies_are_of_16_bit_parameters_alone(monkeypatch):
+    """Those of others would go stale: no step uses them."""
+    _moments_on_the_cpu(monkeypatch)
+    master = _filled((BF16, F32), 1.0).param_groups[0]["_moments"]["master"]
+    assert bool((master[:12] == 1).all()) and not bool(master[12:].any())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_load_refuses_types_whose_copies_were_not_kept(monkeypatch, bits):
+    """fp32 when saved and bf16 now: the parameter would go on from a copy that no step had written."""
+    _moments_on_the_cpu(monkeypatch)
+    saved = _filled((BF16, F32), 1.0, state_bits=bits).state_dict()
+    now = _filled((BF16, BF16), 5.0, state_bits=bits)
+    with pytest.raises(ValueError, match="saved"):
+        now.load_state_dict(saved)
+    assert bool((now.param_groups[0]["_moments"]["master"][:12] == 5).all())
+    for dtypes in ((BF16, F32), (F32, BF16)):
+        opt = _filled(dtypes, 5.0, state_bits=bits)
+        if dtypes == (F32, BF16):
+            with pytest.raises(ValueError, match="saved"):
+                opt.load_state_dict(saved)
+        else:
+            opt.load_state_dict(saved)
+            assert bool((opt.param_groups[0]["_moments"]["master"][:12] == 1).all())
+    _filled((BF16, F32), 5.0, state_bits=bits).load_state_dict(_filled((BF16, BF16), 1.0, state_bits=bits).state_dict())
+
+
+def test_load_takes_other_types_without_copies(monkeypatch):
+    """Moments are the same in either type."""
+    _moments_on_the_cpu(monkeypatch)
+    a, b = (AdamW([torch.nn.Parameter(torch.zeros(4, 3, dtype=d))]) for d in (F32, BF16))
+    a.param_groups[0]["_moments"]["m"].fill_(3.0)
+    b.load_state_dict(a.state_dict())
+    assert bool((b.param_groups[0]["_moments"]["m"] == 3).all())
+
+
+def test_load_takes_states_that_were_saved_without_types(monkeypatch):
+    """As this optimizer saved them at first: they are taken to be of the parameters' types now."""
+    _moments_on_the_cpu(monkeypatch)
+    saved = _filled((BF16, F32), 1.0).state_dict()
+    for st in saved["adamw"]["groups"]:
+        assert st.pop("types") == ["bfloat16", "float32"]
+    opt = _filled((BF16, F32), 5.0)
+    opt.load_state_dict(saved)
+    assert bool((opt.param_groups[0]["_moments"]["master"][:12] == 1).all())
+    assert opt.state_dict()["adamw"]["groups"][0]["types"] == ["bfloat16", "float32"]
