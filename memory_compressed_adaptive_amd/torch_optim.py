@@ -399,7 +399,8 @@ class AdamW(torch.optim.Optimizer):
         return sd
 
     def load_state_dict(self, state_dict):
-        """Moments, copies and counts are written where this optimizer's lie."""
+        """Moments, copies, counts and an lr that is a tensor are written where this optimizer's lie, so
+        that a captured step goes on with them."""
         saved, mine = state_dict["adamw"], [(g["_moments"], g["_layout"]) for g in self.param_groups]
         same = len(saved["groups"]) == len(mine) and all(
             a.keys() | {"types"} == b.keys() | {"types"} and [tuple(map(tuple, x)) for x in a["layout"]] == b["layout"]
@@ -412,7 +413,17 @@ class AdamW(torch.optim.Optimizer):
             if "master" in b and any(y == "bfloat16" != x for x, y in zip(a.get("types", b["types"]), b["types"])):
                 raise ValueError("a bfloat16 parameter was float32 when its state was saved, without a 32-bit copy: load into "
                                  "parameters of the types that were saved")
+        rates, shared = [g["lr"] for g in self.param_groups], {}
+        for lr, g in zip(rates, state_dict["param_groups"]):
+            if torch.is_tensor(lr) and shared.setdefault(id(lr), float(g["lr"])) != float(g["lr"]):
+                raise ValueError("groups share one tensor for lr, and other rates were saved for them")
         super().load_state_dict({"state": state_dict["state"], "param_groups": [dict(g) for g in state_dict["param_groups"]]})
+        for g, lr in zip(self.param_groups, rates):
+            if torch.is_tensor(lr):
+                lr.fill_(float(g["lr"]))
+                g["lr"] = lr
+            elif torch.is_tensor(g["lr"]) and g["params"]:
+                g["lr"] = g["lr"].to(g["params"][0].device)
         for g, (st, layout), new, slots in zip(self.param_groups, mine, saved["groups"], saved["slots"]):
             g["_moments"], g["_layout"], g["_slots"] = st, layout, list(slots)
             for k, v in new.items():

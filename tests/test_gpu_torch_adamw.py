@@ -411,3 +411,49 @@ def test_load_with_copies_goes_by_the_types_saved(bits):
         y.grad = x.grad.clone()
     a.step(), b.step()
     assert all(torch.equal(x, y) for x, y in zip(a.param_groups[0]["params"], b.param_groups[0]["params"]))
+
+
+def test_a_captured_step_goes_on_after_a_load(tmp_path):
+    """Moments, counts and the rate are read where they were when the step was captured."""
+    ps, qs = _params(19, (BF16, F32)), _params(19, (BF16, F32))
+    kw = dict(weight_decay=0.1, state_bits=8, master_weights=True, max_norm=1e-2)
+    rate = torch.full((1,), 0.01, device="cuda")
+    captured, eager = AdamW(ps, lr=rate, **kw), AdamW(qs, lr=0.01, **kw)
+    for p, q, g in zip(ps, qs, _grads(19)):
+        p.grad, q.grad = g.to(p.dtype), g.to(p.dtype)
+    captured.step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured.step()
+    for t in range(3):
+        graph.replay()
+        eager.step()
+        torch.cuda.synchronize()
+    eager.param_groups[0]["lr"] = 2.0 ** -7
+    for saved in (0, 1):
+        torch.save((eager.state_dict(), [q.detach() for q in qs]), tmp_path / "state")
+        sd, values = torch.load(tmp_path / "state", weights_only=True, map_location="cpu")
+        captured.load_state_dict(sd)
+        for p, x in zip(ps, values):
+            p.data.copy_(x)
+        assert captured.param_groups[0]["lr"] is rate and float(rate) == 2.0 ** -7
+        for t in range(3):
+            for p, q, g in zip(ps, qs, _grads(120 + 3 * saved + t)):
+                p.grad.copy_(g)
+                q.grad.copy_(g)
+            graph.replay()
+            eager.step()
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip(ps, qs)), (saved, t)
+        captured.step(), eager.step()
+        assert all(torch.equal(p, q) for p, q in zip(ps, qs))
+    other = AdamW(_params(20, (BF16, F32)), **kw)     # a number before: the saved tensor, on the parameters' device
+    torch.save(captured.state_dict(), tmp_path / "state")
+    other.load_state_dict(torch.load(tmp_path / "state", weights_only=True, map_location="cpu"))
+    assert other.param_groups[0]["lr"].is_cuda
+    for p, x in zip(other.param_groups[0]["params"], ps):
+        p.data.copy_(x.data)
+        p.grad = x.grad.clone()
+    other.step(), captured.step()
+    assert all(torch.equal(p, q) for p, q in zip(ps, other.param_groups[0]["params"]))

@@ -437,3 +437,41 @@ def test_load_takes_states_that_were_saved_without_types(monkeypatch):
     opt.load_state_dict(saved)
     assert bool((opt.param_groups[0]["_moments"]["master"][:12] == 1).all())
     assert opt.state_dict()["adamw"]["groups"][0]["types"] == ["bfloat16", "float32"]
+
+
+def _rated(lr, *more):
+    return AdamW([{"params": [_p(4)], "lr": lr}, *({"params": [_p(4)], "lr": x} for x in more)])
+
+
+@pytest.mark.parametrize("shape", [(1,), ()])
+@pytest.mark.parametrize("saved", [0.25, torch.tensor(0.25), torch.tensor([0.25], dtype=torch.float64)], ids=["number", "0-d", "1-d of 64 bits"])
+def test_load_writes_a_rate_where_it_lies(monkeypatch, shape, saved):
+    """A captured step reads it there."""
+    monkeypatch.setattr(torch_optim, "_moments", lambda group, first: {"layout": []})
+    rate = torch.full(shape, 0.5)
+    opt = _rated(rate, 3.0)
+    state = _rated(saved, 2.0).state_dict()
+    opt.load_state_dict(state)
+    assert opt.param_groups[0]["lr"] is rate and rate.shape == shape and rate.tolist() in (0.25, [0.25])
+    assert opt.param_groups[1]["lr"] == 2.0
+    rate.fill_(0.125)
+    assert float(torch.as_tensor(saved)) == float(torch.as_tensor(state["param_groups"][0]["lr"])) == 0.25
+
+
+def test_load_takes_a_rate_in_a_tensor_for_a_number(monkeypatch):
+    monkeypatch.setattr(torch_optim, "_moments", lambda group, first: {"layout": []})
+    rate, opt = torch.tensor([0.25]), _rated(0.5)
+    opt.load_state_dict(_rated(rate).state_dict())
+    got = opt.param_groups[0]["lr"]
+    assert torch.is_tensor(got) and got is not rate and torch.equal(got, rate)
+
+
+def test_load_into_a_shared_rate(monkeypatch):
+    monkeypatch.setattr(torch_optim, "_moments", lambda group, first: {"layout": []})
+    rate = torch.tensor([0.5])
+    opt = _rated(rate, rate)
+    opt.load_state_dict(_rated(0.25, 0.25).state_dict())
+    assert all(g["lr"] is rate for g in opt.param_groups) and float(rate) == 0.25
+    with pytest.raises(ValueError, match="share"):
+        opt.load_state_dict(_rated(0.125, 0.0625).state_dict())
+    assert all(g["lr"] is rate for g in opt.param_groups) and float(rate) == 0.25
