@@ -260,8 +260,10 @@ class AdamW(torch.optim.Optimizer):
     every replay.  A parameter without a gradient is left alone, its moments and its
     count of steps too.  Counts are kept on the GPU, one for all parameters that
     have had gradients at the same steps; these go in one call for each group.  A
-    captured step goes on with the parameters and counts it was captured with.  A
-    step that is refused changes nothing in any group and is not counted.
+    captured step goes on with the parameters and counts it was captured with; the
+    parameters that share a count there have gradients together from then on, in
+    other steps too, or none (RuntimeError).  A step that is refused changes nothing in
+    any group and is not counted.
     Gradients are float32 or bfloat16 as they are; others, and ones that lie unlike
     their parameter, are copied first.
     """
@@ -275,6 +277,8 @@ class AdamW(torch.optim.Optimizer):
         # which one a parameter goes by.  A history is at least one parameter's, so that there is room
         # for all of them from the start: a captured step holds their addresses.
         self._counts, self._histories, self._begun = [], 0, False
+        # The histories that a captured step goes by.
+        self._captured = set()
         super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits,
                                       master_weights=master_weights))
 
@@ -348,6 +352,8 @@ class AdamW(torch.optim.Optimizer):
                 count.add_(taken)
         for call in calls:
             call()
+        if torch.cuda.is_current_stream_capturing():
+            self._captured.update(slots)
         return loss
 
     def _part(self, grads):
@@ -358,6 +364,10 @@ class AdamW(torch.optim.Optimizer):
             has.update(s for s, g in zip(group["_slots"], gs) if g is not None)
         parting = [(group["_slots"], i) for group, gs in zip(self.param_groups, grads)
                    for i, (s, g) in enumerate(zip(group["_slots"], gs)) if g is None and s in has]
+        if any(slots[i] in self._captured for slots, i in parting):
+            # its replays take them all, by one count
+            raise RuntimeError("only some of the parameters that a captured step takes together have gradients: without that "
+                               "step go on with a new AdamW, loaded with this one's state_dict()")
         if parting and self._begun and torch.cuda.is_current_stream_capturing():
             # every replay would copy the count anew
             raise RuntimeError("other parameters have gradients than in the steps before: take a step with these before capturing one")
@@ -378,7 +388,7 @@ class AdamW(torch.optim.Optimizer):
     def __setstate__(self, state):
         if "_counts" in state:   # (not where torch loads a state dictionary)
             counts = state["_counts"]
-            state = {**state, "_counts": [] if counts is None else list(counts.split(1))}
+            state = {**state, "_counts": [] if counts is None else list(counts.split(1)), "_captured": set()}
         super().__setstate__(state)
         for g in self.param_groups:
             # unpickled onto another device, moments and all
@@ -413,6 +423,9 @@ class AdamW(torch.optim.Optimizer):
             if "master" in b and any(y == "bfloat16" != x for x, y in zip(a.get("types", b["types"]), b["types"])):
                 raise ValueError("a bfloat16 parameter was float32 when its state was saved, without a 32-bit copy: load into "
                                  "parameters of the types that were saved")
+        if self._captured and [list(x) for x in saved["slots"]] != [g["_slots"] for g in self.param_groups]:
+            raise RuntimeError("the saved parameters had gradients together that a captured step does not take together: load "
+                               "into a new AdamW")
         rates, shared = [g["lr"] for g in self.param_groups], {}
         for lr, g in zip(rates, state_dict["param_groups"]):
             if torch.is_tensor(lr) and shared.setdefault(id(lr), float(g["lr"])) != float(g["lr"]):

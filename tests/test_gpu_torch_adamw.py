@@ -457,3 +457,27 @@ def test_a_captured_step_goes_on_after_a_load(tmp_path):
         p.grad = x.grad.clone()
     other.step(), captured.step()
     assert all(torch.equal(p, q) for p, q in zip(ps, other.param_groups[0]["params"]))
+
+
+def test_a_captured_steps_parameters_have_gradients_together():
+    ps, qs = _params(21), _params(21)
+    a, b = AdamW(ps, lr=1e-2), AdamW(qs, lr=1e-2)
+    for p, q, g in zip(ps, qs, _grads(21)):
+        p.grad, q.grad = g, g.clone()
+    a.step(), b.step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        a.step()
+    held, ps[2].grad = ps[2].grad, None
+    with pytest.raises(RuntimeError, match="captured"):
+        a.step()
+    ps[2].grad = held
+    for t in range(3):
+        graph.replay()
+        b.step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(ps, qs)), t
+        a.step(), b.step()
+        assert all(torch.equal(p, q) for p, q in zip(ps, qs)), t
+    assert a.state_dict()["adamw"]["counts"] == b.state_dict()["adamw"]["counts"] == [7]

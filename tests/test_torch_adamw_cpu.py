@@ -475,3 +475,59 @@ def test_load_into_a_shared_rate(monkeypatch):
     with pytest.raises(ValueError, match="share"):
         opt.load_state_dict(_rated(0.125, 0.0625).state_dict())
     assert all(g["lr"] is rate for g in opt.param_groups) and float(rate) == 0.25
+
+
+def _captured(monkeypatch, **kw):
+    """An optimizer of a, b (one group) and c, whose second step, of all but c, has been captured."""
+    calls = _without_a_gpu(monkeypatch)
+    ps = [_p(4), _p(4), _p(4)]
+    opt = AdamW([{"params": ps[:2]}, {"params": ps[2:]}], **kw)
+    _gradients(ps, 0, 1, 2)
+    opt.step()
+    _gradients(ps, 0, 1)
+    opt.step()
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    opt.step()
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    return opt, ps, calls
+
+
+def _gradients(ps, *which):
+    for i, p in enumerate(ps):
+        p.grad = torch.ones_like(p) if i in which else None
+
+
+@pytest.mark.parametrize("max_norm", [None, 1.0])
+def test_parameters_that_a_captured_step_takes_together_stay_together(monkeypatch, max_norm):
+    """A replay goes by one count for them, and would take one that another step had left out by a wrong one."""
+    opt, ps, calls = _captured(monkeypatch, max_norm=max_norm)
+    for which in ((0,), (1, 2)):
+        _gradients(ps, *which)
+        calls.clear()
+        before = opt.state_dict()["adamw"]
+        with pytest.raises(RuntimeError, match="captured"):
+            opt.step()
+        assert calls == [] and {k: opt.state_dict()["adamw"][k] for k in ("counts", "slots")} == {k: before[k] for k in ("counts", "slots")}
+    for which in ((0, 1), (2,), (0, 1, 2)):       # all of them, or none
+        _gradients(ps, *which)
+        opt.step()
+    assert opt.state_dict()["adamw"]["slots"] == [[0, 0], [1]]
+    new = AdamW([{"params": ps[:2]}, {"params": ps[2:]}])
+    new.load_state_dict(opt.state_dict())
+    _gradients(ps, 0)
+    new.step()
+    assert new.state_dict()["adamw"]["slots"] == [[0, 2], [1]]
+    copied = copy.deepcopy(opt)
+    _gradients([p for g in copied.param_groups for p in g["params"]], 0)
+    copied.step()
+
+
+def test_load_beside_a_captured_step(monkeypatch):
+    opt, ps, _ = _captured(monkeypatch)
+    opt.load_state_dict(opt.state_dict())
+    other = AdamW([{"params": [_p(4), _p(4)]}, {"params": [_p(4)]}])
+    with pytest.raises(RuntimeError, match="captured"):
+        opt.load_state_dict(other.state_dict())
+    assert opt.state_dict()["adamw"]["slots"] == [[0, 0], [1]]
+    _gradients(ps, 0, 1)
+    opt.step()
