@@ -46,8 +46,11 @@ int type_of(const at::Tensor &t, const char *otherwise) {
   throw Refused{otherwise};
 }
 
-// Whether its elements fill a stretch of memory, in whatever order, and mean what they are.
-bool dense(const at::Tensor &t) { return t.layout() == at::kStrided && !t.is_neg() && (t.is_contiguous() || t.is_non_overlapping_and_dense()); }
+// Whether its elements fill a stretch of memory, in whatever order, with the values that they have:
+// a negated view's memory holds others, a tensor of zeros may have none.
+bool dense(const at::Tensor &t) {
+  return t.layout() == at::kStrided && !t.is_neg() && !t._is_zerotensor() && (t.is_contiguous() || t.is_non_overlapping_and_dense());
+}
 
 // Whether gradient and parameter, both dense, have the same elements in the same places.
 bool like(const at::Tensor &g, const at::Tensor &p) {

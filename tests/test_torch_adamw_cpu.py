@@ -531,3 +531,10 @@ def test_load_beside_a_captured_step(monkeypatch):
     assert opt.state_dict()["adamw"]["slots"] == [[0, 0], [1]]
     _gradients(ps, 0, 1)
     opt.step()
+
+
+def test_gradients_without_memory_are_copied():
+    """Zeros that autograd never wrote down."""
+    p, g = _p(4, 6), torch._efficientzerotensor((4, 6))
+    got = torch_optim._like(g, p)
+    assert got is not g and got.data_ptr() and not bool(got.any())
