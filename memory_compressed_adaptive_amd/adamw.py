@@ -67,6 +67,12 @@ def _native():
     return _tensors
 
 
+@functools.lru_cache(maxsize=None)
+def _device(index: int):
+    import torch
+    return torch.device("cuda", index)
+
+
 def require_dense(params) -> None:
     """ValueError unless every parameter is one that the steps take."""
     params = _sequence(params)
@@ -99,15 +105,17 @@ def _sequence(x):
 
 
 def _state(t, what: str, dtype, size: int, device):
-    if not (t.dtype == dtype and t.is_contiguous() and t.numel() == size and t.device == device and not t.is_neg()):
+    at = _native().data(t, dtype, size, device)
+    if at is None:
         raise ValueError(f"{what} must be contiguous {dtype} of {size} elements on the device of the tensors")
-    return t.data_ptr()
+    return at
 
 
 def _one(t, what: str, dtype, device):
-    if not (t.dtype == dtype and t.numel() == 1 and t.device == device and not t.is_neg()):
+    at = _native().data(t, dtype, 1, device)
+    if at is None:
         raise ValueError(f"{what} must be one {dtype} on the device of the tensors")
-    return t.data_ptr()
+    return at
 
 
 def _arguments(t, lr, beta1, beta2, eps, wd, scale, device):
@@ -143,11 +151,16 @@ def grad_norm(grads, max_norm: float = math.inf, t=None, out=None, stream=None):
     factor is NaN, and a step with it changes nothing.  t: an int64 tensor, a
     count of steps that is raised by one if the norm is finite.  out: fp32 of two
     elements for both."""
+    return norm_into(out, grads, max_norm, t, stream).unbind()
+
+
+def norm_into(out, grads, max_norm, t=None, stream=None):
+    """grad_norm's call; `out`, or what is allocated for None."""
     import torch
     grads = _sequence(grads)
     rows, count, index = _native().grads(grads)
     _L.require(count > 0 or out is not None, "there must be a gradient, or out")
-    device = torch.device("cuda", index) if count else out.device
+    device = _device(index) if count else out.device
     _L.require(device.type == "cuda", "out must be a CUDA tensor")
     L = _L.lib()
     nbytes = L.ma_grad_norm_workspace(count)
@@ -160,7 +173,7 @@ def grad_norm(grads, max_norm: float = math.inf, t=None, out=None, stream=None):
         _L.check(L.ma_grad_norm(count, rows, max_norm, to, None if t is None else _one(t, "t", torch.int64, device),
                                 ws.data_ptr(), nbytes, s))
     _native().changed((out, t), (), ())
-    return out.unbind()
+    return out
 
 
 def adamw_step(params, grads, m, v, t, lr=1e-3, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8, wd: float = 0.0,
@@ -196,7 +209,7 @@ def step_call(params, grads, state, t, lr, beta1, beta2, eps, wd, scale=None, ma
     rows, count, index, size = _native().rows(params, grads)
     if not count:
         return None
-    device = torch.device("cuda", index)
+    device = _device(index)
     if len(state) == 2:
         fn = _L.lib().ma_adamw_many_step
         at = _state(state[0], "m", torch.float32, size, device), _state(state[1], "v", torch.float32, size, device)

@@ -8,6 +8,8 @@
 #include <ATen/core/Tensor.h>
 #include <c10/hip/HIPFunctions.h>
 #include <c10/hip/HIPStream.h>
+#include <torch/csrc/Device.h>
+#include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <algorithm>
@@ -165,6 +167,7 @@ PyObject *overlap(PyObject *, PyObject *args) {
   if (!gs.o) return nullptr;
   return guarded([&]() -> PyObject * {
     std::vector<std::pair<const char *, const char *>> spans;
+    spans.reserve((size_t)PySequence_Fast_GET_SIZE(ps.o));
     bool sorted = true;
     for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(ps.o) && i < PySequence_Fast_GET_SIZE(gs.o); ++i) {
       if (items(gs)[i] == Py_None) continue;
@@ -187,6 +190,7 @@ PyObject *layout(PyObject *, PyObject *arg) {
   if (!ps.o) return nullptr;
   return guarded([&]() -> PyObject * {
     std::vector<int64_t> out;
+    out.reserve(7 * (size_t)PySequence_Fast_GET_SIZE(ps.o));   // of matrices
     for (Py_ssize_t i = 0; i < PySequence_Fast_GET_SIZE(ps.o); ++i) {
       const at::Tensor &p = tensor(items(ps)[i], "a tensor");
       out.push_back((int64_t)p.scalar_type());
@@ -222,6 +226,25 @@ PyObject *changed(PyObject *, PyObject *args) {
   });
 }
 
+// data(tensor, dtype, elements, device) -> where its elements lie one after the other; None if they do
+// not, or are others
+PyObject *data(PyObject *, PyObject *const *args, Py_ssize_t n) {
+  if (n != 4 || !THPDtype_Check(args[1]) || !THPDevice_Check(args[3])) {
+    PyErr_SetString(PyExc_TypeError, "data(tensor, dtype, elements, device)");
+    return nullptr;
+  }
+  const long long size = PyLong_AsLongLong(args[2]);
+  if (size == -1 && PyErr_Occurred()) return nullptr;
+  return guarded([&]() -> PyObject * {
+    if (!THPVariable_Check(args[0])) Py_RETURN_NONE;
+    const at::Tensor &t = THPVariable_Unpack(args[0]);
+    if (t.scalar_type() != reinterpret_cast<THPDtype *>(args[1])->scalar_type || t.device() != reinterpret_cast<THPDevice *>(args[3])->device ||
+        t.numel() != size || !dense(t) || !t.is_contiguous())
+      Py_RETURN_NONE;
+    return PyLong_FromVoidPtr(t.mutable_data_ptr());
+  });
+}
+
 // stream(device) -> the current stream's handle; None if another device is the current one
 PyObject *stream(PyObject *, PyObject *arg) {
   const long device = PyLong_AsLong(arg);
@@ -238,6 +261,7 @@ PyMethodDef methods[] = {{"rows", rows, METH_VARARGS, nullptr},
                          {"overlap", overlap, METH_VARARGS, nullptr},
                          {"layout", layout, METH_O, nullptr},
                          {"changed", changed, METH_VARARGS, nullptr},
+                         {"data", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(data)), METH_FASTCALL, nullptr},
                          {"stream", stream, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_tensors", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

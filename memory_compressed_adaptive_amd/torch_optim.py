@@ -335,16 +335,16 @@ class AdamW(torch.optim.Optimizer):
         calls = []
         for group, gs in zip(self.param_groups, grads):
             st, (b1, b2) = group["_moments"], group["betas"]
-            state = [st[k] for k in (("cm", "cv", "sm", "sr") if "cm" in st else ("m", "v")) if k in st]
             for slot, count in zip(slots, counts):
                 some = gs if len(slots) == 1 else [g if s == slot else None for s, g in zip(group["_slots"], gs)]
                 if all(g is None for g in some):
                     continue
+                state = (st["cm"], st["cv"], st["sm"], st["sr"]) if "cm" in st else (st["m"], st["v"])
                 calls.append(_adamw.step_call(group["params"], some, state, count, group["lr"], b1, b2, group["eps"], group["weight_decay"],
-                                              scale=scale, master=st.get("master"), apart=True))
+                                              scale, st.get("master"), apart=True))
         if norm is not None:
             # the norm's call counts the step where there is one count to raise
-            _adamw.grad_norm([g for gs in grads for g in gs], self.max_norm, t=counts[0] if len(slots) == 1 else None, out=out)
+            _adamw.norm_into(out, [g for gs in grads for g in gs], self.max_norm, counts[0] if len(slots) == 1 else None)
             self.grad_norm = norm
         if norm is None or len(slots) > 1:
             taken = 1 if scale is None else (scale == scale).reshape(1)
