@@ -699,3 +699,15 @@ def test_norm_of_gradients_that_an_iterator_makes(n):
         # one rounding each, beside those in 64 bits
         assert float(norm) == pytest.approx(want, rel=1.01 * 2.0 ** -24)
         assert float(scale) == pytest.approx(1 / (want + 1e-6), rel=1.01 * 2.0 ** -24)
+
+
+def test_codes_next_to_a_border():
+    """Enough elements that some lie nearer to a border between two codes than the kernel's 32-bit
+    estimates can tell (6e-7 of the code, so twice that of the value), and are decided in 64 bits; none
+    so near that 64 bits cannot tell."""
+    c = Case(50, shapes=[(1 << 18,)], bits=8)
+    for t in range(1, 4):
+        g, before = c.grads(), c.snapshot()
+        c.run(g, t, lr=1e-3)
+        c.check(before, g, t, 1e-3, 0.0)
+    assert 1e-13 < c.near < 6e-7
