@@ -7,12 +7,13 @@
 // they are aligned whatever the parameters are; parameters and gradients may
 // begin at any element.
 //
-// All of it is bound by memory (14 to 28 bytes an element and some 30 to 60
-// operations), short lists by the launch.  The steps give each workgroup one chunk:
-// in a loop, a wave's next loads would wait for its last stores, which retire in
-// order with them (51.8 million fp32 parameters: 279 us with 2048 workgroups in a
-// loop, 251 with one chunk each, 5.4 TB/s; 405 million bf16 ones with copies 2290
-// and 2130, 5.3 TB/s; a copy of 1 GiB runs at 5.1).  Loads that bypass the caches
+// All of it is bound by memory, short lists by the launch: the norm reads 2 or 4 bytes an
+// element, the step moves 22 to 30 with some 45 vector instructions, the 8-bit step 10
+// to 18 with some 55.  The steps give each workgroup one chunk: in a loop, a wave's
+// next loads would wait for its last stores, which retire in order with them (51.8
+// million fp32 parameters: 279 us with 2048 workgroups in a loop, 251 with one chunk
+// each, 5.4 TB/s; 405 million bf16 ones with copies 2290 and 2140, 5.3 TB/s; a copy of
+// 1 GiB runs at 5.1).  Loads that bypass the caches
 // made the steps 4% slower, such stores 0.5% faster but reading 8-bit moments twice
 // as slow: neither is used.
 #pragma once
@@ -278,8 +279,8 @@ template <class T> __device__ __forceinline__ T block_max(T x) {
   return rows_max(x);
 }
 
-// sqrt(x) of a positive x far from the ends of the range of 64 bits, to its last bits
-// (the library's root guards those ends).
+// sqrt(x) of a positive x far from the ends of the range of 64 bits, to its last bits, by
+// Goldschmidt's iteration (the library's root guards those ends).
 __device__ __forceinline__ double root(double x) {
   const double r = __builtin_amdgcn_rsq(x);
   double s = x * r, h = 0.5 * r;
@@ -323,13 +324,14 @@ __device__ __forceinline__ uint32_t kept(uint32_t w, int left) {
 }
 
 // Written down plainly, this is bound by instructions: 960 us for 262 million bf16 parameters,
-// whose bytes take 510 at a copy's rate.  64-bit operations cost what 32-bit ones do (4 cycles a
+// whose bytes take 517 at a copy's rate.  64-bit operations cost what 32-bit ones do (4 cycles a
 // wave; additions and products in 32 bits less), so moments are formed in 64 bits; what follows
 // goes by 32-bit estimates of the codes' roots, good to a few parts in 10^7, and a lane with
 // an element nearer to a border than that (one in 600) decides its codes again in 64 bits.
 // 1/x and roots are the hardware's estimates: the update is off by a few parts in 10^7 of
 // itself.  443 instructions a wave and 8 elements, 89 registers, five waves a SIMD (with four
-// the same time, with six, and registers in memory, 545 us): 502 to 520 us, 5.1 to 5.3 TB/s.
+// the same time, with six, and registers in memory, 545 us): 508 us in the fastest of a trace's
+// calls, 530 in the median one, 5.0 TB/s.
 template <class P, class G, bool COPY>
 __global__ __launch_bounds__(kThreads, 5) void step8_kernel(Table T, StepArgs A, float *copies, int8_t *cm, uint8_t *cv, float *sm,
                                                             float *sr) {
@@ -505,7 +507,7 @@ template <int THREADS> __device__ __forceinline__ double group_sum(double x) {
 // A workgroup takes chunks of kNormChunk elements in turn, kNormRuns runs of a thread at once: it
 // only reads, so what counts is how many loads are on their way.  809 million bf16 gradients:
 // 346 us with one load of a thread at a time (1024 groups); with four, 253 (6.4 TB/s) with 512
-// groups, 278 with 384, 263 with 1024, 276 with 8192; with eight 260 with 512, with two 351.
+// groups (247 in a trace), 278 with 384, 263 with 1024, 276 with 8192; with eight 260 with 512, with two 351.
 // Eight gradients as they are loaded: nothing waits for them before the first is widened.
 template <class G> struct Raw;
 template <> struct Raw<float> {
@@ -586,6 +588,8 @@ __global__ __launch_bounds__(kThreads) void norm_finish_kernel(const double *par
 // launches, one tensor takes 2.5 us on the GPU instead of 3.9 and 8.2 us of the host's time instead of
 // 10.5; 32 chunks 4.0 instead of 4.7 and 8.8 instead of 11.1; 64 chunks 5.8 instead of 4.6 and
 // 9.1 instead of 11.2; 120 chunks 8.9 instead of 4.7 (a CU reads 64 bytes a cycle): up to 64 then.
+// That is for eager calls, which the host holds up: a captured one, without its time, is
+// even at 45 chunks and 1.2 us slower than two launches would be at 64.
 __global__ __launch_bounds__(kSmallThreads) void norm_small_kernel(NormTable T, double max_norm, float *out, int64_t *t) {
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const double s = group_sum<kSmallThreads>(squares<kSmallSpan>(T, wave, kSmallThreads / 64, threadIdx.x % 64 * kRun));
