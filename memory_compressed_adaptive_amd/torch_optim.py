@@ -385,6 +385,9 @@ class AdamW(torch.optim.Optimizer):
         return {**super().__getstate__(), "max_norm": self.max_norm, "grad_norm": self.grad_norm, "_histories": self._histories,
                 "_begun": self._begun, "_counts": torch.cat(self._counts) if self._counts else None}
 
+    def __copy__(self):
+        raise TypeError("a shallow copy of AdamW would step the same moments by counts of its own: use copy.deepcopy")
+
     def __setstate__(self, state):
         if "_counts" in state:   # (not where torch loads a state dictionary)
             counts = state["_counts"]

@@ -538,3 +538,10 @@ def test_gradients_without_memory_are_copied():
     p, g = _p(4, 6), torch._efficientzerotensor((4, 6))
     got = torch_optim._like(g, p)
     assert got is not g and got.data_ptr() and not bool(got.any())
+
+
+def test_a_shallow_copy_is_refused(monkeypatch):
+    """It would step the same moments by counts of its own."""
+    monkeypatch.setattr(torch_optim, "_moments", lambda group, first: {"layout": []})
+    with pytest.raises(TypeError, match="deepcopy"):
+        copy.copy(AdamW([_p(3)]))
