@@ -253,7 +253,8 @@ class AdamW(torch.optim.Optimizer):
     parameters, which take the steps in their place; they are made here, of the
     weights that the parameters have now.  max_norm: clips the gradients of all groups
     together to this norm; `grad_norm` is then the last step's, as a tensor on the
-    GPU, and a step whose norm is not finite changes nothing and is not counted.
+    GPU (a captured step's is the one that its capture left there), and a step whose
+    norm is not finite changes nothing and is not counted.
 
     lr, betas, eps and weight_decay may be changed between steps; lr may be a
     float32 tensor of one element on the GPU, which a captured step reads at
@@ -262,7 +263,8 @@ class AdamW(torch.optim.Optimizer):
     have had gradients at the same steps; these go in one call for each group.  A
     captured step goes on with the parameters and counts it was captured with; the
     parameters that share a count there have gradients together from then on, in
-    other steps too, or none (RuntimeError).  A step that is refused changes nothing in
+    other steps too, or none (RuntimeError); where several sets of them do, a step is
+    taken with each before the first capture.  A step that is refused changes nothing in
     any group and is not counted.
     Gradients are float32 or bfloat16 as they are; others, and ones that lie unlike
     their parameter, are copied first.
@@ -366,8 +368,9 @@ class AdamW(torch.optim.Optimizer):
                    for i, (s, g) in enumerate(zip(group["_slots"], gs)) if g is None and s in has]
         if any(slots[i] in self._captured for slots, i in parting):
             # its replays take them all, by one count
-            raise RuntimeError("only some of the parameters that a captured step takes together have gradients: without that "
-                               "step go on with a new AdamW, loaded with this one's state_dict()")
+            raise RuntimeError("only some of the parameters that a captured step takes together have gradients: take a step with "
+                               "each such set before the first capture or, without that captured step, go on with a new AdamW "
+                               "that is loaded with this one's state_dict()")
         if parting and self._begun and torch.cuda.is_current_stream_capturing():
             # every replay would copy the count anew
             raise RuntimeError("other parameters have gradients than in the steps before: take a step with these before capturing one")

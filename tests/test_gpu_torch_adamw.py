@@ -481,3 +481,34 @@ def test_a_captured_steps_parameters_have_gradients_together():
         a.step(), b.step()
         assert all(torch.equal(p, q) for p, q in zip(ps, qs)), t
     assert a.state_dict()["adamw"]["counts"] == b.state_dict()["adamw"]["counts"] == [7]
+
+
+def test_two_captured_steps_of_different_parameters():
+    """Taken with each set before the first capture, the steps replay in any order beside eager ones."""
+    ps, qs = _params(22), _params(22)
+    a, b = AdamW(ps, lr=1e-2, max_norm=1e-2), AdamW(qs, lr=1e-2, max_norm=1e-2)
+    held = [(torch.empty_like(p), torch.empty_like(p)) for p in ps]
+    sets = {"all": range(5), "some": (0, 3), "one": (3,)}
+
+    def grads(t, name):
+        for i, (p, q, g) in enumerate(zip(ps, qs, _grads(140 + t))):
+            held[i][0].copy_(g), held[i][1].copy_(g)
+            p.grad, q.grad = held[i] if i in sets[name] else (None, None)
+
+    for t, name in enumerate(sets):
+        grads(t, name), a.step(), b.step()
+    torch.cuda.synchronize()
+    graphs = {}
+    for name in ("all", "some"):
+        grads(3, name)
+        graphs[name] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graphs[name]):
+            a.step()
+    for t, name in enumerate(("some", "all", "one", "some", "some", "one", "all"), 4):
+        grads(t, name)
+        graphs[name].replay() if name in graphs else a.step()
+        b.step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(ps, qs)), (t, name)
+    counts = lambda o: [o.state_dict()["adamw"]["counts"][s] for s in o.param_groups[0]["_slots"]]  # noqa: E731
+    assert counts(a) == counts(b) == [7, 3, 3, 10, 3]
